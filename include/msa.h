@@ -59,7 +59,8 @@ enum {
     MSA_DEV_OK = 0,
     MSA_DEV_ROPE_POSITION = 1, /* a RoPE position was >= max_pos; that row was not rotated/pooled */
     MSA_DEV_WAIT_TIMEOUT = 2,  /* an mbarrier wait in the tensor-core router ran out of time */
-    MSA_DEV_BAD_INDEX = 3      /* a doc index outside [0, n_docs) reached a kernel */
+    MSA_DEV_BAD_INDEX = 3,     /* a doc or page index, an offset or a length out of range reached a kernel */
+    MSA_DEV_NONFINITE = 4      /* a NaN or infinite value was appended to an 8-bit cache */
 };
 
 /* Thread-local text of the last error on this host thread ("" if none). */
@@ -318,6 +319,92 @@ msa_status msa_sparse_attn_split_plan(int n_q, int T, int hq, int hkv, int max_m
                                       int* key_ranges, int* cluster);
 
 /* ---------------------------------------------------------------------------------------------
+ * Paged 8-bit key/value cache of the active context. msa_sparse_attn's local keys are one dense bf16
+ * buffer with one length for all queries; contexts that grow long and apart (the Memory Interleave
+ * loop of [P1] §组件 3 appends to them round by round) are kept here instead, in pages of 16, 32, 64 or
+ * 128 tokens that the caller hands out, at a quarter to an eighth of the bytes. The pages define no
+ * such cache; it is a library addition.
+ *   pages:  e4m3 values, device [n_pages][2][hkv][page][d], K at [p][0] and V at [p][1];
+ *   scales: device float [n_pages][2][hkv], powers of two from 2^-50 to 2^50: a stored value stands for
+ *           e4m3 * scale, which is a bf16 number;
+ *   bounds: device bf16 [n_pages][hkv][2][d], the elementwise minimum ([0]) and maximum ([1]) of the
+ *           keys that the page holds, for msa_page_select; NULL where that is not used;
+ *   page_table: device int32 [n_seq][max_pages]: the page of tokens page * i .. page * i + page - 1 of a
+ *           sequence; entries behind its last page are not read;
+ *   seq_len: device int32 [n_seq]: tokens of each sequence, the call's new tokens included.
+ * d must be 128. The struct is host memory, read during the call; what it points to is the caller's and
+ * stays in place, so a captured call can be replayed after page_table and seq_len were refilled.
+ *
+ * New tokens are packed: the rows tok_off[s] .. tok_off[s+1]-1 (device int64 [n_seq+1], non-decreasing) of
+ * k, v, q and out are the last n = tok_off[s+1] - tok_off[s] tokens of sequence s, n from 0 to max_new.
+ * Rows before tok_off[0] or from tok_off[n_seq] on are neither read nor written. A sequence whose offsets
+ * or length contradict n_tok, max_new, max_pages or one another records MSA_DEV_BAD_INDEX and is skipped
+ * whole; a page index outside [0, n_pages) records it too, and that page's tokens are skipped: not stored,
+ * and not seen by any query. Pages may be shared by sequences that only read them; a page that a call
+ * appends to belongs to one sequence.
+ * --------------------------------------------------------------------------------------------- */
+typedef struct msa_paged_kv {
+    void* pages;
+    float* scales;
+    void* bounds;
+    const int32_t* page_table;
+    const int32_t* seq_len;
+    int64_t n_pages;
+    int n_seq, max_pages, page, hkv, d;
+} msa_paged_kv;
+
+/* Appends new tokens: k is rotated to position pos_offset + its place in the sequence (the global RoPE of
+ * msa_rope_doc), v is stored as it is, both rounded once to e4m3 at the page's scale. With q, the queries
+ * of the same tokens are rotated to the same positions into q_rot.
+ *   k, v: device [n_tok][hkv][d]; q, q_rot: device [n_tok][hq][d] or NULL, q_rot may equal q; all of dt;
+ *   cos_sin: device table of msa_rope_table(max_pos, d, base).
+ * Scale of a (page, K or V, kv head): the smallest power of two s with max|x| <= 448 s over the new rows of
+ * the page (at least 2^-50, at most 2^50), or the one it has where that is larger and the page holds older
+ * rows; older rows of a scale that grows are rounded to it (exact unless they fall below the smallest normal
+ * e4m3 value). A page whose first row is written starts anew: its old scale, bounds and rows count for
+ * nothing. bounds (where not NULL) are kept equal to those of the stored keys; rows given up by shortening
+ * seq_len stay in scale and bounds until their page starts anew.
+ * A position >= max_pos leaves that row unrotated and records MSA_DEV_ROPE_POSITION. A value that is not
+ * finite records MSA_DEV_NONFINITE; it does not set a scale, and is stored as 0 (NaN) or as the largest
+ * value of its sign (infinity, and any value above 448 * 2^50), so that pages hold finite values only.
+ * One launch, no workspace. */
+msa_status msa_paged_append(const msa_paged_kv* kv, const void* k, const void* v, const void* q, msa_dtype dt,
+                            int64_t n_tok, int hq, const int64_t* tok_off, int max_new, int64_t pos_offset,
+                            const float* cos_sin, int64_t max_pos, void* q_rot, void* stream);
+
+/* Attention of the new tokens over the cache: token i of a sequence of len tokens, n of them new, sees the
+ * cached tokens 0 .. len - n + i (itself included):
+ *   out = softmax(scale * q . K) V,   kv head of query head h: h / (hq / hkv)
+ *   q, out: device [n_tok][hq][d], bf16, q already rotated; lse: optional device float [n_tok][hq], the
+ *   natural-log sum of exp(scale * q . k) over the keys that the row sees, to join the result with another
+ *   part's (attention over fetched memory, say).
+ * With sel (device int32 [n_tok][hkv][k], msa_page_select's list or the caller's own) a token's query heads
+ * see only the listed pages of their kv head, as indices into the sequence's row of page_table; -1 entries
+ * are empty, an entry outside the pages that the token sees records MSA_DEV_BAD_INDEX and counts as empty,
+ * a page listed twice counts twice. A row that sees no key is 0 with lse -inf. Rows of a page behind the
+ * sequence's end are never used, whatever they hold.
+ * bf16 only, d == 128, hq/hkv in {1, 2, 4, 8}. ws: msa_paged_attn_workspace_size bytes. */
+msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_dtype dt, int64_t n_tok, int hq,
+                          const int64_t* tok_off, int max_new, const int32_t* sel, int k, float scale, void* out,
+                          float* lse, void* ws, size_t ws_bytes, void* stream);
+/* k: entries of a page list, 0 without one. */
+msa_status msa_paged_attn_workspace_size(int64_t n_tok, int n_seq, int max_new, int hq, int hkv, int max_pages,
+                                         int page, int k, size_t* bytes);
+
+/* Pages for a sparse pass of msa_paged_attn: for every new token and kv head the k pages, of those that the
+ * token sees, with the largest score
+ *   max over the group's query heads of sum_d max(q_d * bounds_min_d, q_d * bounds_max_d),
+ * the largest q . k that keys inside the page's bounds could give (summed in 64 bits); the `recent` newest
+ * pages always count as the best, equal scores go to the lower page. sel: device int32 [n_tok][hkv][k], page
+ * indices into the sequence's row of page_table, ascending, -1 behind the last where the token sees fewer
+ * than k pages. Rows outside the sequences are left as they were. bf16 queries (rotated), 1 <= recent <= k,
+ * hq/hkv in {1, 2, 4, 8}. ws: msa_page_select_workspace_size bytes. */
+msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa_dtype dt, int64_t n_tok, int hq,
+                           const int64_t* tok_off, int max_new, int k, int recent, int32_t* sel, void* ws,
+                           size_t ws_bytes, void* stream);
+msa_status msa_page_select_workspace_size(int64_t n_tok, int hkv, int max_pages, size_t* bytes);
+
+/* ---------------------------------------------------------------------------------------------
  * Backward pass (end-to-end training: [P1] 核心创新 端到端可训练性 — routing, compression and
  * attention are optimised in one gradient flow; [P1] §训练策略 and [P2] §训练层面 — a weighted
  * auxiliary loss supervises every layer's router). The top-k selection carries no gradient. All
@@ -491,12 +578,16 @@ enum {
     MSA_OP_SPARSE_ATTN_SPLIT = 3,   /* msa_sparse_attn_split     cfg: const msa_attn_ws_cfg*      */
     MSA_OP_SPARSE_ATTN_BACKWARD = 4,/* msa_sparse_attn_backward  cfg: const msa_attn_ws_cfg*      */
     MSA_OP_ROUTE_BACKWARD = 5,      /* msa_route_backward        cfg: const msa_route_bwd_ws_cfg* */
-    MSA_OP_INTERLEAVE = 6           /* msa_interleave_step       cfg: const msa_interleave_args*  */
+    MSA_OP_INTERLEAVE = 6,          /* msa_interleave_step       cfg: const msa_interleave_args*  */
+    MSA_OP_PAGED_ATTN = 7,          /* msa_paged_attn            cfg: const msa_paged_attn_ws_cfg* */
+    MSA_OP_PAGE_SELECT = 8          /* msa_page_select           cfg: const msa_page_select_ws_cfg* */
 };
 typedef struct { int n_q, T, H, d; msa_dtype dt; } msa_route_ws_cfg;
 typedef struct { int n_q; int64_t n_docs; int k; } msa_topk_ws_cfg;
 typedef struct { int n_q, T, hq, hkv, max_mem, L; } msa_attn_ws_cfg;
 typedef struct { int64_t n_chunks; int n_q, T, H, d; } msa_route_bwd_ws_cfg;
+typedef struct { int64_t n_tok; int n_seq, max_new, hq, hkv, max_pages, page, k; } msa_paged_attn_ws_cfg;
+typedef struct { int64_t n_tok; int hkv, max_pages; } msa_page_select_ws_cfg;
 msa_status msa_workspace_size(int op, const void* cfg, size_t* bytes);
 
 #ifdef __cplusplus

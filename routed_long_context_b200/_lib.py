@@ -33,8 +33,14 @@ class InterleaveArgs(ctypes.Structure):
                 ("ws", vp), ("ws_bytes", sz)]
 
 
+class PagedKVArgs(ctypes.Structure):
+    _fields_ = [("pages", vp), ("scales", vp), ("bounds", vp), ("page_table", vp), ("seq_len", vp), ("n_pages", i64),
+                ("n_seq", ctypes.c_int), ("max_pages", ctypes.c_int), ("page", ctypes.c_int), ("hkv", ctypes.c_int),
+                ("d", ctypes.c_int)]
+
+
 MSA_OP_ROUTE, MSA_OP_TOPK, MSA_OP_SPARSE_ATTN_SPLIT, MSA_OP_SPARSE_ATTN_BACKWARD, MSA_OP_ROUTE_BACKWARD, \
-    MSA_OP_INTERLEAVE = range(1, 7)
+    MSA_OP_INTERLEAVE, MSA_OP_PAGED_ATTN, MSA_OP_PAGE_SELECT = range(1, 9)
 
 
 class RouteWsCfg(ctypes.Structure):
@@ -53,6 +59,15 @@ class AttnWsCfg(ctypes.Structure):
 class RouteBwdWsCfg(ctypes.Structure):
     _fields_ = [("n_chunks", i64), ("n_q", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("d", ctypes.c_int)]
+
+
+class PagedAttnWsCfg(ctypes.Structure):
+    _fields_ = [("n_tok", i64), ("n_seq", ctypes.c_int), ("max_new", ctypes.c_int), ("hq", ctypes.c_int),
+                ("hkv", ctypes.c_int), ("max_pages", ctypes.c_int), ("page", ctypes.c_int), ("k", ctypes.c_int)]
+
+
+class PageSelectWsCfg(ctypes.Structure):
+    _fields_ = [("n_tok", i64), ("hkv", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 # name -> (restype, argtypes)
@@ -106,6 +121,15 @@ SIGNATURES = {
                                  vp, vp, vp, vp, sz, vp]),
     "msa_route_backward_workspace_size": (i32, [i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                 ctypes.POINTER(sz)]),
+    "msa_paged_append": (i32, [ctypes.POINTER(PagedKVArgs), vp, vp, vp, i32, i64, ctypes.c_int, vp, ctypes.c_int, i64,
+                               vp, i64, vp, vp]),
+    "msa_paged_attn": (i32, [ctypes.POINTER(PagedKVArgs), vp, i32, i64, ctypes.c_int, vp, ctypes.c_int, vp,
+                             ctypes.c_int, f32, vp, vp, vp, sz, vp]),
+    "msa_paged_attn_workspace_size": (i32, [i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                            ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)]),
+    "msa_page_select": (i32, [ctypes.POINTER(PagedKVArgs), vp, i32, i64, ctypes.c_int, vp, ctypes.c_int, ctypes.c_int,
+                              ctypes.c_int, vp, vp, sz, vp]),
+    "msa_page_select_workspace_size": (i32, [i64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)]),
     "msa_interleave_step": (i32, [ctypes.POINTER(InterleaveArgs), vp, vp, i64]),
     "msa_interleave_workspace_size": (i32, [ctypes.POINTER(InterleaveArgs), ctypes.POINTER(sz)]),
     "msa_interleave_graph_create": (i32, [ctypes.POINTER(InterleaveArgs), vp, ctypes.POINTER(vp)]),

@@ -310,6 +310,145 @@ def msa_sparse_attn_split(q, mem_kv, mem_len, local_k, local_v, L: int, q_start:
     return out
 
 
+# ------------------------------------------------------------------------------------------------ paged cache
+def _on_current(who: str, **tensors) -> None:
+    """The kernels run on the current device and read plain memory of it: anything else is refused."""
+    for name, t in tensors.items():
+        if t is not None and not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
+            raise ValueError(f"{who}: {name} is on {t.device}, not on the current CUDA device")
+
+
+def _want(who: str, name: str, t: torch.Tensor, dtype, shape) -> None:
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{who}: {name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
+
+
+class PagedKV:
+    """A paged 8-bit key/value cache (msa_paged_kv of include/msa.h) over the caller's tensors.
+
+    pages float8_e4m3fn [n_pages, 2, hkv, page, d], scales float32 [n_pages, 2, hkv], page_table int32 [n_seq,
+    max_pages], seq_len int32 [n_seq] (the tokens of a call included), bounds bfloat16 [n_pages, hkv, 2, d] or None.
+    The tensors stay where they are: page_table and seq_len are refilled in place as sequences grow."""
+
+    def __init__(self, pages, scales, page_table, seq_len, bounds=None):
+        n_pages, two, hkv, page, d = pages.shape
+        n_seq, max_pages = page_table.shape
+        _want("PagedKV", "pages", pages, torch.float8_e4m3fn, (n_pages, 2, hkv, page, d))
+        _want("PagedKV", "scales", scales, torch.float32, (n_pages, 2, hkv))
+        _want("PagedKV", "page_table", page_table, torch.int32, (n_seq, max_pages))
+        _want("PagedKV", "seq_len", seq_len, torch.int32, (n_seq,))
+        if bounds is not None:
+            _want("PagedKV", "bounds", bounds, torch.bfloat16, (n_pages, hkv, 2, d))
+        self.pages, self.scales, self.page_table, self.seq_len, self.bounds = pages, scales, page_table, seq_len, bounds
+        self.n_seq, self.max_pages, self.page, self.hkv, self.d = n_seq, max_pages, page, hkv, d
+        self.device = pages.device
+        for name, t in (("scales", scales), ("page_table", page_table), ("seq_len", seq_len), ("bounds", bounds)):
+            if t is not None and t.device != pages.device:
+                raise ValueError(f"PagedKV: {name} is on {t.device}, pages on {pages.device}")
+        self.args = _lib.PagedKVArgs(_ptr(pages), _ptr(scales), _ptr(bounds), _ptr(page_table), _ptr(seq_len), n_pages,
+                                     n_seq, max_pages, page, hkv, d)
+        self._ref = ctypes.byref(self.args)
+
+    @classmethod
+    def empty(cls, n_pages: int, n_seq: int, max_pages: int, hkv: int, page: int = 64, d: int = 128,
+              bounds: bool = True, device="cuda") -> "PagedKV":
+        """A cache of n_pages free pages and n_seq empty sequences."""
+        return cls(torch.empty((n_pages, 2, hkv, page, d), dtype=torch.float8_e4m3fn, device=device),
+                   torch.ones((n_pages, 2, hkv), dtype=torch.float32, device=device),
+                   torch.zeros((n_seq, max_pages), dtype=torch.int32, device=device),
+                   torch.zeros(n_seq, dtype=torch.int32, device=device),
+                   torch.zeros((n_pages, hkv, 2, d), dtype=torch.bfloat16, device=device) if bounds else None)
+
+    def _check(self, who: str, tok_off, x, heads: int) -> None:
+        _on_current(who, cache=self.pages, tok_off=tok_off, tokens=x)
+        if tok_off.dtype != torch.int64 or tok_off.shape != (self.n_seq + 1,):
+            raise ValueError(f"{who}: tok_off must be int64 [{self.n_seq + 1}], got {tok_off.dtype} of "
+                             f"{tuple(tok_off.shape)}")
+        if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != self.d:
+            raise ValueError(f"{who}: expected [n_tok, {heads}, {self.d}], got {tuple(x.shape)}")
+
+
+def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offset: int = 0, q=None, q_rot=None,
+                     stream=None):
+    """Append k, v [n_tok, hkv, d] to the cache, keys rotated to pos_offset + their place in the sequence; tok_off
+    int64 [n_seq + 1] (device) splits the packed tokens, at most max_new a sequence; kv.seq_len already counts them.
+    With q [n_tok, hq, d] the queries are rotated too: returns q_rot (allocated when not given), else None."""
+    kv._check("msa_paged_append", tok_off, k, kv.hkv)
+    _on_current("msa_paged_append", v=v, cos_sin=cos_sin, q=q, q_rot=q_rot)
+    _want("msa_paged_append", "v", v, k.dtype, k.shape)
+    if cos_sin.dtype != torch.float32 or cos_sin.shape[1:] != (kv.d // 2, 2):
+        raise ValueError(f"msa_paged_append: cos_sin must be float32 [max_pos, {kv.d // 2}, 2]")
+    hq = 0
+    if q is not None:
+        hq = q.shape[1]
+        _want("msa_paged_append", "q", q, k.dtype, (k.shape[0], hq, kv.d))
+        if q_rot is None:
+            q_rot = torch.empty_like(q)
+        _want("msa_paged_append", "q_rot", q_rot, q.dtype, q.shape)
+    check(lib.msa_paged_append(kv._ref, _ptr(k), _ptr(v), _ptr(q), _dt(k), k.shape[0], hq, _ptr(tok_off), max_new,
+                               pos_offset, _ptr(cos_sin), cos_sin.shape[0], _ptr(q_rot) if q is not None else None,
+                               _stream(stream)), "msa_paged_append")
+    return q_rot if q is not None else None
+
+
+def page_select_workspace_size(n_tok: int, hkv: int, max_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(lib.msa_page_select_workspace_size(n_tok, hkv, max_pages, ctypes.byref(n)), "msa_page_select_workspace_size")
+    return n.value
+
+
+def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int = 1, sel=None, ws=None, stream=None):
+    """The k pages that each new token's query heads q [n_tok, hq, d] (rotated) should attend over, by the bounds of
+    the pages' keys -> sel int32 [n_tok, hkv, k], ascending page indices of the sequence, -1 where there are fewer."""
+    n_tok, hq = q.shape[:2]
+    kv._check("msa_page_select", tok_off, q, hq)
+    if sel is None:
+        sel = torch.empty((n_tok, kv.hkv, k), dtype=torch.int32, device=kv.device)
+    _on_current("msa_page_select", sel=sel, ws=ws)
+    _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
+    if ws is None:
+        ws = _ws(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages), kv.device)
+    check(lib.msa_page_select(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, k, recent, _ptr(sel),
+                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "msa_page_select")
+    return sel
+
+
+def paged_attn_workspace_size(n_tok: int, n_seq: int, max_new: int, hq: int, hkv: int, max_pages: int, page: int,
+                              k: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    check(lib.msa_paged_attn_workspace_size(n_tok, n_seq, max_new, hq, hkv, max_pages, page, k, ctypes.byref(n)),
+          "msa_paged_attn_workspace_size")
+    return n.value
+
+
+def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float | None = None, out=None, lse=None,
+                   want_lse: bool = False, ws=None, stream=None):
+    """Attention of the new tokens q [n_tok, hq, d] (bf16, rotated) over the cache, causal within the call; with sel
+    int32 [n_tok, hkv, k] over the listed pages only. Returns out [n_tok, hq, d], with lse float32 [n_tok, hq]
+    (given or wanted) the pair (out, lse)."""
+    n_tok, hq = q.shape[:2]
+    kv._check("msa_paged_attn", tok_off, q, hq)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((n_tok, hq), dtype=torch.float32, device=kv.device)
+    _on_current("msa_paged_attn", out=out, lse=lse, sel=sel, ws=ws)
+    _want("msa_paged_attn", "out", out, q.dtype, q.shape)
+    if lse is not None:
+        _want("msa_paged_attn", "lse", lse, torch.float32, (n_tok, hq))
+    k = 0
+    if sel is not None:
+        k = sel.shape[-1]
+        _want("msa_paged_attn", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
+    if ws is None:
+        ws = _ws(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k), kv.device)
+    scale = 1.0 / math.sqrt(kv.d) if scale is None else scale
+    check(lib.msa_paged_attn(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, _ptr(sel), k, scale,
+                             _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+          "msa_paged_attn")
+    return out if lse is None else (out, lse)
+
+
 # ------------------------------------------------------------------------------------------------ backward
 def msa_sparse_attn_backward(q, mem_kv, mem_len, local_k, local_v, L: int, q_start: int, out, dout, lse,
                              scale: float | None = None, grads=None, ws=None, stream=None):

@@ -129,6 +129,15 @@ msa_status msa_workspace_size(int op, const void* cfg, size_t* bytes) {
         }
         case MSA_OP_INTERLEAVE:
             return msa_interleave_workspace_size(static_cast<const msa_interleave_args*>(cfg), bytes);
+        case MSA_OP_PAGED_ATTN: {
+            const auto* c = static_cast<const msa_paged_attn_ws_cfg*>(cfg);
+            return msa_paged_attn_workspace_size(c->n_tok, c->n_seq, c->max_new, c->hq, c->hkv, c->max_pages, c->page,
+                                                 c->k, bytes);
+        }
+        case MSA_OP_PAGE_SELECT: {
+            const auto* c = static_cast<const msa_page_select_ws_cfg*>(cfg);
+            return msa_page_select_workspace_size(c->n_tok, c->hkv, c->max_pages, bytes);
+        }
         default:
             return set_error(MSA_ERR_INVALID_ARG, "msa_workspace_size: unknown op %d", op);
     }

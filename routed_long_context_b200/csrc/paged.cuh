@@ -1,0 +1,91 @@
+// The paged 8-bit key/value cache (msa_paged_kv): what its kernels share.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace msa {
+
+constexpr int kPagedD = 128;             // head dimension
+constexpr int kScaleMin = -50;           // range of the scale exponents; with both ends inside fp32's own
+constexpr int kScaleMax = 50;            // range, scale and 1 / scale are exact and so is every product
+
+struct PagedView {
+    uint8_t* pages;                      // e4m3 [n_pages][2][hkv][page][128]
+    float* scales;                       // [n_pages][2][hkv]
+    __nv_bfloat16* bounds;               // [n_pages][hkv][2][128] or NULL
+    const int32_t* table;                // [n_seq][max_pages]
+    const int32_t* len;                  // [n_seq]
+    int64_t n_pages;
+    int n_seq, max_pages, page, shift, hkv;   // page = 1 << shift
+};
+
+// Checks what the host can see of a cache; `who` names the entry point in the message.
+msa_status paged_view(const msa_paged_kv* kv, const char* who, PagedView* out);
+// Checks of the arguments that every call on a cache takes.
+msa_status paged_tokens_ok(const msa_paged_kv* kv, const char* who, int64_t n_tok, const int64_t* tok_off, int max_new);
+
+// The new tokens of a sequence: rows t0 .. t0 + n_new - 1 of the packed buffers, the last n_new of its
+// `len` cached tokens.
+struct SeqSpan {
+    int64_t t0;
+    int n_new, len;
+};
+// False (with MSA_DEV_BAD_INDEX recorded) where offsets or length contradict the call's sizes: the sequence
+// is then skipped by every kernel.
+__device__ __forceinline__ bool seq_span(const PagedView& v, const int64_t* __restrict__ tok_off, int64_t n_tok,
+                                         int max_new, int s, SeqSpan* sp, int* err) {
+    const int64_t a = tok_off[s], b = tok_off[s + 1];
+    const int64_t len = v.len[s];
+    sp->t0 = a;
+    sp->n_new = 0;
+    sp->len = 0;
+    if (a < 0 || b < a || b > n_tok || b - a > max_new || len < b - a || len > (int64_t)v.max_pages << v.shift) {
+        record_device_error(err, MSA_DEV_BAD_INDEX);
+        return false;
+    }
+    sp->n_new = (int)(b - a);
+    sp->len = (int)len;
+    return true;
+}
+
+// The sequence of packed row t: the last one that starts at or before it. Every lane of a warp takes part.
+__device__ __forceinline__ int seq_of_token(const int64_t* __restrict__ tok_off, int n_seq, int64_t t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = n_seq;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int s = lo + lane * step;
+        const bool in = lane * step < n && tok_off[s] <= t;
+        const int hit = 31 - __clz(__ballot_sync(0xffffffffu, in) | 1u);
+        n = min(step, n - hit * step);
+        lo += hit * step;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }   // -126 <= e <= 127
+__device__ __forceinline__ int exponent_of(float pow2) { return (int)((__float_as_uint(pow2) >> 23) & 255u) - 127; }
+
+// Exponent of the smallest power of two s with amax / s <= 448 = 1.75 * 2^8, by the bits of amax:
+// amax = m 2^x with 1 <= m < 2 needs x - 8 where m <= 1.75 and x - 7 otherwise (also for subnormals, whose
+// exponent field reads -127: they clamp to the smallest scale).
+__device__ __forceinline__ int scale_exponent(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return max(kScaleMin, min(kScaleMax, e));
+}
+
+// Two fp32 values to e4m3, to nearest even, saturating: the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 e4m3x2_f32(uint32_t u) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u, __NV_E4M3);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+}  // namespace msa
