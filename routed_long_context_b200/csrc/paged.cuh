@@ -5,6 +5,8 @@
 #include <cuda_fp8.h>
 #include <cuda_fp16.h>
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace msa {
@@ -87,5 +89,48 @@ __device__ __forceinline__ float2 e4m3x2_f32(uint32_t u) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u, __NV_E4M3);
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
+
+// ---- attention: how the work is cut ---------------------------------------------------------------
+// A segment is one softmax: the query rows of one kv head that are handled together, over their keys. The
+// segments' key tiles are numbered through (sequence, row block, kv head, tile) and the numbers cut into one
+// contiguous range of equal length per CTA, so that lengths however far apart load every SM alike. A CTA that
+// holds the whole of a segment writes its output; otherwise the pieces go to the workspace (slot 1 of the CTA
+// in which the segment starts, slot 0 of those in which it goes on) and are joined by the combine pass.
+struct PagedAttnArgs {
+    PagedView v;
+    const __nv_bfloat16* q;
+    int64_t n_tok;
+    const int64_t* tok_off;
+    int max_new, G;
+    const int32_t* sel;      // page lists [n_tok][hkv][k] or NULL
+    int k;
+    float scale_log2e;
+    __nv_bfloat16* out;
+    float* lse;
+    int rows;                // rows of a workspace slot
+    float* part_o;           // [CTA][2][rows][128], unnormalised
+    float2* part_ml;         // [CTA][2][rows]: reference maximum (log2) and sum
+    struct OpenSegment* open;  // [CTA]
+    int* err;
+};
+struct OpenSegment {         // the segment that starts in a CTA and ends in a later one
+    int64_t t0;              // first packed row
+    int head, rows, n_more;  // kv head, query rows, later CTAs that hold pieces (0: there is no such segment)
+    float unit;              // of the unnormalised output
+};
+
+// CTA i of n takes tiles total * i / n .. total * (i + 1) / n - 1; the one that holds tile x:
+__device__ __forceinline__ int64_t cta_first(int64_t total, int n, int i) { return total * i / n; }
+__device__ __forceinline__ int cta_of_tile(int64_t total, int n, int64_t x) {
+    int i = (int)(x * n / total);
+    while (cta_first(total, n, i + 1) <= x) ++i;
+    while (cta_first(total, n, i) > x) --i;
+    return i;
+}
+
+// The few-rows kernel (paged_decode.cu) and the many-rows kernel (paged_prompt.cu).
+constexpr int kDecodeRows = 8;
+constexpr int kDecodeTile = 16;
+msa_status launch_paged_decode(const PagedAttnArgs& a, int grid, cudaStream_t s);
 
 }  // namespace msa

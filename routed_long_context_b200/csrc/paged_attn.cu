@@ -12,20 +12,6 @@
 namespace msa {
 namespace {
 
-struct PagedAttnArgs {
-    PagedView v;
-    const __nv_bfloat16* q;
-    int64_t n_tok;
-    const int64_t* tok_off;
-    int max_new, G;
-    const int32_t* sel;
-    int k;
-    float scale_log2e;
-    __nv_bfloat16* out;
-    float* lse;
-    int* err;
-};
-
 template <int G>
 __global__ void __launch_bounds__(128) paged_attn_kernel(const PagedAttnArgs a) {
     const PagedView& v = a.v;
@@ -119,6 +105,58 @@ __global__ void __launch_bounds__(128) paged_attn_kernel(const PagedAttnArgs a) 
     }
 }
 
+// The combine pass, a programmatic dependent of the attention kernel: block (i, y) joins rows 2 y and 2 y + 1 of
+// the segment that starts in CTA i and goes on in later ones, in the CTAs' order.
+__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const OpenSegment seg = a.open[blockIdx.x];
+    const int n = 2 * blockIdx.y + (threadIdx.x >> 7), d = threadIdx.x & 127;
+    if (seg.n_more == 0 || n >= seg.rows) return;
+    const int64_t first = ((int64_t)blockIdx.x * 2 + 1) * a.rows + n;
+    float M = -INFINITY;
+    for (int i = 0; i <= seg.n_more; ++i) M = fmaxf(M, a.part_ml[first + (i ? 2 * i - 1 : 0) * a.rows].x);
+    float L = 0.f, x = 0.f;
+#pragma unroll 4
+    for (int i = 0; i <= seg.n_more; ++i) {
+        const int64_t row = first + (i ? 2 * i - 1 : 0) * a.rows;    // slot 1, then slot 0 of the next CTAs
+        const float2 ml = a.part_ml[row];
+        const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+        L += ml.x == -INFINITY ? ml.y : w * ml.y;
+        x += w * a.part_o[row * kPagedD + d];
+    }
+    const int64_t row = (seg.t0 + n / a.G) * (a.v.hkv * a.G) + seg.head * a.G + n % a.G;
+    a.out[row * kPagedD + d] = __float2bfloat16_rn(L == 0.f ? 0.f : x * (seg.unit / L));
+    if (a.lse && d == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+constexpr int kGrid = 296;        // CTAs of the few-rows kernel: two per SM
+
+struct AttnPlan {
+    bool few;                     // the few-rows kernel
+    int grid, rows;
+    size_t o, ml, open, bytes;    // offsets in the workspace
+};
+AttnPlan attn_plan(int64_t n_tok, int n_seq, int max_new, int hq, int hkv, int max_pages, int page, int k) {
+    AttnPlan p{};
+    const int G = hq / hkv;
+    p.few = k > 0 || (int64_t)max_new * G <= kDecodeRows;
+    p.rows = kDecodeRows;
+    const int64_t pages = k > 0 ? n_tok * k : (int64_t)std::min<int64_t>(n_tok, n_seq) * max_pages;
+    const int64_t tiles = pages * hkv * (page / kDecodeTile);
+    p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(kGrid, (tiles + 7) / 8));
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t was = at;
+        at += align_up(n, 256);
+        return was;
+    };
+    p.o = take((size_t)p.grid * 2 * p.rows * kPagedD * sizeof(float));
+    p.ml = take((size_t)p.grid * 2 * p.rows * sizeof(float2));
+    p.open = take((size_t)p.grid * sizeof(OpenSegment));
+    p.bytes = at;
+    return p;
+}
+
 }  // namespace
 }  // namespace msa
 
@@ -128,9 +166,9 @@ extern "C" msa_status msa_paged_attn_workspace_size(int64_t n_tok, int n_seq, in
                                                     int max_pages, int page, int k, size_t* bytes) {
     MSA_REQUIRE(bytes != nullptr, "msa_paged_attn_workspace_size: bytes is NULL");
     MSA_REQUIRE(n_tok >= 0 && n_seq > 0 && max_new >= 0 && hkv > 0 && hq > 0 && hq % hkv == 0 && max_pages > 0 &&
-                    page > 0 && k >= 0,
+                    page >= 16 && k >= 0,
                 "msa_paged_attn_workspace_size: bad sizes");
-    *bytes = 256;
+    *bytes = attn_plan(n_tok, n_seq, max_new, hq, hkv, max_pages, page, k).bytes;
     return MSA_OK;
 }
 
@@ -147,6 +185,7 @@ extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_
     if (a.G != 1 && a.G != 2 && a.G != 4 && a.G != 8)
         return set_error(MSA_ERR_UNSUPPORTED, "msa_paged_attn: hq/hkv = %d unsupported", a.G);
     MSA_REQUIRE(sel == nullptr || k >= 1, "msa_paged_attn: k must be at least 1 with a page list");
+    MSA_REQUIRE(sel == nullptr || (int64_t)k * kv->page <= (int64_t)INT32_MAX, "msa_paged_attn: k * page too large");
     if (n_tok == 0 || max_new == 0) return MSA_OK;
     MSA_REQUIRE(q && out && ws, "msa_paged_attn: NULL pointer");
     MSA_REQUIRE(aligned16(q) && aligned16(out) && aligned16(lse) && aligned16(sel) && aligned16(ws),
@@ -162,6 +201,27 @@ extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_
     a.lse = lse;
     a.err = device_error_word();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const AttnPlan p = attn_plan(n_tok, kv->n_seq, max_new, hq, kv->hkv, kv->max_pages, kv->page, sel ? k : 0);
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    a.rows = p.rows;
+    a.part_o = reinterpret_cast<float*>(w + p.o);
+    a.part_ml = reinterpret_cast<float2*>(w + p.ml);
+    a.open = reinterpret_cast<OpenSegment*>(w + p.open);
+    if (p.few) {
+        MSA_RETURN_IF(launch_paged_decode(a, p.grid, s));
+        if (p.grid == 1) return MSA_OK;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)p.grid, (unsigned)(std::min<int64_t>(p.rows, sel ? a.G : (int64_t)max_new * a.G) + 1) / 2);
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        MSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_combine_kernel, a));
+        return MSA_OK;
+    }
     const dim3 grid((unsigned)n_tok, (unsigned)kv->hkv);
     switch (a.G) {
         case 1: paged_attn_kernel<1><<<grid, 128, 0, s>>>(a); break;
