@@ -1,0 +1,784 @@
+// Attention of many query rows over a paged 8-bit cache, on tcgen05 tensor cores.
+//
+//   out = softmax(scale q . K) V  for blocks of 128 or 256 rows (token, query head) of one kv head.
+// Rows are TMEM lanes. Per tile of 128 keys and 128 rows:
+//   S = Qhi K^T + Qlo K^T     tcgen05.mma f8f6f4, M = N = 128, K = 128 each, straight from the cache's bytes. A query row
+//                             is split as q = s (hi + lo), s a power of two that brings its largest to 224..448 and hi
+//                             and lo e4m3: eight significant bits, which is all that bf16 has, down to 2^-11 of the
+//                             row's largest; what lies below is off by at most 2^-10 s. Two 8-bit products cost what
+//                             one 16-bit product would, and K needs no conversion.
+//   P = 2^(S f - m)           a thread per row; f carries the softmax scale, s and the page's scale of K (a power of two
+//                             per 16 columns at least). m is a stale maximum: P is rounded to bf16, whose exponent has
+//                             room, so m moves only when a tile's sum shows a logit more than 2^15 above it, and no
+//                             maximum is taken otherwise. P replaces S in TMEM.
+//   O += P V                  tcgen05.mma f16 (bf16), A = P from TMEM, B = V as bf16 (exact: e4m3 times its scale), put
+//                             into shared memory by four warps of their own.
+// Two warpgroups take the two row blocks of 256 rows in turns (their products and exponentials overlap), or, of a
+// 128-row block, the even and the odd key tiles, joined at the end.
+// The products cost 8 * 128^3 flops a tile and row block, 1,024 cycles at the tensor peak; 128 * 128 exponentials take
+// as long on the special-function units: both bound it.
+//
+// Roles of the 512 threads: warp 0 loads pages by TMA (128-byte swizzle, K three tiles deep, V two), warp 1 issues the
+// products, warps 4..11 run the softmax, warps 12..15 convert V. Every wait is bounded; when one runs out the block
+// records MSA_DEV_WAIT_TIMEOUT and leaves in order.
+#include <algorithm>
+#include <mutex>
+
+#include "kernels.cuh"
+#include "mma.cuh"
+#include "paged.cuh"
+#include "tc.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kKT = 128;                                   // keys per tile
+constexpr int kRowsTile = 128;                             // MMA M
+constexpr int kKStages = 3, kVStages = 2, kV16Stages = 2, kInfo = 8;
+constexpr int kWin = kThreads;                             // sequences looked at together
+constexpr float kTrigger = 32768.f;                        // a tile's sum above it moves the reference maximum
+
+constexpr int kBytes8 = kKT * kPagedD;                     // a tile of K or V in 8 bits: 16 KB
+constexpr int kBytes16 = 2 * kBytes8;
+
+struct PromptSmem {
+    uint8_t q[2][2][kRowsTile * kPagedD];                  // [row block][hi, lo]
+    uint8_t k[kKStages][kBytes8];
+    uint8_t v8[kVStages][kBytes8];
+    uint8_t v16[kV16Stages][kBytes16];                     // [d half][key][64]
+    float sk[kInfo][8], sv[kInfo][8];                      // scales per 16 keys of a tile; sv 0: nothing there
+    uint64_t k_full[kKStages], k_empty[kKStages], v8_full[kVStages], v8_empty[kVStages];
+    uint64_t v16_full[kV16Stages], v16_empty[kV16Stages];
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
+    uint32_t tmem;
+    int abort_flag, stop;
+    long long pre[kWin + 1];
+    int64_t t0[kWin];
+    int n_new[kWin], len[kWin];
+    long long scan[kThreads / 32];
+    float2 ml[kRowsTile];
+};
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A from TMEM
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32_u32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+// One run of key tiles of one segment.
+struct Piece {
+    int64_t t0;            // first packed row of the block's tokens
+    int head, rows;        // kv head, query rows
+    int seen0;             // keys that the block's first token sees
+    int len;               // keys of the sequence
+    int s;                 // sequence
+    int k0, n;             // first key tile, number of them
+    bool starts, ends;     // holds the segment's first tile, its last
+    long long seg_end;     // one past the segment's last tile, in the window's numbers
+};
+
+__device__ __forceinline__ int seg_tiles(int base, int n_new, int tpb, int rb) {
+    return (base + min(n_new, (rb + 1) * tpb) + kKT - 1) / kKT;
+}
+
+template <bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_constant__ CUtensorMap tm,
+                                                                   const PagedAttnArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    PromptSmem& sm = *reinterpret_cast<PromptSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const PagedView& v = a.v;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.G, hq = v.hkv * G;
+    const int tpb = (SPLIT ? kRowsTile : 2 * kRowsTile) / G;       // tokens of a row block
+    const float ninf = -INFINITY;
+    volatile int* abort_flag = &sm.abort_flag;
+
+    if (tid == 0) {
+        for (int i = 0; i < kKStages; ++i) mbar_init(smem_u32(&sm.k_full[i]), 1), mbar_init(smem_u32(&sm.k_empty[i]), 1);
+        for (int i = 0; i < kVStages; ++i) mbar_init(smem_u32(&sm.v8_full[i]), 1), mbar_init(smem_u32(&sm.v8_empty[i]), 128);
+        for (int i = 0; i < kV16Stages; ++i)
+            mbar_init(smem_u32(&sm.v16_full[i]), 128), mbar_init(smem_u32(&sm.v16_empty[i]), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.q_full[i]), 128);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), 128);
+            mbar_init(smem_u32(&sm.o_done[i]), 1);
+        }
+        mbar_init(smem_u32(&sm.drain), 1);
+        sm.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+
+    // tiles of all sequences
+    const int n_windows = (v.n_seq + kWin - 1) / kWin;
+    auto load_window = [&](int w) -> long long {
+        const int s = w * kWin + tid;
+        SeqSpan sp{0, 0, 0};
+        if (s < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, blockIdx.x == 0 ? a.err : nullptr);
+        long long x = 0;
+        for (int rb = 0; rb * tpb < sp.n_new; ++rb) x += seg_tiles(sp.len - sp.n_new, sp.n_new, tpb, rb);
+        x *= v.hkv;
+        long long up = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, up, o);
+            if (lane >= o) up += y;
+        }
+        __syncthreads();
+        sm.t0[tid] = sp.t0;
+        sm.n_new[tid] = sp.n_new;
+        sm.len[tid] = sp.len;
+        if (lane == 31) sm.scan[warp] = up;
+        __syncthreads();
+        long long before = 0, total = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += sm.scan[i];
+            total += sm.scan[i];
+        }
+        sm.pre[tid + 1] = before + up;
+        if (tid == 0) sm.pre[0] = 0;
+        __syncthreads();
+        return total;
+    };
+    long long total = 0, first_total = 0;
+    for (int w = n_windows - 1; w >= 0; --w) {
+        first_total = load_window(w);
+        total += first_total;
+    }
+    constexpr int kMinTiles = SPLIT ? 2 : 1;
+    const int n_cta = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+    if ((int)blockIdx.x >= n_cta) {
+        if (tid == 0) a.open[blockIdx.x].n_more = 0;
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        return;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;                         // S (and P) of warpgroup w at 128 w, O at 256 + 128 w
+    const long long my_a = cta_first(total, n_cta, blockIdx.x), my_b = cta_first(total, n_cta, blockIdx.x + 1);
+
+    long long base = 0;
+    // every role's own counts, which give the ring stages and phases
+    int cnt = 0;                                           // tiles of earlier pieces
+    int pieces = 0;                                        // pieces (softmax: those in which the warpgroup had a tile)
+    int taken[2] = {0, 0};                                 // tiles of each softmax warpgroup
+    for (int w = 0; w < n_windows; ++w) {
+        const long long in_window = (w == 0) ? first_total : load_window(w);
+        const long long A = max(my_a - base, 0LL), B = min(my_b - base, in_window);
+        if (A >= B) {
+            base += in_window;
+            continue;
+        }
+        // the pieces of [A, B), in order; every role walks them for itself
+        auto walk = [&](auto&& body) {
+            int lo = 0, n = min(kWin, v.n_seq - w * kWin);
+            while (n > 1) {
+                const int h = n / 2;
+                if (sm.pre[lo + h] <= A) {
+                    lo += h;
+                    n -= h;
+                } else {
+                    n = h;
+                }
+            }
+            int rb = 0, head = 0;
+            int n_new = sm.n_new[lo], len = sm.len[lo];
+            int tiles = seg_tiles(len - n_new, n_new, tpb, 0);
+            long long start = sm.pre[lo];
+            while (start + (long long)tiles * v.hkv <= A) {
+                start += (long long)tiles * v.hkv;
+                tiles = seg_tiles(len - n_new, n_new, tpb, ++rb);
+            }
+            head = (int)((A - start) / tiles);
+            start += (long long)head * tiles;
+            for (long long g = A; g < B;) {
+                const long long g1 = min(B, start + tiles);
+                Piece p;
+                p.t0 = sm.t0[lo] + rb * tpb;
+                p.head = head;
+                p.rows = min(tpb, n_new - rb * tpb) * G;
+                p.seen0 = len - n_new + rb * tpb + 1;
+                p.len = len;
+                p.s = w * kWin + lo;
+                p.k0 = (int)(g - start);
+                p.n = (int)(g1 - g);
+                p.starts = g == start;
+                p.ends = g1 == start + tiles;
+                p.seg_end = start + tiles;
+                if (!body(p)) return;
+                g = g1;
+                if (!p.ends) return;
+                start = g1;
+                if (++head == v.hkv) {
+                    head = 0;
+                    if (++rb * tpb >= n_new) {
+                        if (g >= B) return;
+                        rb = 0;
+                        do ++lo;
+                        while (sm.n_new[lo] == 0);
+                        n_new = sm.n_new[lo];
+                        len = sm.len[lo];
+                    }
+                    tiles = seg_tiles(len - n_new, n_new, tpb, rb);
+                }
+            }
+        };
+
+        if (warp == 0) {
+            // ------------------------------------------------------------------ loader
+            // Lane 8 i + c looks up 16-key chunk c of tile i of a group of four tiles; the page ids of the group after
+            // the next and the scales of the next are on their way while a group is issued.
+            const int c = lane & 7, sub = lane >> 3;
+            const int cps = v.shift - 4;                   // log2(chunks per page)
+            walk([&](const Piece& p) -> bool {
+                const int32_t* table = v.table + (int64_t)p.s * v.max_pages;
+                auto exists = [&](int group) -> bool {
+                    const int j = 4 * group + sub;
+                    return j < p.n && (int64_t)(p.k0 + j) * kKT + 16 * c < p.len;
+                };
+                auto page_id = [&](int group) -> int32_t {
+                    return exists(group) ? table[((p.k0 + 4 * group + sub) * 8 + c) >> cps] : -1;
+                };
+                auto scales = [&](int group, int32_t& id, float* sk, float* sv) {
+                    *sk = *sv = 0.f;
+                    if (id < 0 || id >= v.n_pages) {
+                        if (exists(group)) record_device_error(a.err, MSA_DEV_BAD_INDEX);
+                        id = -1;
+                        return;
+                    }
+                    const int64_t slab = (int64_t)id * 2 * v.hkv + p.head;
+                    *sk = v.scales[slab];
+                    *sv = v.scales[slab + v.hkv];
+                };
+                int32_t id0 = page_id(0), id1 = page_id(1), id2;
+                float sk0, sv0, sk1, sv1;
+                scales(0, id0, &sk0, &sv0);
+                for (int group = 0; 4 * group < p.n; ++group) {
+                    id2 = page_id(group + 2);
+                    scales(group + 1, id1, &sk1, &sv1);
+                    for (int i = 0; i < 4 && 4 * group + i < p.n; ++i) {
+                        const int n = cnt + 4 * group + i;
+                        const int ks = n % kKStages, vs = n % kVStages;
+                        const bool here = sub == i;
+                        const bool first = here && id0 >= 0 && (c & ((1 << cps) - 1)) == 0;
+                        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, first)) * (uint32_t)(v.page * kPagedD);
+                        const int row = first ? (int)(((int64_t)id0 * 2 * v.hkv + p.head) * v.page) : 0;
+                        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.k_empty[ks]), ((uint32_t)(n / kKStages) & 1u) ^ 1u, abort_flag)))
+                            return false;
+                        if (here) {
+                            sm.sk[n % kInfo][c] = sk0;
+                            sm.sv[n % kInfo][c] = sv0;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_expect_tx(smem_u32(&sm.k_full[ks]), bytes);
+                        __syncwarp();
+                        if (first) tma_load_2d(smem_u32(sm.k[ks]) + c * 16 * kPagedD, &tm, 0, row, smem_u32(&sm.k_full[ks]));
+                        taken[0] = n + 1;                              // here: tiles whose K, V is under way
+                        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.v8_empty[vs]), ((uint32_t)(n / kVStages) & 1u) ^ 1u, abort_flag)))
+                            return false;
+                        if (lane == 0) mbar_expect_tx(smem_u32(&sm.v8_full[vs]), bytes);
+                        __syncwarp();
+                        if (first)
+                            tma_load_2d(smem_u32(sm.v8[vs]) + c * 16 * kPagedD, &tm, 0, row + v.hkv * v.page,
+                                        smem_u32(&sm.v8_full[vs]));
+                        taken[1] = n + 1;
+                    }
+                    id0 = id1;
+                    sk0 = sk1;
+                    sv0 = sv1;
+                    id1 = id2;
+                }
+                cnt += p.n;
+                return true;
+            });
+        } else if (warp == 1) {
+            // ------------------------------------------------------------------ products
+            if (lane == 0) {
+                // f8f6f4: e4m3 x e4m3 -> fp32, both K-major; f16: bf16 x bf16 -> fp32, V MN-major
+                const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(kRowsTile >> 4) << 24);
+                const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kPagedD >> 3) << 17) |
+                                         ((uint32_t)(kRowsTile >> 4) << 24);
+                walk([&](const Piece& p) -> bool {
+                    auto issue_s = [&](int wg, int j, bool wait_k) -> bool {
+                        const int n = cnt + j, ks = n % kKStages;
+                        if (wait_k && !mbar_wait(smem_u32(&sm.k_full[ks]), (uint32_t)(n / kKStages) & 1u, abort_flag)) return false;
+                        tc_fence_after();
+                        const uint64_t kd = sw128_desc(smem_u32(sm.k[ks]));
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            const uint64_t qd = sw128_desc(smem_u32(sm.q[SPLIT ? 0 : wg][part]));
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_f8(tmem + 128 * wg, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), idesc_s,
+                                        (part | kk) ? 1u : 0u);
+                        }
+                        umma_commit(smem_u32(&sm.s_full[wg]));
+                        return true;
+                    };
+                    auto issue_o = [&](int wg, int j, bool wait_v, bool fresh) -> bool {
+                        if (!mbar_wait(smem_u32(&sm.p_full[wg]), (uint32_t)taken[wg] & 1u, abort_flag)) return false;
+                        ++taken[wg];
+                        const int n = cnt + j, vs = n % kV16Stages;
+                        if (wait_v && !mbar_wait(smem_u32(&sm.v16_full[vs]), (uint32_t)(n / kV16Stages) & 1u, abort_flag)) return false;
+                        tc_fence_after();
+                        const uint64_t vd = sw128_mn_desc(smem_u32(sm.v16[vs]), kKT * 128);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)     // 16 keys: 8 columns of P, 16 rows of V
+                            umma_bf16_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)),
+                                         idesc_o, (!fresh || kk) ? 1u : 0u);
+                        return true;
+                    };
+                    const uint32_t qp = (uint32_t)pieces & 1u;
+                    if (SPLIT) {
+                        if (!mbar_wait(smem_u32(&sm.q_full[0]), qp, abort_flag)) return false;
+                        for (int j = 0; j < 2 && j < p.n; ++j) {
+                            if (!issue_s(j, j, true)) return false;
+                            umma_commit(smem_u32(&sm.k_empty[(cnt + j) % kKStages]));
+                        }
+                        for (int j = 0; j < p.n; ++j) {
+                            const int wg = j & 1;
+                            if (!issue_o(wg, j, true, j < 2)) return false;
+                            umma_commit(smem_u32(&sm.v16_empty[(cnt + j) % kV16Stages]));
+                            if (j + 2 < p.n) {
+                                if (!issue_s(wg, j + 2, true)) return false;
+                                umma_commit(smem_u32(&sm.k_empty[(cnt + j + 2) % kKStages]));
+                            } else {
+                                umma_commit(smem_u32(&sm.o_done[wg]));
+                            }
+                        }
+                    } else {
+                        for (int wg = 0; wg < 2; ++wg) {
+                            if (!mbar_wait(smem_u32(&sm.q_full[wg]), qp, abort_flag)) return false;
+                            if (!issue_s(wg, 0, wg == 0)) return false;
+                        }
+                        umma_commit(smem_u32(&sm.k_empty[cnt % kKStages]));
+                        for (int j = 0; j < p.n; ++j)
+                            for (int wg = 0; wg < 2; ++wg) {
+                                if (!issue_o(wg, j, wg == 0, j == 0)) return false;
+                                if (wg == 1) umma_commit(smem_u32(&sm.v16_empty[(cnt + j) % kV16Stages]));
+                                if (j + 1 < p.n) {
+                                    if (!issue_s(wg, j + 1, wg == 0)) return false;
+                                    if (wg == 1) umma_commit(smem_u32(&sm.k_empty[(cnt + j + 1) % kKStages]));
+                                } else {
+                                    umma_commit(smem_u32(&sm.o_done[wg]));
+                                }
+                            }
+                    }
+                    cnt += p.n;
+                    ++pieces;
+                    return true;
+                });
+            }
+        } else if (warp >= 12) {
+            // ------------------------------------------------------------------ V to bf16
+            // Thread (row y of 16, piece c of 8): 16 values of rows y, y + 16, ...; the 32 bytes go to two 16-byte places
+            // of the swizzled bf16 tile, in an order that keeps the eight threads of a row on distinct banks.
+            const int ct = tid - 384, c = ct & 7, y = ct >> 3;
+            walk([&](const Piece& p) -> bool {
+                for (int j = 0; j < p.n; ++j) {
+                    const int n = cnt + j, vs = n % kVStages, v2 = n % kV16Stages;
+                    if (!mbar_wait(smem_u32(&sm.v8_full[vs]), (uint32_t)(n / kVStages) & 1u, abort_flag)) return false;
+                    if (!mbar_wait(smem_u32(&sm.v16_empty[v2]), ((uint32_t)(n / kV16Stages) & 1u) ^ 1u, abort_flag)) return false;
+                    const int left = p.len - (p.k0 + j) * kKT;         // keys of the tile that the sequence has
+                    uint8_t* dst = sm.v16[v2] + (c >> 2) * (kKT * 128);
+                    const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 16 * i + y;
+                        const float sv = sm.sv[n % kInfo][i];
+                        uint4 u = *reinterpret_cast<const uint4*>(sm.v8[vs] + row * 128 + ((c ^ (row & 7)) << 4));
+                        if (row >= left || sv == 0.f) u = make_uint4(0, 0, 0, 0);   // anything may stand there
+                        // bits of bf16 2^-120 too low, times 2^120 and the scale (in two steps where that is too large)
+                        const int e = exponent_of(sv);
+                        const uint32_t up = (uint32_t)(min(e, 7) + 247) << 7, up2 = up | (up << 16);
+                        const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&up2);
+                        const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const uint32_t z = __byte_perm(us[x >> 1], 0, (x & 1) ? 0x3020 : 0x1000);
+                            const uint32_t b = ((z >> 4) & 0x07F007F0u) | (z & 0x80008000u);
+                            const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
+                            o[x] = *reinterpret_cast<const uint32_t*>(&r);
+                        }
+                        if (e > 7) {
+                            const uint32_t mo = (uint32_t)(e - 7 + 127) << 7, mo2 = mo | (mo << 16);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[x]),
+                                                                 *reinterpret_cast<const __nv_bfloat162*>(&mo2));
+                                o[x] = *reinterpret_cast<const uint32_t*>(&r);
+                            }
+                        }
+                        const bool odd = c >> 2;           // values 8.. first
+                        const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4*>(dst + row * 128 + ((first ^ (row & 7)) << 4)) = odd ? hi4 : lo4;
+                        *reinterpret_cast<uint4*>(dst + row * 128 + ((second ^ (row & 7)) << 4)) = odd ? lo4 : hi4;
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(smem_u32(&sm.v16_full[v2]));
+                    mbar_arrive(smem_u32(&sm.v8_empty[vs]));
+                }
+                cnt += p.n;
+                return true;
+            });
+        } else if (warp >= 4) {
+            // ------------------------------------------------------------------ softmax
+            const int wg = (warp - 4) >> 2, rl = (warp & 3) * 32 + lane;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t ts = tmem + lanes + 128 * wg, to = tmem + lanes + 256 + 128 * wg;
+            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag));
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            walk([&](const Piece& p) -> bool {
+                const int row = (SPLIT ? 0 : wg * kRowsTile) + rl;
+                const bool valid = row < p.rows;
+                const int seen = valid ? p.seen0 + row / G : 0;
+                const int seen_warp = p.seen0 + (row - lane) / G;      // of the warp's first row: the fewest of all
+                const int64_t gr = valid ? (p.t0 + row / G) * hq + p.head * G + row % G : 0;
+
+                // queries
+                float top = 0.f;
+                if (valid) {
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) {
+                        float x[8];
+                        load16_f32(a.q + gr * kPagedD + 8 * i, x);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+                    }
+                }
+                // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                const uint32_t ub = __float_as_uint(top);
+                const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                const float fr = a.scale_log2e * pow2f(e), inv = pow2f(-e);
+                if (!SPLIT || wg == 0) {
+                    uint8_t* hi = sm.q[SPLIT ? 0 : wg][0] + rl * kPagedD;
+                    uint8_t* lo = sm.q[SPLIT ? 0 : wg][1] + rl * kPagedD;
+#pragma unroll 2
+                    for (int i = 0; i < 8; ++i) {
+                        float x[16];
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) x[k] = 0.f;
+                        if (valid) {
+                            load16_f32(a.q + gr * kPagedD + 16 * i, x);
+                            load16_f32(a.q + gr * kPagedD + 16 * i + 8, x + 8);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t hh = 0, ll = 0;
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const float y0 = x[4 * k + 2 * z] * inv, y1 = x[4 * k + 2 * z + 1] * inv;
+                                const uint32_t u = e4m3x2(y0, y1);
+                                const float2 back = e4m3x2_f32(u);
+                                hh |= u << (16 * z);
+                                ll |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * z);
+                            }
+                            h[k] = hh;
+                            l[k] = ll;
+                        }
+                        const int at = (i ^ (rl & 7)) << 4;
+                        *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive(smem_u32(&sm.q_full[SPLIT ? 0 : wg]));
+                }
+
+                float m = valid ? ninf : 0.f, l = 0.f, le = 0.f;       // le: roundings of l
+                bool any = false;                                      // O holds something
+                bool ok = true;
+                for (int j = SPLIT ? wg : 0; j < p.n; j += SPLIT ? 2 : 1) {
+                    if (!(ok = wait(&sm.s_full[wg], (uint32_t)taken[wg] & 1u))) break;
+                    ++taken[wg];
+                    const float* sk = sm.sk[(cnt + j) % kInfo];
+                    const int key0 = (p.k0 + j) * kKT;
+                    bool hole = false;                                 // a page that is not there
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) hole |= sk[i] == 0.f;
+                    const bool masked = hole || key0 + kKT > seen_warp;
+                    const int vis = seen - key0;
+                    uint32_t pk[64];
+                    float sum = 0.f;
+                    // P of the tile against the reference maximum `ref`
+                    auto exps = [&](float ref, bool mask) {
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int part = 0; part < 4; ++part) {
+                            float x[32];
+                            tmem_ld32(ts + 32 * part, x);
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const float kscale = sk[2 * part + half];
+                                const float f = fr * kscale;
+#pragma unroll
+                                for (int i = 16 * half; i < 16 * half + 16; i += 2) {
+                                    float x0 = fmaf(x[i], f, -ref), x1 = fmaf(x[i + 1], f, -ref);
+                                    if (mask) {
+                                        x0 = (32 * part + i < vis && kscale != 0.f) ? x0 : ninf;
+                                        x1 = (32 * part + i + 1 < vis && kscale != 0.f) ? x1 : ninf;
+                                    }
+                                    x0 = ex2(x0);
+                                    x1 = ex2(x1);
+                                    s0 += x0;
+                                    s1 += x1;
+                                    pk[16 * part + i / 2] = pack_bf16(x0, x1);
+                                }
+                            }
+                        }
+                        sum = s0 + s1;
+                    };
+                    bool high = m == ninf;
+                    if (!__any_sync(0xffffffffu, high)) {
+                        if (masked) exps(m, true);
+                        else exps(m, false);
+                        high = sum > kTrigger;
+                    }
+                    if (__any_sync(0xffffffffu, high)) {
+                        float mt = ninf;
+#pragma unroll
+                        for (int part = 0; part < 4; ++part) {
+                            float x[32];
+                            tmem_ld32(ts + 32 * part, x);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float kscale = sk[2 * part + (i >> 4)];
+                                const float y = x[i] * (fr * kscale);
+                                mt = fmaxf(mt, (32 * part + i < vis && kscale != 0.f) ? y : ninf);
+                            }
+                        }
+                        mt = fmaxf(mt, m);
+                        const float al = m == mt ? 1.f : ex2(m - mt);
+                        m = mt;
+                        l *= al;
+                        le *= al;
+                        if (any) {
+#pragma unroll
+                            for (int part = 0; part < 4; ++part) {
+                                float x[32];
+                                tmem_ld32(to + 32 * part, x);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) x[i] *= al;
+                                tmem_st32(to + 32 * part, x);
+                            }
+                        }
+                        exps(m == ninf ? 0.f : m, true);
+                    }
+                    any = true;
+                    {
+                        const float d = sum - le, t = l + d;
+                        le = (t - l) - d;
+                        l = t;
+                    }
+                    tmem_st32_u32(ts, pk);
+                    tmem_st32_u32(ts + 32, pk + 32);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sm.p_full[wg]));
+                }
+                if (ok && any) ok = wait(&sm.o_done[wg], (uint32_t)pieces & 1u);
+                if (any) ++pieces;
+                if (!SPLIT && !ok) return false;
+                cnt += p.n;
+
+                // out, or the workspace
+                const bool whole = p.starts && p.ends;
+                float w0 = 1.f, w1 = 0.f;
+                if (SPLIT) {
+                    // join the odd tiles' part to the even tiles': 64 columns at a time through the second row block's
+                    // place; named barrier 1 holds both warpgroups together
+                    float* xch = reinterpret_cast<float*>(sm.q[1][0]) + rl * 64;
+                    const bool two = p.n > 1;
+                    if (wg == 1) sm.ml[rl] = make_float2(m, l);
+                    if (wg == 1 && two) {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            float x[32];
+                            tmem_ld32(to + 32 * part, x);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<float4*>(xch + (((8 * part + i) ^ (rl & 15)) << 2)) =
+                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        }
+                    }
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    if (wg == 0) {
+                        const float2 other = sm.ml[rl];
+                        const float M = fmaxf(m, other.x);
+                        w0 = m == ninf ? 0.f : ex2(m - M);
+                        w1 = other.x == ninf ? 0.f : ex2(other.x - M);
+                        l = (m == ninf ? l : w0 * l) + (!two ? 0.f : other.x == ninf ? other.y : w1 * other.y);
+                        if (!two) w1 = 0.f;
+                        m = M;
+                    }
+                }
+                const float inv_l = l == 0.f ? 0.f : 1.f / l;
+                const int64_t slot = ((int64_t)blockIdx.x * 2 + (p.starts ? 1 : 0)) * a.rows + row;
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {
+                    if (SPLIT && part == 2) {
+                        float* xch = reinterpret_cast<float*>(sm.q[1][0]) + rl * 64;
+                        asm volatile("bar.sync 1, 256;" ::: "memory");
+                        if (wg == 1 && p.n > 1) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float x[32];
+                                tmem_ld32(to + 64 + 32 * h, x);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    *reinterpret_cast<float4*>(xch + (((8 * h + i) ^ (rl & 15)) << 2)) =
+                                        make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            }
+                        }
+                        asm volatile("bar.sync 1, 256;" ::: "memory");
+                    }
+                    if (SPLIT && wg == 1) continue;
+                    float x[32];
+                    tmem_ld32(to + 32 * part, x);
+                    if (SPLIT) {
+                        const float* xch = reinterpret_cast<const float*>(sm.q[1][0]) + rl * 64;
+                        if (p.n > 1) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 y = *reinterpret_cast<const float4*>(xch + (((8 * (part & 1) + i) ^ (rl & 15)) << 2));
+                                x[4 * i] = w0 * x[4 * i] + w1 * y.x;
+                                x[4 * i + 1] = w0 * x[4 * i + 1] + w1 * y.y;
+                                x[4 * i + 2] = w0 * x[4 * i + 2] + w1 * y.z;
+                                x[4 * i + 3] = w0 * x[4 * i + 3] + w1 * y.w;
+                            }
+                        }
+                    }
+                    if (!valid) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] *= inv_l;
+                        store_f32<__nv_bfloat16, 32>(a.out + gr * kPagedD + 32 * part, x);
+                    } else {
+                        store_f32<float, 32>(a.part_o + slot * kPagedD + 32 * part, x);
+                    }
+                }
+                if (valid && (!SPLIT || wg == 0)) {
+                    if (whole) {
+                        if (a.lse) a.lse[gr] = l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
+                    } else {
+                        a.part_ml[slot] = make_float2(m, l);
+                    }
+                }
+                tc_fence_before();
+                if (SPLIT) {
+                    // the next piece's queries may come; both warpgroups go on, or neither
+                    if (wg == 0 && rl == 0) sm.stop = *abort_flag;
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    return sm.stop == 0;
+                }
+                return true;
+            });
+        }
+        if (tid == 64) {
+            // warp 2: what the combine pass needs to know
+            OpenSegment open{0, 0, 0, 0, 1.f};
+            walk([&](const Piece& p) -> bool {
+                if (p.starts && !p.ends) {
+                    open.t0 = p.t0;
+                    open.head = p.head;
+                    open.rows = p.rows;
+                    open.n_more = cta_of_tile(total, n_cta, base + p.seg_end - 1) - (int)blockIdx.x;
+                }
+                return true;
+            });
+            if (base + B == my_b) a.open[blockIdx.x] = open;
+        }
+        base += in_window;
+        __syncthreads();
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (*abort_flag) {
+        if (tid == 0) record_device_error(a.err, MSA_DEV_WAIT_TIMEOUT);
+        if (warp == 1 && lane == 0) {
+            umma_commit(smem_u32(&sm.drain));
+            mbar_wait_drain(smem_u32(&sm.drain), 0);
+        }
+        if (tid == 0) {
+            // leave no copy in flight: each stage's last load
+            for (int i = 0; i < kKStages; ++i)
+                if (taken[0] > i) mbar_wait_drain(smem_u32(&sm.k_full[i]), (uint32_t)((taken[0] - 1 - i) / kKStages) & 1u);
+            for (int i = 0; i < kVStages; ++i)
+                if (taken[1] > i) mbar_wait_drain(smem_u32(&sm.v8_full[i]), (uint32_t)((taken[1] - 1 - i) / kVStages) & 1u);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <bool SPLIT>
+msa_status launch(const CUtensorMap& tm, const PagedAttnArgs& a, int grid, cudaStream_t s) {
+    constexpr int smem = (int)sizeof(PromptSmem) + 1024;
+    static_assert(smem <= 232448, "shared memory");
+    static std::mutex mu;
+    static bool opted[64] = {false};
+    int dev = 0;
+    MSA_CUDA_TRY(cudaGetDevice(&dev));
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev < 0 || dev >= 64 || !opted[dev]) {
+            MSA_CUDA_TRY(cudaFuncSetAttribute(paged_prompt_kernel<SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+            if (dev >= 0 && dev < 64) opted[dev] = true;
+        }
+    }
+    paged_prompt_kernel<SPLIT><<<grid, kThreads, smem, s>>>(tm, a);
+    MSA_LAUNCH_CHECK();
+    return MSA_OK;
+}
+
+}  // namespace
+
+msa_status launch_paged_prompt(const PagedAttnArgs& a, int grid, cudaStream_t s) {
+    // the pages as rows of 128 bytes (64 two-byte elements); a box is one page of keys or of values of a head
+    CUtensorMap tm{};
+    const uint64_t dims[2] = {64, (uint64_t)(a.v.n_pages * 2 * a.v.hkv * a.v.page)};
+    const uint64_t strides[1] = {kPagedD};
+    const uint32_t box[2] = {64, (uint32_t)a.v.page};
+    MSA_RETURN_IF(make_tensor_map_bf16(&tm, a.v.pages, 2, dims, strides, box));
+    return a.rows == kRowsTile ? launch<true>(tm, a, grid, s) : launch<false>(tm, a, grid, s);
+}
+
+}  // namespace msa
