@@ -6,6 +6,7 @@ in the CUDA kernels of libmsa.so. Outputs that the caller does not pass are allo
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import numpy as np
@@ -35,8 +36,9 @@ def _ptr(t, strided: bool = False) -> int | None:
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:        # the handle alone: a torch.cuda.Stream object would cost 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -311,11 +313,11 @@ def msa_sparse_attn_split(q, mem_kv, mem_len, local_k, local_v, L: int, q_start:
 
 
 # ------------------------------------------------------------------------------------------------ paged cache
-def _on_current(who: str, **tensors) -> None:
+def _on_current(who: str, dev: int, *tensors) -> None:
     """The kernels run on the current device and read plain memory of it: anything else is refused."""
-    for name, t in tensors.items():
-        if t is not None and not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
-            raise ValueError(f"{who}: {name} is on {t.device}, not on the current CUDA device")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{who}: a tensor of shape {tuple(t.shape)} is on {t.device}, the current CUDA device is {dev}")
 
 
 def _want(who: str, name: str, t: torch.Tensor, dtype, shape) -> None:
@@ -341,7 +343,7 @@ class PagedKV:
             _want("PagedKV", "bounds", bounds, torch.bfloat16, (n_pages, hkv, 2, d))
         self.pages, self.scales, self.page_table, self.seq_len, self.bounds = pages, scales, page_table, seq_len, bounds
         self.n_seq, self.max_pages, self.page, self.hkv, self.d = n_seq, max_pages, page, hkv, d
-        self.device = pages.device
+        self.device, self._index = pages.device, pages.get_device()
         for name, t in (("scales", scales), ("page_table", page_table), ("seq_len", seq_len), ("bounds", bounds)):
             if t is not None and t.device != pages.device:
                 raise ValueError(f"PagedKV: {name} is on {t.device}, pages on {pages.device}")
@@ -359,8 +361,10 @@ class PagedKV:
                    torch.zeros(n_seq, dtype=torch.int32, device=device),
                    torch.zeros((n_pages, hkv, 2, d), dtype=torch.bfloat16, device=device) if bounds else None)
 
-    def _check(self, who: str, tok_off, x, heads: int) -> None:
-        _on_current(who, cache=self.pages, tok_off=tok_off, tokens=x)
+    def _check(self, who: str, tok_off, x, heads: int, *others) -> None:
+        if self._index < 0:
+            raise ValueError(f"{who}: the cache is on {self.device}, not on the current CUDA device")
+        _on_current(who, torch.cuda.current_device(), self.pages, tok_off, x, *others)
         if tok_off.dtype != torch.int64 or tok_off.shape != (self.n_seq + 1,):
             raise ValueError(f"{who}: tok_off must be int64 [{self.n_seq + 1}], got {tok_off.dtype} of "
                              f"{tuple(tok_off.shape)}")
@@ -373,8 +377,7 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
     """Append k, v [n_tok, hkv, d] to the cache, keys rotated to pos_offset + their place in the sequence; tok_off
     int64 [n_seq + 1] (device) splits the packed tokens, at most max_new a sequence; kv.seq_len already counts them.
     With q [n_tok, hq, d] the queries are rotated too: returns q_rot (allocated when not given), else None."""
-    kv._check("msa_paged_append", tok_off, k, kv.hkv)
-    _on_current("msa_paged_append", v=v, cos_sin=cos_sin, q=q, q_rot=q_rot)
+    kv._check("msa_paged_append", tok_off, k, kv.hkv, v, cos_sin, q, q_rot)
     _want("msa_paged_append", "v", v, k.dtype, k.shape)
     if cos_sin.dtype != torch.float32 or cos_sin.shape[1:] != (kv.d // 2, 2):
         raise ValueError(f"msa_paged_append: cos_sin must be float32 [max_pos, {kv.d // 2}, 2]")
@@ -391,6 +394,7 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
     return q_rot if q is not None else None
 
 
+@functools.lru_cache(maxsize=256)
 def page_select_workspace_size(n_tok: int, hkv: int, max_pages: int) -> int:
     n = ctypes.c_size_t(0)
     check(lib.msa_page_select_workspace_size(n_tok, hkv, max_pages, ctypes.byref(n)), "msa_page_select_workspace_size")
@@ -401,11 +405,11 @@ def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int =
     """The k pages that each new token's query heads q [n_tok, hq, d] (rotated) should attend over, by the bounds of
     the pages' keys -> sel int32 [n_tok, hkv, k], ascending page indices of the sequence, -1 where there are fewer."""
     n_tok, hq = q.shape[:2]
-    kv._check("msa_page_select", tok_off, q, hq)
+    kv._check("msa_page_select", tok_off, q, hq, sel, ws)
     if sel is None:
         sel = torch.empty((n_tok, kv.hkv, k), dtype=torch.int32, device=kv.device)
-    _on_current("msa_page_select", sel=sel, ws=ws)
-    _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
+    else:
+        _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
         ws = _ws(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages), kv.device)
     check(lib.msa_page_select(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, k, recent, _ptr(sel),
@@ -413,6 +417,7 @@ def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int =
     return sel
 
 
+@functools.lru_cache(maxsize=256)
 def paged_attn_workspace_size(n_tok: int, n_seq: int, max_new: int, hq: int, hkv: int, max_pages: int, page: int,
                               k: int = 0) -> int:
     n = ctypes.c_size_t(0)
@@ -427,15 +432,15 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     int32 [n_tok, hkv, k] over the listed pages only. Returns out [n_tok, hq, d], with lse float32 [n_tok, hq]
     (given or wanted) the pair (out, lse)."""
     n_tok, hq = q.shape[:2]
-    kv._check("msa_paged_attn", tok_off, q, hq)
+    kv._check("msa_paged_attn", tok_off, q, hq, out, lse, sel, ws)
     if out is None:
         out = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = torch.empty((n_tok, hq), dtype=torch.float32, device=kv.device)
-    _on_current("msa_paged_attn", out=out, lse=lse, sel=sel, ws=ws)
-    _want("msa_paged_attn", "out", out, q.dtype, q.shape)
+    else:
+        _want("msa_paged_attn", "out", out, q.dtype, q.shape)
     if lse is not None:
         _want("msa_paged_attn", "lse", lse, torch.float32, (n_tok, hq))
+    elif want_lse:
+        lse = torch.empty((n_tok, hq), dtype=torch.float32, device=kv.device)
     k = 0
     if sel is not None:
         k = sel.shape[-1]

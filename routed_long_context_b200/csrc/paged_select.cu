@@ -1,12 +1,26 @@
 // Picking the pages of a paged cache that a query token attends over, by the bounds of their keys.
 //
-// score(token, kv head, page) = max over the group's query heads of sum_d max(q_d lo_d, q_d hi_d): the largest
-// logit (before the scale) that any key inside the page's bounds could give. Sums are in 64 bits, so that
-// what is picked does not depend on the order of summation. The newest pages count as infinite; the k best are
-// picked, ties to the lower page, and listed in ascending order.
+//   score(token, kv head, page) = max over the group's query heads of sum_d max(q_d lo_d, q_d hi_d),
+// the largest logit (before the scale) that any key inside the page's bounds could give; the newest pages count
+// as infinite, the k best are picked, ties to the lower page, and listed in ascending order. What is picked is
+// decided by sums in 64 bits, so that it does not depend on the order of summation. Those cost 64-bit
+// operations for every page, so they are done for the pages near the border alone:
+//
+// 1. page_score_kernel: all scores in fp32 on the tensor cores. max(q lo, q hi) = min(q, 0) lo + max(q, 0) hi
+//    where lo <= hi, so the scores of 16 pages and 8 query rows are one product over 2 * 128 elements whose page
+//    operand is the bounds as they lie in memory. The products of two bf16 are exact; the sums are off by at
+//    most E = 2^-14 sum|q_d| max|bound|: each of the 16 steps adds 17 numbers and loses at most 2^-22 of the
+//    sum of magnitudes (2^-24 would be a rounding, the tensor cores may truncate), 2^-18 over 16 steps. Bound
+//    by the bytes of the bounds: 512 per page and kv head.
+// 2. page_pick_kernel: one block per (token, kv head). T = the k-th best fp32 score, by its bits from the top, two
+//    at a time (counting only: no histogram, whose counters equal leading bits would all hit). Pages above
+//    T + 2 E are in, those below T - 2 E are out, and where more than k remain those in between are summed again
+//    in 64 bits and ranked.
 #include <algorithm>
+#include <mutex>
 
 #include "kernels.cuh"
+#include "mma.cuh"
 #include "paged.cuh"
 
 namespace msa {
@@ -19,79 +33,212 @@ struct SelectArgs {
     const int64_t* tok_off;
     int max_new, G, k, recent;
     int32_t* sel;
-    unsigned long long* keys;      // [n_tok][hkv][max_pages], ordered like the scores
-    int keys_in_smem;
+    unsigned long long* rows;      // [n_tok][hkv][max_pages]: fp32 scores in a row's first half, later 64-bit keys
+    float* bmax;                   // [n_tok][hkv][max_pages], row of a sequence's first token: largest |bound| of a page
+    int chunks, token_parts;       // of the scoring grid
+    int scores_in_smem;
     int* err;
 };
 
-constexpr int kScorePages = 64;    // pages per block of the scoring kernel
+constexpr int kScorePages = 128;   // pages per block of the scoring kernel, 16 per warp
+constexpr int kGroup = 8;          // query row tiles staged together
+constexpr int kPickThreads = 256;
+constexpr int kNear = kPickThreads;            // border pages that are ranked in shared memory
+constexpr size_t kPickSmem = 200 * 1024;       // of scores; more pages are all summed in 64 bits
+constexpr float kNoPage = -3.402823466e38f;    // score of a page that is not there
 
-// Order-preserving map of a double to an unsigned integer (-0 below +0, which the score never distinguishes
-// because it adds +0 first).
-__device__ __forceinline__ unsigned long long ordered(double x) {
-    const long long b = __double_as_longlong(x);
-    return b < 0 ? ~(unsigned long long)b : (unsigned long long)b | 0x8000000000000000ull;
-}
-
-template <int G>
 __global__ void __launch_bounds__(256) page_score_kernel(const SelectArgs a) {
+    __shared__ uint4 s_q[kGroup][8][32];       // B fragments: [row tile][16-byte piece][lane]
     const PagedView& v = a.v;
-    const int64_t t = blockIdx.z;
-    const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int s = seq_of_token(a.tok_off, v.n_seq, t);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    const int s = blockIdx.x / a.chunks, chunk = blockIdx.x - s * a.chunks;
+    const int g = blockIdx.y / a.token_parts, part = blockIdx.y - g * a.token_parts;
+    const int G = a.G, hq = v.hkv * G;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     SeqSpan sp;
-    if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) || t < sp.t0 || t >= sp.t0 + sp.n_new) return;
-    const int at = sp.len - sp.n_new + (int)(t - sp.t0);
-    const int last = at >> v.shift;
-    const int p0 = blockIdx.x * kScorePages;
-    if (p0 > last || last < a.k) return;          // every visible page is picked
-    double q[G][4];
+    if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) || sp.n_new == 0) return;
+    const int n_pages = (sp.len + v.page - 1) >> v.shift;
+    const int p0 = chunk * kScorePages;
+    if (p0 >= n_pages || n_pages <= a.k) return;           // every visible page is picked
+    const int row_tiles = (sp.n_new * G + 7) / 8;
+    const int per = (row_tiles + a.token_parts - 1) / a.token_parts;
+    const int rt0 = part * per, rt1 = min(row_tiles, rt0 + per);
+    if (rt0 >= rt1) return;
+
+    // A: bounds of pages r and r + 8 of the warp's 16; the thread's 16-byte pieces are 4 i + c
+    uint4 w[2][8];
+    bool there[2];
+    float top[2];
 #pragma unroll
-    for (int h = 0; h < G; ++h)
+    for (int h = 0; h < 2; ++h) {
+        const int p = p0 + 16 * warp + 8 * h + r;
+        there[h] = false;
+        if (p < n_pages) {
+            const int32_t pid = v.table[(int64_t)s * v.max_pages + p];
+            there[h] = pid >= 0 && pid < v.n_pages;
+            if (!there[h] && c == 0) record_device_error(a.err, MSA_DEV_BAD_INDEX);
+            const uint4* b = reinterpret_cast<const uint4*>(v.bounds + ((int64_t)pid * v.hkv + g) * 2 * kPagedD) + c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            q[h][i] = (double)__bfloat162float(a.q[((t * v.hkv + g) * G + h) * kPagedD + lane * 4 + i]);
-    unsigned long long* keys = a.keys + (t * v.hkv + g) * v.max_pages;
-    for (int p = p0 + warp; p < min(p0 + kScorePages, last + 1); p += 8) {
-        const int32_t pid = v.table[(int64_t)s * v.max_pages + p];
-        double best = -INFINITY;
-        if (pid < 0 || pid >= v.n_pages) {
-            if (lane == 0) record_device_error(a.err, MSA_DEV_BAD_INDEX);
+            for (int i = 0; i < 8; ++i) w[h][i] = there[h] ? b[4 * i] : make_uint4(0, 0, 0, 0);
         } else {
-            const __nv_bfloat16* b = v.bounds + ((int64_t)pid * v.hkv + g) * 2 * kPagedD + lane * 4;
-            double lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[h][i] = make_uint4(0, 0, 0, 0);
+        }
+        if (part == 0) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u[4] = {w[h][i].x, w[h][i].y, w[h][i].z, w[h][i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+            }
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            top[h] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            if (p < n_pages && c == 0) a.bmax[(sp.t0 * v.hkv + g) * v.max_pages + p] = top[h];
+        }
+    }
+
+    for (int rt = rt0; rt < rt1; rt += kGroup) {
+        const int n_rt = min(kGroup, rt1 - rt);
+        __syncthreads();
+        if (warp < n_rt) {                                 // a warp lays out one tile of 8 query rows
+            const int row = (rt + warp) * 8 + r;
+            const bool valid = row < sp.n_new * G;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                a.q + ((sp.t0 + (valid ? row / G : 0)) * hq + g * G + (valid ? row % G : 0)) * kPagedD) + c;
+            const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                lo[i] = (double)__bfloat162float(b[i]);
-                hi[i] = (double)__bfloat162float(b[kPagedD + i]);
-            }
+                const uint4 x = valid ? src[4 * i] : make_uint4(0, 0, 0, 0);
+                uint4 neg, pos;
+                const uint32_t* xs = &x.x;
 #pragma unroll
-            for (int h = 0; h < G; ++h) {
-                double x = 0.0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x += fmax(q[h][i] * lo[i], q[h][i] * hi[i]);
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                best = fmax(best, x);
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&xs[j]);
+                    const __nv_bfloat162 lo = __hmin2(y, zero), hi = __hmax2(y, zero);
+                    (&neg.x)[j] = *reinterpret_cast<const uint32_t*>(&lo);
+                    (&pos.x)[j] = *reinterpret_cast<const uint32_t*>(&hi);
+                }
+                s_q[warp][i][lane] = neg;                  // against the minima, the first 128 elements
+                s_q[warp][4 + i][lane] = pos;
             }
         }
-        if (p > last - a.recent) best = INFINITY;
-        if (lane == 0) keys[p] = ordered(best + 0.0);
+        __syncthreads();
+        for (int t = 0; t < n_rt; ++t) {
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 b = s_q[t][i][lane];
+                const uint32_t a0[4] = {w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y};
+                const uint32_t a1[4] = {w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w};
+                mma_bf16_16816(x, a0, b.x, b.y);
+                mma_bf16_16816(x, a1, b.z, b.w);
+            }
+            // x: page r, rows 2 c and 2 c + 1; page r + 8, the same rows. The largest of a token's rows:
+            const int row = (rt + t) * 8 + 2 * c;
+            if (G == 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = p0 + 16 * warp + 8 * (i >> 1) + r, tok = row + (i & 1);
+                    if (p < n_pages && tok < sp.n_new)
+                        reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] =
+                            there[i >> 1] ? x[i] : kNoPage;
+                }
+                continue;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float y = fmaxf(x[2 * h], x[2 * h + 1]);
+                if (G >= 4) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+                if (G >= 8) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                const int p = p0 + 16 * warp + 8 * h + r, tok = row / G;
+                if (row % G == 0 && p < n_pages && tok < sp.n_new)
+                    reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] = there[h] ? y : kNoPage;
+            }
+        }
     }
 }
 
-// One block per (token, kv head): the k-th largest key by radix digits from the top, then the pages above it
-// and the first of those equal to it, in ascending order.
-constexpr int kPickThreads = 256;
+// Order-preserving maps to unsigned integers (-0 counts as +0, NaN as the least).
+__device__ __forceinline__ uint32_t ordered32(float x) {
+    if (!(x == x)) return 0;
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered32(uint32_t u) {
+    return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ unsigned long long ordered64(double x) {
+    if (!(x == x)) return 0;
+    const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
+    return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
+
+struct PickSmem {
+    int cnt[2][3][kPickThreads / 32];
+    float red[2][kPickThreads / 32];
+    int near[kNear];
+    unsigned long long key[kNear];
+    int hist[256];
+    unsigned long long prefix;
+    int want, done;
+};
+
+// Sum over the block of three counts per thread; `turn` alternates, so that one barrier a call is enough.
+__device__ __forceinline__ int3 block_count(PickSmem& sm, int turn, int x, int y, int z) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    x = __reduce_add_sync(0xffffffffu, x);
+    y = __reduce_add_sync(0xffffffffu, y);
+    z = __reduce_add_sync(0xffffffffu, z);
+    if (lane == 0) {
+        sm.cnt[turn][0][warp] = x;
+        sm.cnt[turn][1][warp] = y;
+        sm.cnt[turn][2][warp] = z;
+    }
+    __syncthreads();
+    int3 t = make_int3(0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < kPickThreads / 32; ++w) {
+        t.x += sm.cnt[turn][0][w];
+        t.y += sm.cnt[turn][1][w];
+        t.z += sm.cnt[turn][2][w];
+    }
+    return t;
+}
+
+// Calls put(place, i) for the i in [0, n) with test(i), place counting them in ascending order.
+template <typename Test, typename Put>
+__device__ __forceinline__ void compact(PickSmem& sm, int n, Test test, Put put) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int before = 0;
+    __syncthreads();
+    for (int i0 = 0, turn = 0; i0 < n; i0 += kPickThreads, turn ^= 1) {
+        const int i = i0 + tid;
+        const bool yes = i < n && test(i);
+        const unsigned m = __ballot_sync(0xffffffffu, yes);
+        if (lane == 0) sm.cnt[turn][0][warp] = __popc(m);
+        __syncthreads();
+        int at = before;
+#pragma unroll
+        for (int w = 0; w < kPickThreads / 32; ++w) {
+            const int x = sm.cnt[turn][0][w];
+            if (w < warp) at += x;
+            before += x;
+        }
+        if (yes) put(at + __popc(m & ((1u << lane) - 1)), i);
+    }
+    __syncthreads();
+}
+
 __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArgs a) {
-    extern __shared__ unsigned long long s_keys[];
-    __shared__ int hist[256];
-    __shared__ unsigned long long s_prefix;
-    __shared__ int s_want, s_done, s_run[2];
-    __shared__ int s_cnt[2][kPickThreads / 32];
+    extern __shared__ uint32_t s_score[];
+    __shared__ PickSmem sm;
     const PagedView& v = a.v;
     const int64_t t = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = a.G, hq = v.hkv * G;
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // of the scoring kernel, where there is one
     const int s = seq_of_token(a.tok_off, v.n_seq, t);
     SeqSpan sp;
     int32_t* sel = a.sel + (t * v.hkv + g) * a.k;
@@ -103,86 +250,231 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
         for (int i = tid; i < a.k; i += kPickThreads) sel[i] = i < n ? i : -1;
         return;
     }
-    const unsigned long long* keys = a.keys + (t * v.hkv + g) * v.max_pages;
-    if (a.keys_in_smem) {
-        for (int i = tid; i < n; i += kPickThreads) s_keys[i] = keys[i];
-        keys = s_keys;
-    }
-    if (tid == 0) {
-        s_prefix = 0;
-        s_want = a.k;
-        s_done = 0;
-    }
-    __syncthreads();
-    int shift = 56;
-    for (;; shift -= 8) {
-        hist[tid] = 0;
-        __syncthreads();
-        const unsigned long long prefix = s_prefix;
-        for (int i = tid; i < n; i += kPickThreads) {
-            const unsigned long long x = keys[i];
-            if (shift == 56 || (x >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(int)(x >> shift) & 255], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l holds digits 255 - 8 l .. 248 - 8 l: counts from the top
-            int c = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) c += hist[255 - 8 * lane - i];
-            int above = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, above, o);
-                if (lane >= o) above += y;
-            }
-            above -= c;
-            const int want = s_want;
-            __syncwarp();
-            if (above < want && above + c >= want) {
-                int i = 0;
-                while (above + hist[255 - 8 * lane - i] < want) above += hist[255 - 8 * lane - i++];
-                const int digit = 255 - 8 * lane - i;
-                s_prefix = prefix | ((unsigned long long)digit << shift);
-                s_want = want - above;
-                s_done = hist[digit] == want - above;        // the whole bucket is picked
-            }
-        }
-        __syncthreads();
-        if (shift == 0 || s_done) break;
-    }
-    // picked: keys whose digits so far are above the prefix, and the first s_want of those equal to it
-    const unsigned long long edge = s_prefix >> shift;
-    const int want = s_want;
-    if (tid < 2) s_run[tid] = 0;
-    __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += kPickThreads) {
-        const int i = i0 + tid;
-        const unsigned long long x = i < n ? keys[i] >> shift : 0;
-        const bool gt = i < n && x > edge, eq = i < n && x == edge;
-        const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            s_cnt[0][warp] = __popc(mg);
-            s_cnt[1][warp] = __popc(me);
-        }
-        __syncthreads();
-        int cg = s_run[0], ce = s_run[1];
-        for (int w = 0; w < warp; ++w) {
-            cg += s_cnt[0][w];
-            ce += s_cnt[1][w];
-        }
-        cg += __popc(mg & ((1u << lane) - 1));
-        ce += __popc(me & ((1u << lane) - 1));
-        if (gt || (eq && ce < want)) sel[cg + min(ce, want)] = i;
-        __syncthreads();
-        if (tid == kPickThreads - 1) {
-            s_run[0] = cg + (gt ? 1 : 0);
-            s_run[1] = ce + (eq ? 1 : 0);
-        }
-        __syncthreads();
-    }
-}
+    const int newest = max(0, n - a.recent);               // pages from here on are in
+    unsigned long long* row64 = a.rows + (t * v.hkv + g) * v.max_pages;
+    const __nv_bfloat16* q = a.q + (t * hq + g * G) * kPagedD;
 
-constexpr size_t kPickSmem = 160 * 1024;
+    // a page's score in 64 bits, by one warp
+    auto exact = [&](int p) -> unsigned long long {
+        const int32_t pid = v.table[(int64_t)s * v.max_pages + p];
+        if (pid < 0 || pid >= v.n_pages) return ordered64((double)-INFINITY);
+        const __nv_bfloat16* b = v.bounds + ((int64_t)pid * v.hkv + g) * 2 * kPagedD + lane * 4;
+        double lo[4], hi[4], best = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = (double)__bfloat162float(b[i]);
+            hi[i] = (double)__bfloat162float(b[kPagedD + i]);
+        }
+        for (int h = 0; h < G; ++h) {
+            double x = 0.0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const double y = (double)__bfloat162float(q[h * kPagedD + lane * 4 + i]);
+                x += fmax(y * lo[i], y * hi[i]);
+            }
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            best = fmax(best, x);
+        }
+        return ordered64(best);
+    };
+    // the `want` largest of keys[0 .. m), the first of equal ones: by digits of 8 bits, to the edge's bits above
+    // `shift` and the number of keys equal to it that are taken
+    auto radix = [&](const unsigned long long* keys, int m, int want, int* shift_out, unsigned long long* edge, int* ties) {
+        if (tid == 0) {
+            sm.prefix = 0;
+            sm.want = want;
+            sm.done = 0;
+        }
+        __syncthreads();
+        int shift = 56;
+        for (;; shift -= 8) {
+            sm.hist[tid] = 0;
+            __syncthreads();
+            const unsigned long long prefix = sm.prefix;
+            for (int i = tid; i < m; i += kPickThreads) {
+                const unsigned long long x = keys[i];
+                if (shift == 56 || (x >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sm.hist[(int)(x >> shift) & 255], 1);
+            }
+            __syncthreads();
+            if (warp == 0) {
+                int c = 0;                                 // lane l holds digits 255 - 8 l .. 248 - 8 l
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c += sm.hist[255 - 8 * lane - i];
+                int above = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, above, o);
+                    if (lane >= o) above += y;
+                }
+                above -= c;
+                const int need = sm.want;
+                __syncwarp();
+                if (above < need && above + c >= need) {
+                    int i = 0;
+                    while (above + sm.hist[255 - 8 * lane - i] < need) above += sm.hist[255 - 8 * lane - i++];
+                    const int digit = 255 - 8 * lane - i;
+                    sm.prefix = prefix | ((unsigned long long)digit << shift);
+                    sm.want = need - above;
+                    sm.done = sm.hist[digit] == need - above;          // the whole bucket is taken
+                }
+            }
+            __syncthreads();
+            if (shift == 0 || sm.done) break;
+        }
+        *shift_out = shift;
+        *edge = sm.prefix >> shift;
+        *ties = sm.want;
+        __syncthreads();
+    };
+    // takes the `want` best of all n keys of row64
+    auto take_from_row = [&](int want) {
+        int shift, ties;
+        unsigned long long edge;
+        radix(row64, n, want, &shift, &edge, &ties);
+        // equal keys are counted first, so that each knows its rank among them
+        int equal = 0, at = 0;
+        for (int i0 = 0, turn = 0; i0 < n; i0 += kPickThreads, turn ^= 1) {
+            const int i = i0 + tid;
+            const unsigned long long x = i < n ? row64[i] >> shift : 0;
+            const bool gt = i < n && x > edge, eq = i < n && x == edge;
+            const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
+            if (lane == 0) {
+                sm.cnt[turn][0][warp] = __popc(mg);
+                sm.cnt[turn][1][warp] = __popc(me);
+            }
+            __syncthreads();
+            int cg = at, ce = equal;
+#pragma unroll
+            for (int w = 0; w < kPickThreads / 32; ++w) {
+                const int xg = sm.cnt[turn][0][w], xe = sm.cnt[turn][1][w];
+                if (w < warp) {
+                    cg += xg;
+                    ce += xe;
+                }
+                at += xg;
+                equal += xe;
+            }
+            cg += __popc(mg & ((1u << lane) - 1));
+            ce += __popc(me & ((1u << lane) - 1));
+            if (gt || (eq && ce < ties)) sel[cg + min(ce, ties)] = i;
+        }
+    };
+
+    if (!a.scores_in_smem) {                               // the scores were not made: all pages in 64 bits
+        for (int p = warp; p < n; p += kPickThreads / 32) {
+            const unsigned long long x = p >= newest ? ~0ull : exact(p);
+            if (lane == 0) row64[p] = x;
+        }
+        __syncthreads();
+        take_from_row(a.k);
+        return;
+    }
+
+    // the scores, and how far they may be off
+    const float* score = reinterpret_cast<const float*>(row64);
+    const float* bmax = a.bmax + (sp.t0 * v.hkv + g) * v.max_pages;
+    float bm = 0.f;
+    for (int i = tid; i < n; i += kPickThreads) {
+        s_score[i] = i >= newest ? 0xFFFFFFFFu : ordered32(score[i]);
+        const float b = bmax[i];
+        bm = b <= bm ? bm : b;                             // a NaN stays
+    }
+    float qs = 0.f;
+    if (warp < G) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qs += fabsf(__bfloat162float(q[warp * kPagedD + lane * 4 + i]));
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) qs += __shfl_xor_sync(0xffffffffu, qs, o);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float b = __shfl_xor_sync(0xffffffffu, bm, o);
+        bm = b <= bm ? bm : b;
+    }
+    if (lane == 0) {
+        sm.red[0][warp] = qs;
+        sm.red[1][warp] = bm;
+    }
+    __syncthreads();
+    qs = bm = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPickThreads / 32; ++w) {
+        qs = sm.red[0][w] <= qs ? qs : sm.red[0][w];
+        bm = sm.red[1][w] <= bm ? bm : sm.red[1][w];
+    }
+    const float E = qs * bm * 6.103515625e-05f + 1e-36f;   // 2^-14, and what underflow may lose
+
+    uint32_t T = 0;                                        // the k-th largest, two bits at a time
+    for (int shift = 30, turn = 0; shift >= 0; shift -= 2, turn ^= 1) {
+        const uint32_t t1 = T | (1u << shift), t2 = T | (2u << shift), t3 = T | (3u << shift);
+        int c1 = 0, c2 = 0, c3 = 0;
+        for (int i = tid; i < n; i += kPickThreads) {
+            const uint32_t x = s_score[i];
+            c1 += x >= t1;
+            c2 += x >= t2;
+            c3 += x >= t3;
+        }
+        const int3 c = block_count(sm, turn, c1, c2, c3);
+        T = c.z >= a.k ? t3 : c.y >= a.k ? t2 : c.x >= a.k ? t1 : T;
+    }
+    const float edge = unordered32(T);
+    const bool all_new = T == 0xFFFFFFFFu;                 // the newest pages are the k best
+    const float low = edge - 2.f * E, high = edge + 2.f * E;
+    // 2 in, 1 near the border, 0 out; comparisons with NaN or infinite bounds put a page near the border
+    auto place = [&](int i) -> int {
+        const uint32_t x = s_score[i];
+        if (x == 0xFFFFFFFFu) return 2;
+        if (all_new) return 0;
+        const float y = unordered32(x);
+        if (x != 0 && y > high) return 2;
+        if (x != 0 && y < low) return 0;
+        return 1;
+    };
+    int n_in = 0, n_near = 0;
+    for (int i = tid; i < n; i += kPickThreads) {
+        const int w = place(i);
+        n_in += w == 2;
+        n_near += w == 1;
+    }
+    const int3 c = block_count(sm, 0, n_in, n_near, 0);
+    n_in = c.x;
+    n_near = c.y;
+    const int want = a.k - n_in;
+    if (n_near == want) {
+        compact(sm, n, [&](int i) { return place(i) > 0; }, [&](int at, int i) { sel[at] = i; });
+        return;
+    }
+    if (n_near <= kNear) {
+        compact(sm, n, [&](int i) { return place(i) == 1; }, [&](int at, int i) { sm.near[at] = i; });
+        for (int j = warp; j < n_near; j += kPickThreads / 32) {
+            const unsigned long long x = exact(sm.near[j]);
+            if (lane == 0) sm.key[j] = x;
+        }
+        __syncthreads();
+        if (tid < n_near) {
+            const unsigned long long x = sm.key[tid];
+            int rank = 0;
+            for (int j = 0; j < n_near; ++j) {
+                const unsigned long long y = sm.key[j];
+                rank += y > x || (y == x && j < tid);
+            }
+            s_score[sm.near[tid]] = rank < want ? 0xFFFFFFFFu : 0xFFFFFFFEu;
+        }
+        __syncthreads();
+        compact(sm, n, [&](int i) { return s_score[i] == 0xFFFFFFFFu || (s_score[i] != 0xFFFFFFFEu && place(i) == 2); },
+                [&](int at, int i) { sel[at] = i; });
+        return;
+    }
+    // many scores at the border (equal ones, or bounds without a finite error): the 64-bit keys take the row's place
+    for (int p = warp; p < n; p += kPickThreads / 32) {
+        const int w = place(p);
+        const unsigned long long x = w == 2 ? ~0ull : w == 0 ? 0ull : exact(p);
+        if (lane == 0) row64[p] = x;
+    }
+    __syncthreads();
+    take_from_row(a.k);
+}
 
 }  // namespace
 }  // namespace msa
@@ -193,7 +485,8 @@ extern "C" msa_status msa_page_select_workspace_size(int64_t n_tok, int hkv, int
     MSA_REQUIRE(bytes != nullptr, "msa_page_select_workspace_size: bytes is NULL");
     MSA_REQUIRE(n_tok >= 0 && n_tok < (int64_t)INT32_MAX / 2 && hkv > 0 && hkv <= 4096 && max_pages > 0,
                 "msa_page_select_workspace_size: bad sizes");
-    *bytes = align_up((size_t)n_tok * hkv * max_pages * sizeof(unsigned long long), 256);
+    const size_t rows = (size_t)n_tok * hkv * max_pages;
+    *bytes = align_up(rows * sizeof(unsigned long long), 256) + align_up(rows * sizeof(float), 256);
     return MSA_OK;
 }
 
@@ -217,27 +510,49 @@ extern "C" msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa
     size_t need = 0;
     MSA_RETURN_IF(msa_page_select_workspace_size(n_tok, kv->hkv, kv->max_pages, &need));
     if (ws_bytes < need) return set_error(MSA_ERR_WORKSPACE, "msa_page_select: workspace %zu < %zu", ws_bytes, need);
-    if (n_tok > 65535) return set_error(MSA_ERR_UNSUPPORTED, "msa_page_select: at most 65535 tokens a call");
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.n_tok = n_tok; a.tok_off = tok_off; a.max_new = max_new; a.k = k; a.recent = recent; a.sel = sel;
-    a.keys = static_cast<unsigned long long*>(ws);
+    a.rows = static_cast<unsigned long long*>(ws);
+    a.bmax = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                      align_up((size_t)n_tok * kv->hkv * kv->max_pages * sizeof(unsigned long long), 256));
     a.err = device_error_word();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (k < kv->max_pages) {
-        const dim3 grid((unsigned)((kv->max_pages + kScorePages - 1) / kScorePages), (unsigned)kv->hkv, (unsigned)n_tok);
-        switch (a.G) {
-            case 1: page_score_kernel<1><<<grid, 256, 0, s>>>(a); break;
-            case 2: page_score_kernel<2><<<grid, 256, 0, s>>>(a); break;
-            case 4: page_score_kernel<4><<<grid, 256, 0, s>>>(a); break;
-            default: page_score_kernel<8><<<grid, 256, 0, s>>>(a); break;
-        }
+    a.chunks = (kv->max_pages + kScorePages - 1) / kScorePages;
+    if ((int64_t)a.chunks * kv->n_seq > INT32_MAX)
+        return set_error(MSA_ERR_UNSUPPORTED, "msa_page_select: n_seq * max_pages too large");
+    size_t smem = (size_t)kv->max_pages * sizeof(uint32_t);
+    a.scores_in_smem = smem <= kPickSmem;
+    if (!a.scores_in_smem) smem = 0;
+    const bool scored = k < kv->max_pages && a.scores_in_smem;
+    if (scored) {
+        // blocks for every SM: where pages and heads do not give enough, a sequence's query rows are parted too
+        const int64_t blocks = (int64_t)a.chunks * kv->n_seq * kv->hkv;
+        const int64_t groups = ((int64_t)std::min<int64_t>(max_new, n_tok) * a.G + 8 * kGroup - 1) / (8 * kGroup);
+        a.token_parts = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 592 / std::max<int64_t>(blocks, 1), 65535 / kv->hkv}));
+        page_score_kernel<<<dim3((unsigned)(a.chunks * kv->n_seq), (unsigned)(kv->hkv * a.token_parts)), 256, 0, s>>>(a);
         MSA_LAUNCH_CHECK();
     }
-    size_t smem = (size_t)kv->max_pages * sizeof(unsigned long long);
-    a.keys_in_smem = smem <= kPickSmem;
-    if (!a.keys_in_smem) smem = 0;
-    MSA_CUDA_TRY(cudaFuncSetAttribute(page_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPickSmem));
-    page_pick_kernel<<<dim3((unsigned)n_tok, (unsigned)kv->hkv), kPickThreads, smem, s>>>(a);
-    MSA_LAUNCH_CHECK();
+    static std::mutex mu;
+    static bool opted[64] = {false};
+    int dev = 0;
+    MSA_CUDA_TRY(cudaGetDevice(&dev));
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev < 0 || dev >= 64 || !opted[dev]) {
+            MSA_CUDA_TRY(cudaFuncSetAttribute(page_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPickSmem));
+            if (dev >= 0 && dev < 64) opted[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)n_tok, (unsigned)kv->hkv);
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = scored ? 1 : 0;
+    MSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, page_pick_kernel, a));
     return MSA_OK;
 }

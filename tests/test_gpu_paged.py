@@ -299,6 +299,35 @@ def test_selection_borders_decided_in_64_bits(m, new):
     assert m.device_status() == 0
 
 
+def test_selection_of_more_pages_than_shared_memory_holds(m):
+    n, page, k = 60000, 16, 40
+    c = Cache(m, 41, [n * page], page, 1, max_pages=n)
+    off_d, _ = _offsets([1])
+    q_d, q = _queries(42, 1, 4)
+    sel = m.msa_page_select(c.kv, q_d, off_d, 1, k, 3).cpu().numpy()
+    b = c.kv.bounds[torch.from_numpy(c.table[0, :n].astype(np.int64)).cuda(), 0].double().cpu().numpy()
+    np.testing.assert_array_equal(sel[0, 0], C.pick(C.page_scores(q[0], b[:, 0], b[:, 1]), k, 3))
+    assert m.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attention_over_the_smallest_values(m, new):
+    """Keys and values below the smallest normal e4m3 number, at both ends of the scales' range."""
+    for e in (-50, -3, 50):
+        c = Cache(m, 43, [100], 16, 1)
+        c.bytes[:] = (c.bytes & 0x87)                          # sign and fraction: -7 .. 7 times 2^-9
+        c.vals = C.decode_e4m3(c.bytes)
+        c.scales[:] = 2.0 ** e
+        c.kv.pages.view(torch.uint8).copy_(torch.from_numpy(c.bytes))
+        c.kv.scales.fill_(2.0 ** e)
+        off_d, off = _offsets([new])
+        q_d, q = _queries(44, new, 4)
+        scale = 4.0 * 2.0 ** -e
+        out, lse = m.msa_paged_attn(c.kv, q_d, off_d, new, scale=scale, want_lse=True)
+        assert m.device_status() == 0
+        _check_attn(c, [new], off, q, out, lse, 4, scale)
+
+
 def test_a_list_of_the_callers_own(m):
     """Empty entries anywhere, a page named twice, one out of range, a row without any page."""
     c = Cache(m, 50, [500, 100], 32, 1)
