@@ -132,6 +132,7 @@ __device__ __forceinline__ int cta_of_tile(int64_t total, int n, int64_t x) {
 constexpr int kDecodeRows = 8;
 constexpr int kDecodeTile = 16;
 constexpr int kPromptTile = 128;
+constexpr int kPromptSeqs = 512;     // sequences per launch
 msa_status launch_paged_decode(const PagedAttnArgs& a, int grid, cudaStream_t s);
 // a.rows 128: 128-row blocks, keys shared by two warpgroups; 256: a row block of 128 each
 msa_status launch_paged_prompt(const PagedAttnArgs& a, int grid, cudaStream_t s);

@@ -128,19 +128,27 @@ extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_
     a.part_o = reinterpret_cast<float*>(w + p.o);
     a.part_ml = reinterpret_cast<float2*>(w + p.ml);
     a.open = reinterpret_cast<OpenSegment*>(w + p.open);
-    if (p.few) MSA_RETURN_IF(launch_paged_decode(a, p.grid, s));
-    else MSA_RETURN_IF(launch_paged_prompt(a, p.grid, s));
-    if (p.grid == 1) return MSA_OK;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     const int64_t rows = std::min<int64_t>(p.rows, sel ? a.G : (int64_t)max_new * a.G);
-    cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((rows + kCombineRows - 1) / kCombineRows));
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    MSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_combine_kernel, a));
+    const int step = p.few ? kv->n_seq : kPromptSeqs;
+    for (int first = 0; first < kv->n_seq; first += step) {
+        PagedAttnArgs b = a;
+        b.v.n_seq = std::min(step, kv->n_seq - first);
+        b.v.table += (int64_t)first * kv->max_pages;
+        b.v.len += first;
+        b.tok_off += first;
+        if (p.few) MSA_RETURN_IF(launch_paged_decode(b, p.grid, s));
+        else MSA_RETURN_IF(launch_paged_prompt(b, p.grid, s));
+        if (p.grid == 1) continue;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((rows + kCombineRows - 1) / kCombineRows));
+        cfg.blockDim = dim3(256);
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        MSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_combine_kernel, b));
+    }
     return MSA_OK;
 }

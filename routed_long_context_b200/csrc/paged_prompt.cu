@@ -36,7 +36,8 @@ constexpr int kThreads = 512;
 constexpr int kKT = 128;                                   // keys per tile
 constexpr int kRowsTile = 128;                             // MMA M
 constexpr int kKStages = 3, kVStages = 2, kV16Stages = 2, kInfo = 8;
-constexpr int kWin = kThreads;                             // sequences looked at together
+constexpr int kWin = kPromptSeqs;                          // sequences of a launch, a thread each
+static_assert(kWin == kThreads, "a thread per sequence");
 constexpr float kTrigger = 32768.f;                        // a tile's sum above it moves the reference maximum
 
 constexpr int kBytes8 = kKT * kPagedD;                     // a tile of K or V in 8 bits: 16 KB
@@ -47,7 +48,7 @@ struct PromptSmem {
     uint8_t k[kKStages][kBytes8];
     uint8_t v8[kVStages][kBytes8];
     uint8_t v16[kV16Stages][kBytes16];                     // [d half][key][64]
-    float sk[kInfo][8], sv[kInfo][8];                      // scales per 16 keys of a tile; sv 0: nothing there
+    alignas(16) float sk[kInfo][8], sv[kInfo][8];                      // scales per 16 keys of a tile; sv 0: nothing there
     uint64_t k_full[kKStages], k_empty[kKStages], v8_full[kVStages], v8_empty[kVStages];
     uint64_t v16_full[kV16Stages], v16_empty[kV16Stages];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
@@ -58,6 +59,7 @@ struct PromptSmem {
     int n_new[kWin], len[kWin];
     long long scan[kThreads / 32];
     float2 ml[kRowsTile];
+    float fr[kRowsTile];
 };
 
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -78,6 +80,75 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
         : "memory");
 }
 
+// 32 TMEM columns on their way into registers, which may be used after tmem_wait32
+__device__ __forceinline__ void tmem_issue32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+// two fp32 values in a register pair
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | ((uint64_t)__float_as_uint(hi) << 32);
+}
+__device__ __forceinline__ uint64_t pair_u(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void tmem_st16_u32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8_u32(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st32_u32(uint32_t taddr, const uint32_t* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -98,7 +169,7 @@ struct Piece {
     int s;                 // sequence
     int k0, n;             // first key tile, number of them
     bool starts, ends;     // holds the segment's first tile, its last
-    long long seg_end;     // one past the segment's last tile, in the window's numbers
+    long long seg_end;     // one past the segment's last tile
 };
 
 __device__ __forceinline__ int seg_tiles(int base, int n_new, int tpb, int rb) {
@@ -135,11 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     }
 
     // tiles of all sequences
-    const int n_windows = (v.n_seq + kWin - 1) / kWin;
-    auto load_window = [&](int w) -> long long {
-        const int s = w * kWin + tid;
+    long long total = 0;
+    {
         SeqSpan sp{0, 0, 0};
-        if (s < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, blockIdx.x == 0 ? a.err : nullptr);
+        if (tid < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, tid, &sp, blockIdx.x == 0 ? a.err : nullptr);
         long long x = 0;
         for (int rb = 0; rb * tpb < sp.n_new; ++rb) x += seg_tiles(sp.len - sp.n_new, sp.n_new, tpb, rb);
         x *= v.hkv;
@@ -149,13 +219,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             const long long y = __shfl_up_sync(0xffffffffu, up, o);
             if (lane >= o) up += y;
         }
-        __syncthreads();
         sm.t0[tid] = sp.t0;
         sm.n_new[tid] = sp.n_new;
         sm.len[tid] = sp.len;
         if (lane == 31) sm.scan[warp] = up;
         __syncthreads();
-        long long before = 0, total = 0;
+        long long before = 0;
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += sm.scan[i];
@@ -163,13 +232,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         }
         sm.pre[tid + 1] = before + up;
         if (tid == 0) sm.pre[0] = 0;
-        __syncthreads();
-        return total;
-    };
-    long long total = 0, first_total = 0;
-    for (int w = n_windows - 1; w >= 0; --w) {
-        first_total = load_window(w);
-        total += first_total;
     }
     constexpr int kMinTiles = SPLIT ? 2 : 1;
     const int n_cta = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
@@ -187,23 +249,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;                         // S (and P) of warpgroup w at 128 w, O at 256 + 128 w
-    const long long my_a = cta_first(total, n_cta, blockIdx.x), my_b = cta_first(total, n_cta, blockIdx.x + 1);
+    const long long A = cta_first(total, n_cta, blockIdx.x), B = cta_first(total, n_cta, blockIdx.x + 1);
 
-    long long base = 0;
     // every role's own counts, which give the ring stages and phases
     int cnt = 0;                                           // tiles of earlier pieces
     int pieces = 0;                                        // pieces (softmax: those in which the warpgroup had a tile)
-    int taken[2] = {0, 0};                                 // tiles of each softmax warpgroup
-    for (int w = 0; w < n_windows; ++w) {
-        const long long in_window = (w == 0) ? first_total : load_window(w);
-        const long long A = max(my_a - base, 0LL), B = min(my_b - base, in_window);
-        if (A >= B) {
-            base += in_window;
-            continue;
-        }
+    int loading_k = 0, loading_v = 0;                      // loader: tiles under way or in
+    {
         // the pieces of [A, B), in order; every role walks them for itself
         auto walk = [&](auto&& body) {
-            int lo = 0, n = min(kWin, v.n_seq - w * kWin);
+            int lo = 0, n = v.n_seq;
             while (n > 1) {
                 const int h = n / 2;
                 if (sm.pre[lo + h] <= A) {
@@ -231,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 p.rows = min(tpb, n_new - rb * tpb) * G;
                 p.seen0 = len - n_new + rb * tpb + 1;
                 p.len = len;
-                p.s = w * kWin + lo;
+                p.s = lo;
                 p.k0 = (int)(g - start);
                 p.n = (int)(g1 - g);
                 p.starts = g == start;
@@ -244,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 if (++head == v.hkv) {
                     head = 0;
                     if (++rb * tpb >= n_new) {
-                        if (g >= B) return;
+                        if (g >= B) return;                // there may be no further sequence
                         rb = 0;
                         do ++lo;
                         while (sm.n_new[lo] == 0);
@@ -256,6 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             }
         };
 
+        // 72 + 88 + 2 * 176 = 4 * 128 registers, what the block starts with
+        if (warp < 4) {
+        fewer_registers<72>();
         if (warp == 0) {
             // ------------------------------------------------------------------ loader
             // Lane 8 i + c looks up 16-key chunk c of tile i of a group of four tiles; the page ids of the group after
@@ -305,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         if (lane == 0) mbar_expect_tx(smem_u32(&sm.k_full[ks]), bytes);
                         __syncwarp();
                         if (first) tma_load_2d(smem_u32(sm.k[ks]) + c * 16 * kPagedD, &tm, 0, row, smem_u32(&sm.k_full[ks]));
-                        taken[0] = n + 1;                              // here: tiles whose K, V is under way
+                        loading_k = n + 1;
                         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.v8_empty[vs]), ((uint32_t)(n / kVStages) & 1u) ^ 1u, abort_flag)))
                             return false;
                         if (lane == 0) mbar_expect_tx(smem_u32(&sm.v8_full[vs]), bytes);
@@ -313,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         if (first)
                             tma_load_2d(smem_u32(sm.v8[vs]) + c * 16 * kPagedD, &tm, 0, row + v.hkv * v.page,
                                         smem_u32(&sm.v8_full[vs]));
-                        taken[1] = n + 1;
+                        loading_v = n + 1;
                     }
                     id0 = id1;
                     sk0 = sk1;
@@ -330,6 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(kRowsTile >> 4) << 24);
                 const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kPagedD >> 3) << 17) |
                                          ((uint32_t)(kRowsTile >> 4) << 24);
+                int taken[2] = {0, 0};                     // P tiles of each softmax warpgroup
                 walk([&](const Piece& p) -> bool {
                     auto issue_s = [&](int wg, int j, bool wait_k) -> bool {
                         const int n = cnt + j, ks = n % kKStages;
@@ -401,7 +460,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                     return true;
                 });
             }
+        } else if (tid == 64) {
+            // warp 2: what the combine pass needs to know
+            OpenSegment open{0, 0, 0, 0, 1.f};
+            walk([&](const Piece& p) -> bool {
+                if (p.starts && !p.ends) {
+                    open.t0 = p.t0;
+                    open.head = p.head;
+                    open.rows = p.rows;
+                    open.n_more = cta_of_tile(total, n_cta, p.seg_end - 1) - (int)blockIdx.x;
+                }
+                return true;
+            });
+            a.open[blockIdx.x] = open;
+        }
         } else if (warp >= 12) {
+            fewer_registers<88>();
             // ------------------------------------------------------------------ V to bf16
             // Thread (row y of 16, piece c of 8): 16 values of rows y, y + 16, ...; the 32 bytes go to two 16-byte places
             // of the swizzled bf16 tile, in an order that keeps the eight threads of a row on distinct banks.
@@ -454,69 +528,64 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 cnt += p.n;
                 return true;
             });
-        } else if (warp >= 4) {
+        } else {
+            more_registers<176>();
             // ------------------------------------------------------------------ softmax
             const int wg = (warp - 4) >> 2, rl = (warp & 3) * 32 + lane;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t ts = tmem + lanes + 128 * wg, to = tmem + lanes + 256 + 128 * wg;
+            uint32_t taken = 0;                            // tiles of this warpgroup
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
                 const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag));
                 if (ok) tc_fence_after();
                 return ok;
             };
             walk([&](const Piece& p) -> bool {
-                const int row = (SPLIT ? 0 : wg * kRowsTile) + rl;
+                const int row0 = (SPLIT ? 0 : wg * kRowsTile) + (warp & 3) * 32, row = row0 + lane;
                 const bool valid = row < p.rows;
                 const int seen = valid ? p.seen0 + row / G : 0;
-                const int seen_warp = p.seen0 + (row - lane) / G;      // of the warp's first row: the fewest of all
+                const int seen_warp = p.seen0 + row0 / G;              // of the warp's first row: the fewest of all
                 const int64_t gr = valid ? (p.t0 + row / G) * hq + p.head * G + row % G : 0;
 
-                // queries
-                float top = 0.f;
-                if (valid) {
+                // queries: half a warp per row, eight elements a lane; both halves' parts in 8-byte pieces
+                float fr = 0.f;
+                if (!SPLIT || wg == 0) {
+                    const int half = lane >> 4, piece = lane & 15;
+                    uint8_t* hi = sm.q[SPLIT ? 0 : wg][0];
+                    uint8_t* lo = sm.q[SPLIT ? 0 : wg][1];
 #pragma unroll 4
                     for (int i = 0; i < 16; ++i) {
+                        const int r = row0 + 2 * i + half;
                         float x[8];
-                        load16_f32(a.q + gr * kPagedD + 8 * i, x);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) x[k] = 0.f;
+                        if (r < p.rows) load16_f32(a.q + ((p.t0 + r / G) * hq + p.head * G + r % G) * kPagedD + 8 * piece, x);
+                        float top = 0.f;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
-                    }
-                }
-                // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
-                const uint32_t ub = __float_as_uint(top);
-                const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
-                const float fr = a.scale_log2e * pow2f(e), inv = pow2f(-e);
-                if (!SPLIT || wg == 0) {
-                    uint8_t* hi = sm.q[SPLIT ? 0 : wg][0] + rl * kPagedD;
-                    uint8_t* lo = sm.q[SPLIT ? 0 : wg][1] + rl * kPagedD;
-#pragma unroll 2
-                    for (int i = 0; i < 8; ++i) {
-                        float x[16];
-                        uint32_t h[4], l[4];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = 0.f;
-                        if (valid) {
-                            load16_f32(a.q + gr * kPagedD + 16 * i, x);
-                            load16_f32(a.q + gr * kPagedD + 16 * i + 8, x + 8);
-                        }
+                        for (int o = 8; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                        const uint32_t ub = __float_as_uint(top);
+                        const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                        const float inv = pow2f(-e);
+                        uint32_t h[2] = {0, 0}, l[2] = {0, 0};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            uint32_t hh = 0, ll = 0;
-#pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const float y0 = x[4 * k + 2 * z] * inv, y1 = x[4 * k + 2 * z + 1] * inv;
-                                const uint32_t u = e4m3x2(y0, y1);
-                                const float2 back = e4m3x2_f32(u);
-                                hh |= u << (16 * z);
-                                ll |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * z);
-                            }
-                            h[k] = hh;
-                            l[k] = ll;
+                            const float y0 = x[2 * k] * inv, y1 = x[2 * k + 1] * inv;
+                            const uint32_t u = e4m3x2(y0, y1);
+                            const float2 back = e4m3x2_f32(u);
+                            h[k >> 1] |= u << (16 * (k & 1));
+                            l[k >> 1] |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * (k & 1));
                         }
-                        const int at = (i ^ (rl & 7)) << 4;
-                        *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-                        *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+                        const int rr = (warp & 3) * 32 + 2 * i + half;
+                        const int at = rr * kPagedD + (((piece >> 1) ^ (rr & 7)) << 4) + 8 * (piece & 1);
+                        *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0], h[1]);
+                        *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0], l[1]);
+                        const float mine = __shfl_sync(0xffffffffu, pow2f(e), (lane & 1) * 16);
+                        if (lane >> 1 == i) fr = a.scale_log2e * mine;
                     }
+                    if (SPLIT) sm.fr[rl] = fr;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(smem_u32(&sm.q_full[SPLIT ? 0 : wg]));
                 }
@@ -525,80 +594,103 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 bool any = false;                                      // O holds something
                 bool ok = true;
                 for (int j = SPLIT ? wg : 0; j < p.n; j += SPLIT ? 2 : 1) {
-                    if (!(ok = wait(&sm.s_full[wg], (uint32_t)taken[wg] & 1u))) break;
-                    ++taken[wg];
-                    const float* sk = sm.sk[(cnt + j) % kInfo];
-                    const int key0 = (p.k0 + j) * kKT;
+                    if (!(ok = wait(&sm.s_full[wg], taken & 1u))) break;
+                    ++taken;
+                    if (SPLIT && j == 1) fr = sm.fr[rl];               // written before the products that s_full reports
+                    float f[8];                                        // logit factors, 16 columns each
                     bool hole = false;                                 // a page that is not there
+                    {
+                        const float4* sk = reinterpret_cast<const float4*>(sm.sk[(cnt + j) % kInfo]);
+                        const float4 u = sk[0], w = sk[1];
+                        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = w.x, f[5] = w.y, f[6] = w.z, f[7] = w.w;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) hole |= sk[i] == 0.f;
-                    const bool masked = hole || key0 + kKT > seen_warp;
-                    const int vis = seen - key0;
-                    uint32_t pk[64];
-                    float sum = 0.f;
-                    // P of the tile against the reference maximum `ref`
-                    auto exps = [&](float ref, bool mask) {
-                        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                        for (int part = 0; part < 4; ++part) {
-                            float x[32];
-                            tmem_ld32(ts + 32 * part, x);
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const float kscale = sk[2 * part + half];
-                                const float f = fr * kscale;
-#pragma unroll
-                                for (int i = 16 * half; i < 16 * half + 16; i += 2) {
-                                    float x0 = fmaf(x[i], f, -ref), x1 = fmaf(x[i + 1], f, -ref);
-                                    if (mask) {
-                                        x0 = (32 * part + i < vis && kscale != 0.f) ? x0 : ninf;
-                                        x1 = (32 * part + i + 1 < vis && kscale != 0.f) ? x1 : ninf;
-                                    }
-                                    x0 = ex2(x0);
-                                    x1 = ex2(x1);
-                                    s0 += x0;
-                                    s1 += x1;
-                                    pk[16 * part + i / 2] = pack_bf16(x0, x1);
-                                }
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            hole |= f[i] == 0.f;
+                            f[i] *= fr;
                         }
-                        sum = s0 + s1;
-                    };
-                    bool high = m == ninf;
-                    if (!__any_sync(0xffffffffu, high)) {
-                        if (masked) exps(m, true);
-                        else exps(m, false);
-                        high = sum > kTrigger;
                     }
-                    if (__any_sync(0xffffffffu, high)) {
-                        float mt = ninf;
+                    const int key0 = (p.k0 + j) * kKT;
+                    float sum = 0.f;
+                    bool slow = hole || key0 + kKT > seen_warp || __any_sync(0xffffffffu, m == ninf);
+                    if (!slow) {
+                        // against the reference maximum as it is
+                        uint32_t xa[32], xb[32], pk[64];
+                        const uint64_t nm = pair(-m, -m);
+                        uint64_t sum2 = 0;
+                        auto part = [&](uint32_t (&x)[32], int at) {
 #pragma unroll
-                        for (int part = 0; part < 4; ++part) {
-                            float x[32];
-                            tmem_ld32(ts + 32 * part, x);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float kscale = sk[2 * part + (i >> 4)];
-                                const float y = x[i] * (fr * kscale);
-                                mt = fmaxf(mt, (32 * part + i < vis && kscale != 0.f) ? y : ninf);
+                            for (int i = 0; i < 32; i += 2) {
+                                const float ff = f[2 * at + (i >> 4)];
+                                const uint64_t y = fma2(pair_u(x[i], x[i + 1]), pair(ff, ff), nm);
+                                const float p0 = ex2(first(y)), p1 = ex2(second(y));
+                                sum2 = add2(sum2, pair(p0, p1));
+                                pk[16 * at + i / 2] = pack_bf16(p0, p1);
                             }
+                        };
+                        tmem_issue32(ts, xa);
+                        tmem_wait32(xa);
+                        tmem_issue32(ts + 32, xb);
+                        part(xa, 0);
+                        tmem_wait32(xb);
+                        tmem_issue32(ts + 64, xa);
+                        part(xb, 1);
+                        tmem_wait32(xa);
+                        tmem_issue32(ts + 96, xb);
+                        part(xa, 2);
+                        tmem_wait32(xb);
+                        part(xb, 3);
+                        sum = first(sum2) + second(sum2);
+                        slow = __any_sync(0xffffffffu, sum > kTrigger);
+                        if (!slow) {
+                            tmem_st32_u32(ts, pk);
+                            tmem_st32_u32(ts + 32, pk + 32);
                         }
-                        mt = fmaxf(mt, m);
+                    }
+                    if (slow) {
+                        // masked tiles, and those that move the maximum: 16 columns at a time
+                        const int vis = seen - key0;
+                        const float* sk = sm.sk[(cnt + j) % kInfo];
+                        float mt = m;
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            const float ks = sk[c], ff = fr * ks;
+                            float x[16];
+                            tmem_ld16(ts + 16 * c, x);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) mt = fmaxf(mt, (16 * c + i < vis && ks != 0.f) ? x[i] * ff : ninf);
+                        }
                         const float al = m == mt ? 1.f : ex2(m - mt);
                         m = mt;
                         l *= al;
                         le *= al;
                         if (any) {
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                float x[16];
+                                tmem_ld16(to + 16 * c, x);
+                                uint32_t y[16];
 #pragma unroll
-                            for (int part = 0; part < 4; ++part) {
-                                float x[32];
-                                tmem_ld32(to + 32 * part, x);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) x[i] *= al;
-                                tmem_st32(to + 32 * part, x);
+                                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * al);
+                                tmem_st16_u32(to + 16 * c, y);
                             }
                         }
-                        exps(m == ninf ? 0.f : m, true);
+                        const float ref = m == ninf ? 0.f : m;
+                        sum = 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {                  // P overwrites columns that have been read
+                            const float ks = sk[c], ff = fr * ks;
+                            float x[16];
+                            tmem_ld16(ts + 16 * c, x);
+                            uint32_t y[8];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                x[i] = (16 * c + i < vis && ks != 0.f) ? ex2(fmaf(x[i], ff, -ref)) : 0.f;
+                                sum += x[i];
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+                            tmem_st8_u32(ts + 8 * c, y);
+                        }
                     }
                     any = true;
                     {
@@ -606,8 +698,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         le = (t - l) - d;
                         l = t;
                     }
-                    tmem_st32_u32(ts, pk);
-                    tmem_st32_u32(ts + 32, pk + 32);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     mbar_arrive(smem_u32(&sm.p_full[wg]));
@@ -710,23 +800,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 return true;
             });
         }
-        if (tid == 64) {
-            // warp 2: what the combine pass needs to know
-            OpenSegment open{0, 0, 0, 0, 1.f};
-            walk([&](const Piece& p) -> bool {
-                if (p.starts && !p.ends) {
-                    open.t0 = p.t0;
-                    open.head = p.head;
-                    open.rows = p.rows;
-                    open.n_more = cta_of_tile(total, n_cta, base + p.seg_end - 1) - (int)blockIdx.x;
-                }
-                return true;
-            });
-            if (base + B == my_b) a.open[blockIdx.x] = open;
-        }
-        base += in_window;
-        __syncthreads();
     }
+    __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (*abort_flag) {
         if (tid == 0) record_device_error(a.err, MSA_DEV_WAIT_TIMEOUT);
@@ -737,9 +812,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         if (tid == 0) {
             // leave no copy in flight: each stage's last load
             for (int i = 0; i < kKStages; ++i)
-                if (taken[0] > i) mbar_wait_drain(smem_u32(&sm.k_full[i]), (uint32_t)((taken[0] - 1 - i) / kKStages) & 1u);
+                if (loading_k > i) mbar_wait_drain(smem_u32(&sm.k_full[i]), (uint32_t)((loading_k - 1 - i) / kKStages) & 1u);
             for (int i = 0; i < kVStages; ++i)
-                if (taken[1] > i) mbar_wait_drain(smem_u32(&sm.v8_full[i]), (uint32_t)((taken[1] - 1 - i) / kVStages) & 1u);
+                if (loading_v > i) mbar_wait_drain(smem_u32(&sm.v8_full[i]), (uint32_t)((loading_v - 1 - i) / kVStages) & 1u);
         }
         __syncthreads();
     }

@@ -169,6 +169,23 @@ def test_attention_ignores_what_lies_behind_the_end(m, page, new):
     _check_attn(c, news, off, q, out, lse, 8, 1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("new", [1, 10])
+def test_attention_of_many_sequences(m, new):
+    """More sequences than any kernel looks at together, most of them short, some with nothing new."""
+    r = np.random.default_rng(5)
+    news = [int(x) for x in r.integers(0, new + 1, 1100)]
+    news[0], news[600], news[1099] = new, new, new
+    lens = [n + int(x) for n, x in zip(news, r.integers(0, 60, 1100))]
+    lens[601] = 0
+    news[601] = 0
+    c = Cache(m, 45, lens, 16, 1)
+    off_d, off = _offsets(news)
+    q_d, q = _queries(46, off[-1], 2)
+    out, lse = m.msa_paged_attn(c.kv, q_d, off_d, new, want_lse=True)
+    assert m.device_status() == 0
+    _check_attn(c, news, off, q, out, lse, 2, 1 / math.sqrt(D))
+
+
 @pytest.mark.parametrize("new", [1, 24])
 def test_attention_far_scales_and_sharp_logits(m, new):
     """Scales of neighbouring pages 2^40 apart, a softmax that one key takes, and a negative scale."""
