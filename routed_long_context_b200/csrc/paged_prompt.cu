@@ -40,6 +40,8 @@ constexpr int kWin = kPromptSeqs;                          // sequences of a lau
 static_assert(kWin == kThreads, "a thread per sequence");
 constexpr float kTrigger = 32768.f;                        // a tile's sum above it moves the reference maximum
 
+constexpr float kUnit = 1152921504606846976.f;             // 2^60, the unit in which O is kept
+
 constexpr int kBytes8 = kKT * kPagedD;                     // a tile of K or V in 8 bits: 16 KB
 constexpr int kBytes16 = 2 * kBytes8;
 
@@ -48,7 +50,8 @@ struct PromptSmem {
     uint8_t k[kKStages][kBytes8];
     uint8_t v8[kVStages][kBytes8];
     uint8_t v16[kV16Stages][kBytes16];                     // [d half][key][64]
-    alignas(16) float sk[kInfo][8], sv[kInfo][8];                      // scales per 16 keys of a tile; sv 0: nothing there
+    // per 16 keys of a tile: scale of K (0: no page there), 60 + the exponent of V's, 2^-that
+    alignas(16) float sk[kInfo][8], ev[kInfo][8], iv[kInfo][8];
     uint64_t k_full[kKStages], k_empty[kKStages], v8_full[kVStages], v8_empty[kVStages];
     uint64_t v16_full[kV16Stages], v16_empty[kV16Stages];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
@@ -59,7 +62,7 @@ struct PromptSmem {
     int n_new[kWin], len[kWin];
     long long scan[kThreads / 32];
     float2 ml[kRowsTile];
-    float fr[kRowsTile];
+    float fr[2][kRowsTile];
 };
 
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -132,23 +135,6 @@ __device__ __forceinline__ void tmem_st16_u32(uint32_t taddr, const uint32_t* v)
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st8_u32(uint32_t taddr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 __device__ __forceinline__ void tmem_st32_u32(uint32_t taddr, const uint32_t* v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -183,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     PromptSmem& sm = *reinterpret_cast<PromptSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const PagedView& v = a.v;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = a.G, hq = v.hkv * G;
+    const int G = a.G, gs = 31 - __clz(G), hq = v.hkv * G;
     const int tpb = (SPLIT ? kRowsTile : 2 * kRowsTile) / G;       // tokens of a row block
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
@@ -194,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         for (int i = 0; i < kV16Stages; ++i)
             mbar_init(smem_u32(&sm.v16_full[i]), 128), mbar_init(smem_u32(&sm.v16_empty[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sm.q_full[i]), 128);
+            mbar_init(smem_u32(&sm.q_full[i]), SPLIT ? 256 : 128);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
             mbar_init(smem_u32(&sm.p_full[i]), 128);
             mbar_init(smem_u32(&sm.o_done[i]), 1);
@@ -203,6 +189,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         sm.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+
+    const bool alloc = warp == 1;
+    if (alloc) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
     }
 
     // tiles of all sequences
@@ -237,14 +231,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     const int n_cta = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
+        if (alloc) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         return;
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
@@ -330,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                     return exists(group) ? table[((p.k0 + 4 * group + sub) * 8 + c) >> cps] : -1;
                 };
                 auto scales = [&](int group, int32_t& id, float* sk, float* sv) {
-                    *sk = *sv = 0.f;
+                    *sk = 0.f;
+                    *sv = 1.f;
                     if (id < 0 || id >= v.n_pages) {
                         if (exists(group)) record_device_error(a.err, MSA_DEV_BAD_INDEX);
                         id = -1;
@@ -356,8 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.k_empty[ks]), ((uint32_t)(n / kKStages) & 1u) ^ 1u, abort_flag)))
                             return false;
                         if (here) {
+                            const int e = exponent_of(sv0);
                             sm.sk[n % kInfo][c] = sk0;
-                            sm.sv[n % kInfo][c] = sv0;
+                            sm.ev[n % kInfo][c] = (float)(60 + e);
+                            sm.iv[n % kInfo][c] = pow2f(-60 - e);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_expect_tx(smem_u32(&sm.k_full[ks]), bytes);
@@ -383,86 +375,67 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             });
         } else if (warp == 1) {
             // ------------------------------------------------------------------ products
+            // One issuer for both warpgroups, in turns: that keeps one warpgroup's exponentials under the other's
+            // products (with an issuer each they fall into step and wait together: 3,100 + 2,500 cycles a tile).
+            // What a turn needs besides P is waited for before P is.
             if (lane == 0) {
                 // f8f6f4: e4m3 x e4m3 -> fp32, both K-major; f16: bf16 x bf16 -> fp32, V MN-major
                 const uint32_t idesc_s = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | ((uint32_t)(kRowsTile >> 4) << 24);
                 const uint32_t idesc_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kPagedD >> 3) << 17) |
                                          ((uint32_t)(kRowsTile >> 4) << 24);
-                int taken[2] = {0, 0};                     // P tiles of each softmax warpgroup
+                uint32_t turns = 0;                        // bit wg: parity of its P tiles
                 walk([&](const Piece& p) -> bool {
-                    auto issue_s = [&](int wg, int j, bool wait_k) -> bool {
-                        const int n = cnt + j, ks = n % kKStages;
-                        if (wait_k && !mbar_wait(smem_u32(&sm.k_full[ks]), (uint32_t)(n / kKStages) & 1u, abort_flag)) return false;
-                        tc_fence_after();
-                        const uint64_t kd = sw128_desc(smem_u32(sm.k[ks]));
+                    auto wait_k = [&](int n) -> bool {
+                        return mbar_wait(smem_u32(&sm.k_full[n % kKStages]), (uint32_t)(n / kKStages) & 1u, abort_flag);
+                    };
+                    auto issue_s = [&](int wg, int n, bool last) {
+                        const uint64_t qd = sw128_desc(smem_u32(sm.q[SPLIT ? 0 : wg][0]));
+                        const uint64_t kd = sw128_desc(smem_u32(sm.k[n % kKStages]));
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            const uint64_t qd = sw128_desc(smem_u32(sm.q[SPLIT ? 0 : wg][part]));
+                        for (int part = 0; part < 2; ++part)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                umma_f8(tmem + 128 * wg, qd + (uint64_t)(kk * 2), kd + (uint64_t)(kk * 2), idesc_s,
-                                        (part | kk) ? 1u : 0u);
-                        }
+                                umma_f8(tmem + 128 * wg, qd + (uint64_t)(part * (kBytes8 >> 4) + kk * 2), kd + (uint64_t)(kk * 2),
+                                        idesc_s, (part | kk) ? 1u : 0u);
                         umma_commit(smem_u32(&sm.s_full[wg]));
-                        return true;
+                        if (last) umma_commit(smem_u32(&sm.k_empty[n % kKStages]));
                     };
-                    auto issue_o = [&](int wg, int j, bool wait_v, bool fresh) -> bool {
-                        if (!mbar_wait(smem_u32(&sm.p_full[wg]), (uint32_t)taken[wg] & 1u, abort_flag)) return false;
-                        ++taken[wg];
-                        const int n = cnt + j, vs = n % kV16Stages;
-                        if (wait_v && !mbar_wait(smem_u32(&sm.v16_full[vs]), (uint32_t)(n / kV16Stages) & 1u, abort_flag)) return false;
+                    // turn i of the piece: tile i / 2 of warpgroup i % 2, or tile i, which warpgroup i % 2 has
+                    const int n_turns = SPLIT ? p.n : 2 * p.n;
+                    for (int i = 0; i < 2 && i < n_turns; ++i) {
+                        if ((!SPLIT || i == 0) && !mbar_wait(smem_u32(&sm.q_full[i]), (uint32_t)pieces & 1u, abort_flag)) return false;
+                        const int n = cnt + (SPLIT ? i : 0);
+                        if ((SPLIT || i == 0) && !wait_k(n)) return false;
+                        tc_fence_after();
+                        issue_s(i, n, SPLIT || i == 1);
+                    }
+                    for (int i = 0; i < n_turns; ++i) {
+                        const int wg = i & 1, n = cnt + (SPLIT ? i : i >> 1), vs = n % kV16Stages;
+                        const bool more = i + 2 < n_turns, last = SPLIT || wg == 1;
+                        if (SPLIT || wg == 0) {
+                            if (!mbar_wait(smem_u32(&sm.v16_full[vs]), (uint32_t)(n / kV16Stages) & 1u, abort_flag)) return false;
+                            if (more && !wait_k(SPLIT ? n + 2 : n + 1)) return false;
+                        }
+                        if (!mbar_wait(smem_u32(&sm.p_full[wg]), (turns >> wg) & 1u, abort_flag)) return false;
+                        turns ^= 1u << wg;
                         tc_fence_after();
                         const uint64_t vd = sw128_mn_desc(smem_u32(sm.v16[vs]), kKT * 128);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)     // 16 keys: 8 columns of P, 16 rows of V
-                            umma_bf16_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)),
-                                         idesc_o, (!fresh || kk) ? 1u : 0u);
-                        return true;
-                    };
-                    const uint32_t qp = (uint32_t)pieces & 1u;
-                    if (SPLIT) {
-                        if (!mbar_wait(smem_u32(&sm.q_full[0]), qp, abort_flag)) return false;
-                        for (int j = 0; j < 2 && j < p.n; ++j) {
-                            if (!issue_s(j, j, true)) return false;
-                            umma_commit(smem_u32(&sm.k_empty[(cnt + j) % kKStages]));
-                        }
-                        for (int j = 0; j < p.n; ++j) {
-                            const int wg = j & 1;
-                            if (!issue_o(wg, j, true, j < 2)) return false;
-                            umma_commit(smem_u32(&sm.v16_empty[(cnt + j) % kV16Stages]));
-                            if (j + 2 < p.n) {
-                                if (!issue_s(wg, j + 2, true)) return false;
-                                umma_commit(smem_u32(&sm.k_empty[(cnt + j + 2) % kKStages]));
-                            } else {
-                                umma_commit(smem_u32(&sm.o_done[wg]));
-                            }
-                        }
-                    } else {
-                        for (int wg = 0; wg < 2; ++wg) {
-                            if (!mbar_wait(smem_u32(&sm.q_full[wg]), qp, abort_flag)) return false;
-                            if (!issue_s(wg, 0, wg == 0)) return false;
-                        }
-                        umma_commit(smem_u32(&sm.k_empty[cnt % kKStages]));
-                        for (int j = 0; j < p.n; ++j)
-                            for (int wg = 0; wg < 2; ++wg) {
-                                if (!issue_o(wg, j, wg == 0, j == 0)) return false;
-                                if (wg == 1) umma_commit(smem_u32(&sm.v16_empty[(cnt + j) % kV16Stages]));
-                                if (j + 1 < p.n) {
-                                    if (!issue_s(wg, j + 1, wg == 0)) return false;
-                                    if (wg == 1) umma_commit(smem_u32(&sm.k_empty[(cnt + j + 1) % kKStages]));
-                                } else {
-                                    umma_commit(smem_u32(&sm.o_done[wg]));
-                                }
-                            }
+                            umma_bf16_ts(tmem + 256 + 128 * wg, tmem + 128 * wg + 8 * kk, vd + (uint64_t)(kk * (2048 >> 4)), idesc_o,
+                                         (i > 1 || kk) ? 1u : 0u);
+                        if (more) issue_s(wg, SPLIT ? n + 2 : n + 1, last);
+                        else umma_commit(smem_u32(&sm.o_done[wg]));
+                        if (last) umma_commit(smem_u32(&sm.v16_empty[vs]));
                     }
                     cnt += p.n;
                     ++pieces;
                     return true;
                 });
             }
-        } else if (tid == 64) {
-            // warp 2: what the combine pass needs to know
-            OpenSegment open{0, 0, 0, 0, 1.f};
+        } else if (tid == 96) {
+            // what the combine pass needs to know
+            OpenSegment open{0, 0, 0, 0, kUnit};
             walk([&](const Piece& p) -> bool {
                 if (p.starts && !p.ends) {
                     open.t0 = p.t0;
@@ -483,43 +456,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             walk([&](const Piece& p) -> bool {
                 for (int j = 0; j < p.n; ++j) {
                     const int n = cnt + j, vs = n % kVStages, v2 = n % kV16Stages;
-                    if (!mbar_wait(smem_u32(&sm.v8_full[vs]), (uint32_t)(n / kVStages) & 1u, abort_flag)) return false;
-                    if (!mbar_wait(smem_u32(&sm.v16_empty[v2]), ((uint32_t)(n / kV16Stages) & 1u) ^ 1u, abort_flag)) return false;
+                    const bool in = mbar_wait(smem_u32(&sm.v8_full[vs]), (uint32_t)(n / kVStages) & 1u, abort_flag) &&
+                                    mbar_wait(smem_u32(&sm.v16_empty[v2]), ((uint32_t)(n / kV16Stages) & 1u) ^ 1u, abort_flag);
+                    if (!__all_sync(0xffffffffu, in)) return false;
                     const int left = p.len - (p.k0 + j) * kKT;         // keys of the tile that the sequence has
                     uint8_t* dst = sm.v16[v2] + (c >> 2) * (kKT * 128);
-                    const int first = 2 * (c & 3) + (c >> 2), second = first ^ 1;
+                    const int odd = c >> 2;                            // values 8 .. 15 are written first
+                    uint4 u[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int row = 16 * i + y;
-                        const float sv = sm.sv[n % kInfo][i];
-                        uint4 u = *reinterpret_cast<const uint4*>(sm.v8[vs] + row * 128 + ((c ^ (row & 7)) << 4));
-                        if (row >= left || sv == 0.f) u = make_uint4(0, 0, 0, 0);   // anything may stand there
-                        // bits of bf16 2^-120 too low, times 2^120 and the scale (in two steps where that is too large)
-                        const int e = exponent_of(sv);
-                        const uint32_t up = (uint32_t)(min(e, 7) + 247) << 7, up2 = up | (up << 16);
-                        const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&up2);
-                        const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+                        u[i] = *reinterpret_cast<const uint4*>(sm.v8[vs] + row * 128 + ((c ^ (row & 7)) << 4));
+                    }
+                    const bool hole = left < kKT || sm.sk[n % kInfo][lane & 7] == 0.f;
+                    if (__any_sync(0xffffffffu, hole)) {               // anything may stand where no key is
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (16 * i + y >= left || sm.sk[n % kInfo][i] == 0.f) u[i] = make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = 16 * i + y;
+                        const uint32_t us[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
                         uint32_t o[8];
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const uint32_t z = __byte_perm(us[x >> 1], 0, (x & 1) ? 0x3020 : 0x1000);
-                            const uint32_t b = ((z >> 4) & 0x07F007F0u) | (z & 0x80008000u);
-                            const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
-                            o[x] = *reinterpret_cast<const uint32_t*>(&r);
+                        for (int x = 0; x < 4; ++x) {
+                            // high and low bytes of four bf16, sign and 0000eee, emmm0000: 2^-120 times the values
+                            const uint32_t h = (us[x] & 0x80808080u) | ((us[x] >> 4) & 0x07070707u);
+                            const uint32_t l = (us[x] << 4) & 0xF0F0F0F0u;
+                            o[2 * x] = __byte_perm(l, h, 0x5140);
+                            o[2 * x + 1] = __byte_perm(l, h, 0x7362);
                         }
-                        if (e > 7) {
-                            const uint32_t mo = (uint32_t)(e - 7 + 127) << 7, mo2 = mo | (mo << 16);
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&o[x]),
-                                                                 *reinterpret_cast<const __nv_bfloat162*>(&mo2));
-                                o[x] = *reinterpret_cast<const uint32_t*>(&r);
-                            }
-                        }
-                        const bool odd = c >> 2;           // values 8.. first
                         const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
-                        *reinterpret_cast<uint4*>(dst + row * 128 + ((first ^ (row & 7)) << 4)) = odd ? hi4 : lo4;
-                        *reinterpret_cast<uint4*>(dst + row * 128 + ((second ^ (row & 7)) << 4)) = odd ? lo4 : hi4;
+                        const int at = ((2 * (c & 3) + odd) ^ (row & 7)) << 4;
+                        *reinterpret_cast<uint4*>(dst + row * 128 + at) = odd ? hi4 : lo4;
+                        *reinterpret_cast<uint4*>(dst + row * 128 + (at ^ 16)) = odd ? lo4 : hi4;
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(smem_u32(&sm.v16_full[v2]));
@@ -543,51 +514,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             walk([&](const Piece& p) -> bool {
                 const int row0 = (SPLIT ? 0 : wg * kRowsTile) + (warp & 3) * 32, row = row0 + lane;
                 const bool valid = row < p.rows;
-                const int seen = valid ? p.seen0 + row / G : 0;
-                const int seen_warp = p.seen0 + row0 / G;              // of the warp's first row: the fewest of all
-                const int64_t gr = valid ? (p.t0 + row / G) * hq + p.head * G + row % G : 0;
+                const int seen = valid ? p.seen0 + (row >> gs) : 0;
+                const int seen_warp = p.seen0 + (row0 >> gs);              // of the warp's first row: the fewest of all
+                const int64_t gr = valid ? (p.t0 + (row >> gs)) * hq + p.head * G + (row & (G - 1)) : 0;
 
-                // queries: half a warp per row, eight elements a lane; both halves' parts in 8-byte pieces
-                float fr = 0.f;
-                if (!SPLIT || wg == 0) {
+                // queries: half a warp per row, eight elements a lane, the two parts in 8-byte pieces; of a shared row block
+                // each warpgroup does half
+                {
                     const int half = lane >> 4, piece = lane & 15;
                     uint8_t* hi = sm.q[SPLIT ? 0 : wg][0];
                     uint8_t* lo = sm.q[SPLIT ? 0 : wg][1];
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = row0 + 2 * i + half;
-                        float x[8];
+                    const int first = (warp & 3) * 32 + (SPLIT ? 16 * wg : 0);
+                    constexpr int kIter = SPLIT ? 8 : 16;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < kIter; i0 += 8) {
+                        uint4 x[8];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) x[k] = 0.f;
-                        if (r < p.rows) load16_f32(a.q + ((p.t0 + r / G) * hq + p.head * G + r % G) * kPagedD + 8 * piece, x);
-                        float top = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
-#pragma unroll
-                        for (int o = 8; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
-                        const uint32_t ub = __float_as_uint(top);
-                        const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
-                        const float inv = pow2f(-e);
-                        uint32_t h[2] = {0, 0}, l[2] = {0, 0};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float y0 = x[2 * k] * inv, y1 = x[2 * k + 1] * inv;
-                            const uint32_t u = e4m3x2(y0, y1);
-                            const float2 back = e4m3x2_f32(u);
-                            h[k >> 1] |= u << (16 * (k & 1));
-                            l[k >> 1] |= e4m3x2(y0 - back.x, y1 - back.y) << (16 * (k & 1));
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = (SPLIT ? 0 : wg * kRowsTile) + first + 2 * (i0 + i) + half;
+                            x[i] = make_uint4(0, 0, 0, 0);
+                            if (r < p.rows)
+                                x[i] = *reinterpret_cast<const uint4*>(
+                                    a.q + ((p.t0 + (r >> gs)) * hq + p.head * G + (r & (G - 1))) * kPagedD + 8 * piece);
                         }
-                        const int rr = (warp & 3) * 32 + 2 * i + half;
-                        const int at = rr * kPagedD + (((piece >> 1) ^ (rr & 7)) << 4) + 8 * (piece & 1);
-                        *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0], h[1]);
-                        *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0], l[1]);
-                        const float mine = __shfl_sync(0xffffffffu, pow2f(e), (lane & 1) * 16);
-                        if (lane >> 1 == i) fr = a.scale_log2e * mine;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                            const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(u);
+                            const __nv_bfloat162 t2 = __hmax2(__hmax2(__habs2(b[0]), __habs2(b[1])), __hmax2(__habs2(b[2]), __habs2(b[3])));
+                            float top = fmaxf(__low2float(t2), __high2float(t2));
+#pragma unroll
+                            for (int o = 8; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                            const uint32_t ub = __float_as_uint(top);
+                            const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                            const float inv = pow2f(-e);
+                            uint32_t h[4], l[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __half2 y = __floats2half2_rn(__uint_as_float(u[k] << 16) * inv,
+                                                                    __uint_as_float(u[k] & 0xFFFF0000u) * inv);
+                                h[k] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                                const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h[k], __NV_E4M3);
+                                l[k] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(
+                                    __hsub2(y, *reinterpret_cast<const __half2*>(&back)), __NV_SATFINITE, __NV_E4M3);
+                            }
+                            const int rr = first + 2 * (i0 + i) + half;
+                            const int at = rr * kPagedD + (((piece >> 1) ^ (rr & 7)) << 4) + 8 * (piece & 1);
+                            *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+                            *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+                            if (piece == 0) sm.fr[SPLIT ? 0 : wg][rr] = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : a.scale_log2e * pow2f(e);
+                        }
                     }
-                    if (SPLIT) sm.fr[rl] = fr;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive(smem_u32(&sm.q_full[SPLIT ? 0 : wg]));
+                    __syncwarp();
                 }
 
                 float m = valid ? ninf : 0.f, l = 0.f, le = 0.f;       // le: roundings of l
@@ -596,11 +577,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 for (int j = SPLIT ? wg : 0; j < p.n; j += SPLIT ? 2 : 1) {
                     if (!(ok = wait(&sm.s_full[wg], taken & 1u))) break;
                     ++taken;
-                    if (SPLIT && j == 1) fr = sm.fr[rl];               // written before the products that s_full reports
+                    const float fr = sm.fr[SPLIT ? 0 : wg][rl];        // written before the products that s_full reports
+                    const int info = (cnt + j) % kInfo;
                     float f[8];                                        // logit factors, 16 columns each
                     bool hole = false;                                 // a page that is not there
                     {
-                        const float4* sk = reinterpret_cast<const float4*>(sm.sk[(cnt + j) % kInfo]);
+                        const float4* sk = reinterpret_cast<const float4*>(sm.sk[info]);
                         const float4 u = sk[0], w = sk[1];
                         f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = w.x, f[5] = w.y, f[6] = w.z, f[7] = w.w;
 #pragma unroll
@@ -611,20 +593,66 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                     }
                     const int key0 = (p.k0 + j) * kKT;
                     float sum = 0.f;
-                    bool slow = hole || key0 + kKT > seen_warp || __any_sync(0xffffffffu, m == ninf);
+                    // a new reference maximum: of sum and O
+                    auto move_max = [&](float mt) {
+                        const float al = m == mt ? 1.f : ex2(m - mt);
+                        m = mt;
+                        l *= al;
+                        le *= al;
+                        if (any) {
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t x[32];
+                                tmem_issue32(to + 32 * c, x);
+                                tmem_wait32(x);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
+                                tmem_st32_u32(to + 32 * c, x);
+                            }
+                        }
+                    };
+                    bool slow = hole || key0 + kKT > seen_warp;
                     if (!slow) {
-                        // against the reference maximum as it is
                         uint32_t xa[32], xb[32], pk[64];
-                        const uint64_t nm = pair(-m, -m);
-                        uint64_t sum2 = 0;
+                        if (__any_sync(0xffffffffu, m == ninf)) {      // the row's first keys
+                            float mt = m;
+                            auto part = [&](uint32_t (&x)[32], int at) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) mt = fmaxf(mt, __uint_as_float(x[i]) * f[2 * at + (i >> 4)]);
+                            };
+                            tmem_issue32(ts, xa);
+                            tmem_wait32(xa);
+                            tmem_issue32(ts + 32, xb);
+                            part(xa, 0);
+                            tmem_wait32(xb);
+                            tmem_issue32(ts + 64, xa);
+                            part(xb, 1);
+                            tmem_wait32(xa);
+                            tmem_issue32(ts + 96, xb);
+                            part(xa, 2);
+                            tmem_wait32(xb);
+                            part(xb, 3);
+                            move_max(mt);
+                        }
+                        // against the reference maximum as it is; V's scale goes into P's exponent
+                        const float ref = m == ninf ? 0.f : m;
+                        const float4* evs = reinterpret_cast<const float4*>(sm.ev[info]);
+                        const float4* ivs = reinterpret_cast<const float4*>(sm.iv[info]);
+                        const float4 e4[2] = {evs[0], evs[1]}, i4[2] = {ivs[0], ivs[1]};
                         auto part = [&](uint32_t (&x)[32], int at) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const float ff = f[2 * at + (i >> 4)];
-                                const uint64_t y = fma2(pair_u(x[i], x[i + 1]), pair(ff, ff), nm);
-                                const float p0 = ex2(first(y)), p1 = ex2(second(y));
-                                sum2 = add2(sum2, pair(p0, p1));
-                                pk[16 * at + i / 2] = pack_bf16(p0, p1);
+                            for (int h = 0; h < 2; ++h) {
+                                const int c = 2 * at + h;
+                                const float ff = f[c], nm = (&e4[c >> 2].x)[c & 3] - ref;
+                                uint64_t sum2 = 0;
+#pragma unroll
+                                for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+                                    const uint64_t y = fma2(pair_u(x[i], x[i + 1]), pair(ff, ff), pair(nm, nm));
+                                    const float p0 = ex2(first(y)), p1 = ex2(second(y));
+                                    sum2 = add2(sum2, pair(p0, p1));
+                                    pk[16 * at + i / 2] = pack_bf16(p0, p1);
+                                }
+                                sum = fmaf(first(sum2) + second(sum2), (&i4[c >> 2].x)[c & 3], sum);
                             }
                         };
                         tmem_issue32(ts, xa);
@@ -639,7 +667,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         part(xa, 2);
                         tmem_wait32(xb);
                         part(xb, 3);
-                        sum = first(sum2) + second(sum2);
                         slow = __any_sync(0xffffffffu, sum > kTrigger);
                         if (!slow) {
                             tmem_st32_u32(ts, pk);
@@ -647,49 +674,46 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         }
                     }
                     if (slow) {
-                        // masked tiles, and those that move the maximum: 16 columns at a time
+                        // masked tiles, and those that move the maximum: 32 columns at a time
                         const int vis = seen - key0;
-                        const float* sk = sm.sk[(cnt + j) % kInfo];
+                        const float* sk = sm.sk[info];
                         float mt = m;
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            const float ks = sk[c], ff = fr * ks;
-                            float x[16];
-                            tmem_ld16(ts + 16 * c, x);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t x[32];
+                            tmem_issue32(ts + 32 * c, x);
+                            tmem_wait32(x);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) mt = fmaxf(mt, (16 * c + i < vis && ks != 0.f) ? x[i] * ff : ninf);
-                        }
-                        const float al = m == mt ? 1.f : ex2(m - mt);
-                        m = mt;
-                        l *= al;
-                        le *= al;
-                        if (any) {
-#pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
-                                float x[16];
-                                tmem_ld16(to + 16 * c, x);
-                                uint32_t y[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(x[i] * al);
-                                tmem_st16_u32(to + 16 * c, y);
+                            for (int i = 0; i < 32; ++i) {
+                                const float ks = sk[2 * c + (i >> 4)];
+                                mt = fmaxf(mt, (32 * c + i < vis && ks != 0.f) ? __uint_as_float(x[i]) * (fr * ks) : ninf);
                             }
                         }
+                        move_max(mt);
                         const float ref = m == ninf ? 0.f : m;
                         sum = 0.f;
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {                  // P overwrites columns that have been read
-                            const float ks = sk[c], ff = fr * ks;
-                            float x[16];
-                            tmem_ld16(ts + 16 * c, x);
-                            uint32_t y[8];
+                        for (int c = 0; c < 4; ++c) {                  // P overwrites columns that have been read
+                            uint32_t x[32], y[16];
+                            tmem_issue32(ts + 32 * c, x);
+                            tmem_wait32(x);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                x[i] = (16 * c + i < vis && ks != 0.f) ? ex2(fmaf(x[i], ff, -ref)) : 0.f;
-                                sum += x[i];
+                            for (int h = 0; h < 2; ++h) {
+                                const float ks = sk[2 * c + h], ff = fr * ks, nm = sm.ev[info][2 * c + h] - ref;
+                                float part = 0.f;
+#pragma unroll
+                                for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+                                    float q[2];
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k) {
+                                        q[k] = (32 * c + i + k < vis && ks != 0.f) ? ex2(fmaf(__uint_as_float(x[i + k]), ff, nm)) : 0.f;
+                                        part += q[k];
+                                    }
+                                    y[i / 2] = pack_bf16(q[0], q[1]);
+                                }
+                                sum = fmaf(part, sm.iv[info][2 * c + h], sum);
                             }
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) y[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-                            tmem_st8_u32(ts + 8 * c, y);
+                            tmem_st16_u32(ts + 16 * c, y);
                         }
                     }
                     any = true;
@@ -710,10 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 // out, or the workspace
                 const bool whole = p.starts && p.ends;
                 float w0 = 1.f, w1 = 0.f;
+                float* xch = reinterpret_cast<float*>(sm.q[1][0]) + rl * 64;
                 if (SPLIT) {
                     // join the odd tiles' part to the even tiles': 64 columns at a time through the second row block's
                     // place; named barrier 1 holds both warpgroups together
-                    float* xch = reinterpret_cast<float*>(sm.q[1][0]) + rl * 64;
                     const bool two = p.n > 1;
                     if (wg == 1) sm.ml[rl] = make_float2(m, l);
                     if (wg == 1 && two) {
@@ -738,12 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         m = M;
                     }
                 }
-                const float inv_l = l == 0.f ? 0.f : 1.f / l;
-                const int64_t slot = ((int64_t)blockIdx.x * 2 + (p.starts ? 1 : 0)) * a.rows + row;
+                const float inv_l = l == 0.f ? 0.f : kUnit / l;
+                const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (p.starts ? 1 : 0)) * a.rows + row0;
+                // 32 columns of the warp's rows at a time, through the place of its queries (which no product reads any
+                // more), so that eight lanes write a row's piece
 #pragma unroll
                 for (int part = 0; part < 4; ++part) {
                     if (SPLIT && part == 2) {
-                        float* xch = reinterpret_cast<float*>(sm.q[1][0]) + rl * 64;
                         asm volatile("bar.sync 1, 256;" ::: "memory");
                         if (wg == 1 && p.n > 1) {
 #pragma unroll
@@ -761,33 +786,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                     if (SPLIT && wg == 1) continue;
                     float x[32];
                     tmem_ld32(to + 32 * part, x);
-                    if (SPLIT) {
-                        const float* xch = reinterpret_cast<const float*>(sm.q[1][0]) + rl * 64;
-                        if (p.n > 1) {
+                    if (SPLIT && p.n > 1) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 y = *reinterpret_cast<const float4*>(xch + (((8 * (part & 1) + i) ^ (rl & 15)) << 2));
-                                x[4 * i] = w0 * x[4 * i] + w1 * y.x;
-                                x[4 * i + 1] = w0 * x[4 * i + 1] + w1 * y.y;
-                                x[4 * i + 2] = w0 * x[4 * i + 2] + w1 * y.z;
-                                x[4 * i + 3] = w0 * x[4 * i + 3] + w1 * y.w;
-                            }
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 y = *reinterpret_cast<const float4*>(xch + (((8 * (part & 1) + i) ^ (rl & 15)) << 2));
+                            x[4 * i] = w0 * x[4 * i] + w1 * y.x;
+                            x[4 * i + 1] = w0 * x[4 * i + 1] + w1 * y.y;
+                            x[4 * i + 2] = w0 * x[4 * i + 2] + w1 * y.z;
+                            x[4 * i + 3] = w0 * x[4 * i + 3] + w1 * y.w;
                         }
                     }
-                    if (!valid) continue;
                     if (whole) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] *= inv_l;
-                        store_f32<__nv_bfloat16, 32>(a.out + gr * kPagedD + 32 * part, x);
-                    } else {
-                        store_f32<float, 32>(a.part_o + slot * kPagedD + 32 * part, x);
                     }
+                    uint8_t* stage = sm.q[SPLIT ? 0 : wg][part & 1] + (warp & 3) * 32 * kPagedD;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3), col = 32 * part + 4 * (lane & 7), rr = row0 + r;
+                        const float4 y = *reinterpret_cast<const float4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                        if (rr >= p.rows) continue;
+                        if (whole) {
+                            uint2 u;
+                            u.x = pack_bf16(y.x, y.y);
+                            u.y = pack_bf16(y.z, y.w);
+                            *reinterpret_cast<uint2*>(
+                                a.out + ((p.t0 + (rr >> gs)) * hq + p.head * G + (rr & (G - 1))) * kPagedD + col) = u;
+                        } else {
+                            *reinterpret_cast<float4*>(a.part_o + (slot0 + r) * kPagedD + col) = y;
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (valid && (!SPLIT || wg == 0)) {
                     if (whole) {
                         if (a.lse) a.lse[gr] = l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
                     } else {
-                        a.part_ml[slot] = make_float2(m, l);
+                        a.part_ml[slot0 + lane] = make_float2(m, l);
                     }
                 }
                 tc_fence_before();
