@@ -9,10 +9,11 @@
 // monotone: the bounds of the stored keys are the rounded bounds of the keys, and those of the older rows
 // the older bounds rounded to the new scale, so no older row is read for them.
 //
-// One block per (page that takes tokens, kv head): all of the page's new rows of K and V in registers
-// (eight threads a row, 2 x 8 values of K and of V each, the two halves of a rotate-half pair in one
-// thread), one block-wide max, one write; with queries, one more block per (page, kv head) rotates the
-// group's query heads of the same tokens. Bound by memory: each input read once, each output written once.
+// One block per page that takes tokens and K or V of a kv head, or the query heads of its group: all of the
+// page's new rows in registers (eight threads a row, 2 x 8 values each, the two halves of a rotate-half pair in
+// one thread), one block-wide maximum, one write; the bounds are taken from the rounded values, two to a
+// register. A page's blocks are neighbours in the grid, as their data is in memory. Bound by memory: each input
+// is read once, each output written once; 64 registers a thread keep 1,024 threads of loads on an SM.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -64,7 +65,7 @@ struct AppendPagedArgs {
     void* q_rot;
     int64_t n_tok;
     const int64_t* tok_off;
-    int max_new, G;
+    int max_new, G, parts;
     int per_seq;             // > 0: blocks per_seq * s .. are sequence s's pages; 0: by offsets (page_of_item)
     int64_t pos_offset;
     const float2* cs;
@@ -90,28 +91,46 @@ __device__ __forceinline__ int seq_of_item(const AppendPagedArgs& a, int64_t ite
     return lo;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* out) {
-    load16_f32(p, out);
-    if constexpr (sizeof(T) == 4) load16_f32(p + 4, out + 4);
-}
-
-// 16 elements of a row: 8 at 8 c and their rotate-half partners at 64 + 8 c
-template <typename T>
-__device__ __forceinline__ void load_pair(const T* row, int c, float* x) {
-    load8(row + 8 * c, x);
-    load8(row + 64 + 8 * c, x + 8);
-}
-
-__device__ __forceinline__ void rotate_pair(float* x, const float2* cs, int c) {
+// A thread's 16 elements of a row, 8 at 8 c and their rotate-half partners at 64 + 8 c: as they are in memory,
+// so that several rows may be on their way at few registers, and in fp32.
+template <typename T> struct Raw {
+    static constexpr int N = sizeof(T) / 2;                    // 16-byte pieces per 8 elements: 1 or 2
+    uint4 u[2 * N];
+    __device__ __forceinline__ void load(const T* row, int c) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float4 w = *reinterpret_cast<const float4*>(cs + 8 * c + i);
-        const float a0 = x[i], b0 = x[8 + i], a1 = x[i + 1], b1 = x[9 + i];
-        x[i] = fmaf(a0, w.x, -(b0 * w.y));
-        x[8 + i] = fmaf(b0, w.x, a0 * w.y);
-        x[i + 1] = fmaf(a1, w.z, -(b1 * w.w));
-        x[9 + i] = fmaf(b1, w.z, a1 * w.w);
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[h * N + i] = reinterpret_cast<const uint4*>(row + 64 * h + 8 * c)[i];
+    }
+    __device__ __forceinline__ void f32(float* x) const {
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (N == 2) {
+                    x[4 * i + j] = __uint_as_float(w[j]);
+                } else {
+                    x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                    x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                }
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void load_angles(float4* w, const float2* cs, int c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(cs + 8 * c + 2 * i);
+}
+__device__ __forceinline__ void rotate_pair(float* x, const float4* w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a0 = x[2 * i], b0 = x[8 + 2 * i], a1 = x[2 * i + 1], b1 = x[9 + 2 * i];
+        x[2 * i] = fmaf(a0, w[i].x, -(b0 * w[i].y));
+        x[8 + 2 * i] = fmaf(b0, w[i].x, a0 * w[i].y);
+        x[2 * i + 1] = fmaf(a1, w[i].z, -(b1 * w[i].w));
+        x[9 + 2 * i] = fmaf(b1, w[i].z, a1 * w[i].w);
     }
 }
 
@@ -131,35 +150,28 @@ __device__ __forceinline__ float clean_amax(float* x, bool* bad) {
     return m;
 }
 
-__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, const float* x, float inv) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint2 u;
-        const float* y = x + 8 * h;
-        u.x = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
-        u.y = e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16);
-        *reinterpret_cast<uint2*>(row + 64 * h + 8 * c) = u;
-    }
-}
-
 __device__ __forceinline__ float round_to(float x, float scale, float inv) {
     return e4m3x2_f32(e4m3x2(x * inv, 0.f)).x * scale;
 }
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 template <typename T, int PAGE>
-__global__ void __launch_bounds__(4 * PAGE) paged_append_kernel(const AppendPagedArgs a) {
+__global__ void __launch_bounds__(4 * PAGE, 1024 / (4 * PAGE)) paged_append_kernel(const AppendPagedArgs a) {
     constexpr int kThreads = 4 * PAGE, kPass = PAGE / 2, kWarps = kThreads / 32;
     const PagedView& v = a.v;
     const int tid = threadIdx.x, c = tid & 7;
     int s;
     int64_t j;
+    // the parts of a page's tokens (K, V and groups of query heads) are neighbours, as they are in memory
+    const int item = blockIdx.x / a.parts, part = blockIdx.x - item * a.parts;
     if (a.per_seq > 0) {
-        s = blockIdx.x / a.per_seq;
-        j = blockIdx.x - s * a.per_seq;
+        s = item / a.per_seq;
+        j = item - s * a.per_seq;
     } else {
         int64_t first;
-        s = seq_of_item(a, blockIdx.x, &first);
-        j = (int64_t)blockIdx.x - first;
+        s = seq_of_item(a, item, &first);
+        j = item - first;
     }
     SeqSpan sp;
     if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, tid == 0 ? a.err : nullptr)) return;
@@ -171,160 +183,165 @@ __global__ void __launch_bounds__(4 * PAGE) paged_append_kernel(const AppendPage
     const int64_t tok0 = sp.t0 + (p * PAGE + r0 - base);          // packed row of page row r0
     const int64_t pos0 = a.pos_offset + (int64_t)p * PAGE;        // position of page row 0
 
-    if ((int)blockIdx.y >= v.hkv) {
-        // the query heads of one group: rows (token, head), 8 threads each
-        const int g = blockIdx.y - v.hkv, hq = v.hkv * a.G;
-        const int rows = (r1 - r0) * a.G;
-        for (int i = tid >> 3; i < rows; i += kThreads / 8) {
-            const int r = i / a.G, h = g * a.G + i - r * a.G;
-            const int64_t off = ((tok0 + r) * hq + h) * kPagedD;
-            float x[16];
-            load_pair(static_cast<const T*>(a.q) + off, c, x);
-            const int64_t pos = pos0 + r0 + r;
-            if (pos < a.max_pos) rotate_pair(x, a.cs + pos * (kPagedD / 2), c);
-            else record_device_error(a.err, MSA_DEV_ROPE_POSITION);
-            T* out = static_cast<T*>(a.q_rot) + off;
-            store_f32<T, 8>(out + 8 * c, x);
-            store_f32<T, 8>(out + 64 + 8 * c, x + 8);
+    if (part >= 2 * v.hkv) {
+        // the query heads of one group: eight threads a row, its angles loaded once for all heads
+        constexpr int kHeads = 4 / (sizeof(T) / 2);               // in flight
+        const int g = part - 2 * v.hkv, hq = v.hkv * a.G;
+        for (int r = r0 + (tid >> 3); r < r1; r += kPass) {
+            const int64_t pos = pos0 + r, off = ((tok0 + r - r0) * hq + g * a.G) * kPagedD;
+            const T* src = static_cast<const T*>(a.q) + off;
+            T* dst = static_cast<T*>(a.q_rot) + off;
+            const bool turn = pos < a.max_pos;
+            if (!turn) record_device_error(a.err, MSA_DEV_ROPE_POSITION);
+            float4 w[4];
+            if (turn) load_angles(w, a.cs + pos * (kPagedD / 2), c);
+            for (int h0 = 0; h0 < a.G; h0 += kHeads) {
+                Raw<T> raw[kHeads];
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    if (h0 + h < a.G) raw[h].load(src + (h0 + h) * kPagedD, c);
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    if (h0 + h < a.G) {
+                        float x[16];
+                        raw[h].f32(x);
+                        if (turn) rotate_pair(x, w);
+                        T* out = dst + (h0 + h) * kPagedD + 8 * c;
+                        store_f32<T, 8>(out, x);
+                        store_f32<T, 8>(out + 64, x + 8);
+                    }
+            }
         }
         return;
     }
 
-    const int g = blockIdx.y;
+    const bool keys = part < v.hkv;
+    const int g = keys ? part : part - v.hkv;
     const int32_t pid = v.table[(int64_t)s * v.max_pages + p];
-    float xk[2][16], xv[2][16];
-    float mk = 0.f, mv = 0.f;
-    bool bad = false;
+    Raw<T> raw[2];
+    {
+        const T* src = static_cast<const T*>(keys ? a.k : a.v_in) + (tok0 * v.hkv + g) * kPagedD;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = r0 + i * kPass + (tid >> 3);
-        if (r < r1) {
-            const int64_t off = ((tok0 + r - r0) * v.hkv + g) * kPagedD;
-            load_pair(static_cast<const T*>(a.k) + off, c, xk[i]);
-            load_pair(static_cast<const T*>(a.v_in) + off, c, xv[i]);
+        for (int i = 0; i < 2; ++i) {
+            const int r = r0 + i * kPass + (tid >> 3);
+            if (r < r1) raw[i].load(src + (int64_t)(r - r0) * v.hkv * kPagedD, c);
         }
     }
     if (pid < 0 || pid >= v.n_pages) {
         if (tid == 0) record_device_error(a.err, MSA_DEV_BAD_INDEX);
         return;
     }
-    const int64_t slab = ((int64_t)pid * 2 * v.hkv + g);          // (page, K, head); V is hkv further
-    const float old_k = r0 > 0 ? v.scales[slab] : 0.f, old_v = r0 > 0 ? v.scales[slab + v.hkv] : 0.f;
+    const int64_t slab = (int64_t)pid * 2 * v.hkv + part;         // (page, K or V, head)
+    const float was = r0 > 0 ? v.scales[slab] : 0.f;
+    float x[2][16], top = 0.f;
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = r0 + i * kPass + (tid >> 3);
-        if (r < r1) {
+        if (r >= r1) continue;
+        raw[i].f32(x[i]);
+        if (keys) {
             const int64_t pos = pos0 + r;
-            if (pos < a.max_pos) rotate_pair(xk[i], a.cs + pos * (kPagedD / 2), c);
-            else record_device_error(a.err, MSA_DEV_ROPE_POSITION);
-            mk = fmaxf(mk, clean_amax(xk[i], &bad));
-            mv = fmaxf(mv, clean_amax(xv[i], &bad));
+            if (pos < a.max_pos) {
+                float4 w[4];
+                load_angles(w, a.cs + pos * (kPagedD / 2), c);
+                rotate_pair(x[i], w);
+            } else {
+                record_device_error(a.err, MSA_DEV_ROPE_POSITION);
+            }
         }
+        top = fmaxf(top, clean_amax(x[i], &bad));
     }
     if (bad) record_device_error(a.err, MSA_DEV_NONFINITE);
 
-    __shared__ float s_max[2][kWarps];
-    __shared__ float s_lo[kWarps][kPagedD], s_hi[kWarps][kPagedD];
+    __shared__ float s_max[kWarps];
+    __shared__ uint32_t s_lo[kWarps][kPagedD / 2], s_hi[kWarps][kPagedD / 2];   // fp16 pairs
     const int warp = tid >> 5, lane = tid & 31;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-        mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-    }
-    if (lane == 0) {
-        s_max[0][warp] = mk;
-        s_max[1][warp] = mv;
-    }
-    if (v.bounds) {
-        // this thread's columns over its rows, then over the four row groups of the warp
-        float lo[16], hi[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            lo[e] = __int_as_float(0x7f800000);
-            hi[e] = -lo[e];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (r0 + i * kPass + (tid >> 3) < r1) {
-                    lo[e] = fminf(lo[e], xk[i][e]);
-                    hi[e] = fmaxf(hi[e], xk[i][e]);
-                }
-#pragma unroll
-            for (int o = 8; o <= 16; o <<= 1) {
-                lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
-                hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
-            }
-        }
-        if (lane < 8) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int d = (e >> 3) * 64 + 8 * c + (e & 7);
-                s_lo[warp][d] = lo[e];
-                s_hi[warp][d] = hi[e];
-            }
-        }
-    }
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_max[warp] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        mk = fmaxf(mk, s_max[0][w]);
-        mv = fmaxf(mv, s_max[1][w]);
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_max[w]);
+    int e = scale_exponent(top);
+    if (r0 > 0) e = max(e, min(max(exponent_of(was), kScaleMin), kScaleMax));
+    const float scale = pow2f(e), inv = pow2f(-e);
+    uint8_t* rows = v.pages + slab * PAGE * kPagedD;
+    const bool bounds = keys && v.bounds;
+    uint32_t lo[8], hi[8];                                        // of this thread's columns, as fp16 pairs
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = 0x7C007C00u;
+        hi[i] = 0xFC00FC00u;
     }
-    int ek = scale_exponent(mk), ev = scale_exponent(mv);
-    if (r0 > 0) {
-        ek = max(ek, exponent_of(old_k));
-        ev = max(ev, exponent_of(old_v));
-    }
-    const float sk = pow2f(ek), ik = pow2f(-ek), sv = pow2f(ev), iv = pow2f(-ev);
-    uint8_t* pk = v.pages + slab * PAGE * kPagedD;
-    uint8_t* pv = pk + (int64_t)v.hkv * PAGE * kPagedD;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = r0 + i * kPass + (tid >> 3);
-        if (r < r1) {
-            store_e4m3(pk + r * kPagedD, c, xk[i], ik);
-            store_e4m3(pv + r * kPagedD, c, xv[i], iv);
+        if (r >= r1) continue;
+        uint32_t u[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) u[k] = e4m3x2(x[i][2 * k] * inv, x[i][2 * k + 1] * inv);
+        *reinterpret_cast<uint2*>(rows + r * kPagedD + 8 * c) = make_uint2(u[0] | (u[1] << 16), u[2] | (u[3] << 16));
+        *reinterpret_cast<uint2*>(rows + r * kPagedD + 64 + 8 * c) = make_uint2(u[4] | (u[5] << 16), u[6] | (u[7] << 16));
+        if (bounds) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u[k], __NV_E4M3);
+                const __half2 y = *reinterpret_cast<const __half2*>(&h);
+                lo[k] = as_u32(__hmin2(as_half2(lo[k]), y));
+                hi[k] = as_u32(__hmax2(as_half2(hi[k]), y));
+            }
         }
     }
-    if (tid == 0) {
-        v.scales[slab] = sk;
-        v.scales[slab + v.hkv] = sv;
-    }
+    if (tid == 0) v.scales[slab] = scale;
     // older rows of a scale that grows: rounded again, 16 values a thread
-    if (r0 > 0) {
+    if (r0 > 0 && scale != was) {
+        const float ratio = was * inv;
+        uint4* old = reinterpret_cast<uint4*>(rows);
+        for (int i = tid; i < r0 * (kPagedD / 16); i += kThreads) {
+            uint4 u = old[i];
+            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-            const float was = part ? old_v : old_k, now = part ? sv : sk;
-            if (now == was) continue;
-            const float ratio = was * (part ? iv : ik);
-            uint4* rows = reinterpret_cast<uint4*>(part ? pv : pk);
-            for (int i = tid; i < r0 * (kPagedD / 16); i += kThreads) {
-                uint4 u = rows[i];
-                uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 lo = e4m3x2_f32(w[e] & 0xFFFFu), hi = e4m3x2_f32(w[e] >> 16);
-                    w[e] = e4m3x2(lo.x * ratio, lo.y * ratio) | (e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
-                }
-                rows[i] = u;
+            for (int k = 0; k < 4; ++k) {
+                const float2 y = e4m3x2_f32(w[k] & 0xFFFFu), z = e4m3x2_f32(w[k] >> 16);
+                w[k] = e4m3x2(y.x * ratio, y.y * ratio) | (e4m3x2(z.x * ratio, z.y * ratio) << 16);
             }
+            old[i] = u;
         }
     }
-    if (v.bounds) {
-        for (int d = tid; d < kPagedD; d += kThreads) {
-            float lo = s_lo[0][d], hi = s_hi[0][d];
+    if (!bounds) return;
+    // over the four rows of a warp's eight threads each, then over the warps
 #pragma unroll
-            for (int w = 1; w < kWarps; ++w) {
-                lo = fminf(lo, s_lo[w][d]);
-                hi = fmaxf(hi, s_hi[w][d]);
-            }
-            __nv_bfloat16* b = v.bounds + ((int64_t)pid * v.hkv + g) * 2 * kPagedD + d;
-            if (r0 > 0) {
-                lo = fminf(lo, __bfloat162float(b[0]));
-                hi = fmaxf(hi, __bfloat162float(b[kPagedD]));
-            }
-            b[0] = __float2bfloat16_rn(round_to(lo, sk, ik));
-            b[kPagedD] = __float2bfloat16_rn(round_to(hi, sk, ik));
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+        for (int o = 8; o <= 16; o <<= 1) {
+            lo[k] = as_u32(__hmin2(as_half2(lo[k]), as_half2(__shfl_xor_sync(0xffffffffu, lo[k], o))));
+            hi[k] = as_u32(__hmax2(as_half2(hi[k]), as_half2(__shfl_xor_sync(0xffffffffu, hi[k], o))));
         }
+        if (lane < 8) {
+            s_lo[warp][(k >> 2) * 32 + 4 * c + (k & 3)] = lo[k];
+            s_hi[warp][(k >> 2) * 32 + 4 * c + (k & 3)] = hi[k];
+        }
+    }
+    __syncthreads();
+    if (tid < kPagedD / 2) {
+        __half2 l2 = as_half2(s_lo[0][tid]), h2 = as_half2(s_hi[0][tid]);
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            l2 = __hmin2(l2, as_half2(s_lo[w][tid]));
+            h2 = __hmax2(h2, as_half2(s_hi[w][tid]));
+        }
+        float2 l = __half22float2(l2), h = __half22float2(h2);
+        l = make_float2(l.x * scale, l.y * scale);
+        h = make_float2(h.x * scale, h.y * scale);
+        __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(v.bounds + ((int64_t)pid * v.hkv + g) * 2 * kPagedD) + tid;
+        if (r0 > 0) {
+            const float2 ol = __bfloat1622float2(b[0]), oh = __bfloat1622float2(b[kPagedD / 2]);
+            l = make_float2(fminf(l.x, round_to(ol.x, scale, inv)), fminf(l.y, round_to(ol.y, scale, inv)));
+            h = make_float2(fmaxf(h.x, round_to(oh.x, scale, inv)), fmaxf(h.y, round_to(oh.y, scale, inv)));
+        }
+        b[0] = __floats2bfloat162_rn(l.x, l.y);                   // exact
+        b[kPagedD / 2] = __floats2bfloat162_rn(h.x, h.y);
     }
 }
 
@@ -376,7 +393,9 @@ extern "C" msa_status msa_paged_append(const msa_paged_kv* kv, const void* k, co
         items = packed;
         a.per_seq = 0;
     }
-    const dim3 grid((unsigned)items, (unsigned)(q ? 2 * kv->hkv : kv->hkv), 1);
+    a.parts = (q ? 3 : 2) * kv->hkv;
+    if (items * a.parts > INT32_MAX) return set_error(MSA_ERR_UNSUPPORTED, "msa_paged_append: too many pages a call");
+    const dim3 grid((unsigned)(items * a.parts));
     if (dt == MSA_BF16) launch_paged_append<__nv_bfloat16>(a, grid, static_cast<cudaStream_t>(stream));
     else launch_paged_append<float>(a, grid, static_cast<cudaStream_t>(stream));
     MSA_LAUNCH_CHECK();
