@@ -2,17 +2,21 @@
 // tokens over their page lists.
 //
 //   out = softmax(scale q . K) V,  up to 8 rows (token, query head) of one kv head at a time.
-// Every cached byte is read once for 4 * 8 operations at most, so the bytes bound it; what costs is turning
-// them into operands. A warp takes 16 keys at a time, transposed, on mma.sync (the 128-row tiles of
-// tcgen05.mma would be empty but for 1 to 8 rows, and want the keys' operands written back to shared memory):
-//   S^T [16 keys x 8 rows]  = K [16 x 128] Q^T         K: e4m3 -> fp16 exactly; Q: fp16 times a power of two
-//   O^T [128 x 8 rows]     += V^T [128 x 16] P^T       V: e4m3 -> bf16 exactly; P: bf16
-// so all eight columns are rows of the softmax. The order of d inside both products is free: a thread takes
-// the 16-byte pieces that it can read from shared memory without bank conflicts. Keys and values come by TMA
-// in the 128-byte swizzle, three tiles of 4 KB deep for each of the 16 warps of an SM (192 KB in flight; 44 KB
-// cover the latency). The running maximum moves only when a logit exceeds it by 2^8.
-// P carries the page's scale of V times 2^60, V stands 2^-120 too low: an e4m3 value's bits moved to a bf16's
-// place, subnormals included, need no multiplication that way.
+// Every cached byte is read once for 4 * 8 operations at most, so the bytes bound it, and what a warp spends on
+// each byte decides how near it comes. A warp takes 32 keys at a time, transposed, so that all eight columns are
+// rows of the softmax, on mma.sync with e4m3 operands, which take the cache's bytes as they are (the 128-row
+// tiles of tcgen05.mma would be empty but for 1 to 8 rows; e4m3 mma.sync m16n8k32 measured 1.88 PFLOP/s here,
+// fp16 m16n8k16 0.53):
+//   S^T [32 keys x 8 rows]  = K [32 x 128] (Qhi + Qlo)^T
+//   D   [128 x 8 rows]      = V^T [128 x 32] (Phi + Plo)^T,   O^T += D 2^(mt - m) scale(V)
+// Q is split into two e4m3 parts of a row scaled to 224..448: eight significant bits, all that bf16 has, down to
+// 2^-11 of the row's largest; what lies below is off by at most 2^-10 of the scale. P is taken against the
+// tile's own maximum mt, times 2^8, and split alike: an error of 2^-8 of the value (half a step twice, what one
+// rounding to bf16 costs), or of 2^-18 of the tile's largest for small ones. O and the sum are fp32 against a
+// maximum m that moves only when a tile exceeds it by 2^24. The order of d and of the keys inside the products
+// is free: a thread takes the 16-byte pieces that it can read from shared memory without bank conflicts, and V
+// needs no more than 4 x 4 byte transposes. Keys and values come by TMA in the 128-byte swizzle, three tiles of
+// 8 KB deep for each of the 8 warps of an SM (192 KB in flight; 44 KB cover the latency).
 #include <algorithm>
 #include <mutex>
 
@@ -28,13 +32,13 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 constexpr int kTileBytes = 2 * kDecodeTile * kPagedD;      // K and V of a tile
 constexpr int kWindow = 256;                               // sequences looked at together
-constexpr float kSlack = 8.f;
-constexpr float kUnit = 1152921504606846976.f;             // 2^60: the unit in which O is kept
+constexpr float kSlack = 24.f;
 
-struct TileInfo {
-    int key;          // first key's place in the sequence
-    int rows;         // keys that hold something; 0: nothing was loaded
-    float sk, sv;     // scales of K and of V
+struct TileInfo {     // of the tile's two halves of 16 keys
+    int key[2];       // first key's place in the sequence
+    int rows[2];      // keys that hold something; 0: nothing was loaded
+    float sk[2];      // scales of K
+    float sv[2];      // and of V
 };
 
 struct DecodeSmem {
@@ -50,24 +54,26 @@ struct DecodeSmem {
     int abort_flag;
 };
 
-__device__ __forceinline__ void mma_f16_16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+// c[4] += A [16 x 32] B [32 x 8], e4m3
+__device__ __forceinline__ void mma_e4m3_16832(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t u) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)u, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-// e4m3 bytes in the high bytes of both halves -> bf16 of 2^-120 times their values
-__device__ __forceinline__ uint32_t e4m3_high_bf16x2(uint32_t z) {
-    return ((z >> 4) & 0x07F007F0u) | (z & 0x80008000u);
+// x0, x1 as e4m3 pairs: the nearest, and the nearest to what that leaves (all within fp16's range)
+__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t* hi, uint32_t* lo) {
+    const __half2 y = __floats2half2_rn(x0, x1);
+    *hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+    const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)*hi, __NV_E4M3);
+    *lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__hsub2(y, *reinterpret_cast<const __half2*>(&back)), __NV_SATFINITE,
+                                               __NV_E4M3);
 }
 
 // Prefix sums over the block of one value per thread; returns the block's total.
@@ -95,7 +101,7 @@ __device__ __forceinline__ long long block_prefix(long long x, long long* pre, l
 }
 
 template <bool LIST>
-__global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_constant__ CUtensorMap tm,
+__global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_constant__ CUtensorMap tm,
                                                                    const PagedAttnArgs a) {
     extern __shared__ uint8_t smem_raw[];
     DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -103,7 +109,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;                 // the thread's place in a fragment
     const int G = a.G, hq = v.hkv * G, page = v.page;
-    const int per_page = page / kDecodeTile;
+    // tiles per page, or two pages per tile
+    const bool pairs = page == 16;
+    const int per_page = pairs ? 1 : page / kDecodeTile;
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
     if (tid == 0) sm.abort_flag = 0;
@@ -127,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
                             sm.scan);
     };
     long long total = 0, first_total = 0;
-    const int list_tiles = LIST ? a.k * per_page : 1;
+    const int list_tiles = !LIST ? 1 : pairs ? (a.k + 1) / 2 : a.k * per_page;
     if (LIST) {
         total = first_total = a.n_tok * v.hkv * (long long)list_tiles;
         __syncthreads();
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         return;
     }
     const long long my_a = cta_first(total, n_cta, blockIdx.x), my_b = cta_first(total, n_cta, blockIdx.x + 1);
-    OpenSegment open{0, 0, 0, 0, kUnit};
+    OpenSegment open{0, 0, 0, 0, 1.f};
 
     int it = 0;                                            // tiles this warp has taken: ring stage and phase
     long long base = 0;                                    // tiles before the window
@@ -158,18 +166,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
         const int n_win = LIST ? 0 : min(kWindow, v.n_seq - w * kWindow);
 
         // Lane l looks up tile l of the warp's next 32; they are issued one by one as ring stages come free.
-        TileInfo ti{0, 0, 0.f, 0.f};
-        int ti_row = 0;                                    // tensor-map row of the tile's first key
+        TileInfo ti;
+        int ti_row[2];                                     // tensor-map rows of the halves' first keys
         const int n_mine = (int)((B - A - warp + kWarps - 1) / kWarps);
         int issued = 0;
         auto look_up = [&]() {
-            ti = TileInfo{0, 0, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ti.key[h] = ti.rows[h] = ti_row[h] = 0;
+                ti.sk[h] = ti.sv[h] = 1.f;
+            }
             const long long g = A + warp + (long long)kWarps * (issued + lane);
             if (g >= B) return;
-            int s, p, head, row0, seen;
+            int s, head, seen, at;                         // at: the tile's number in its segment
+            long long seg = 0;
             if (LIST) {
-                const long long seg = g / list_tiles;
-                const int e = (int)(g - seg * list_tiles);
+                seg = g / list_tiles;
+                at = (int)(g - seg * list_tiles);
                 const long long t = seg / v.hkv;
                 head = (int)(seg - t * v.hkv);
                 int lo = 0, n = v.n_seq;                   // the last sequence that starts at or before t
@@ -186,14 +199,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
                 SeqSpan sp;
                 if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, a.err) || t < sp.t0 || t >= sp.t0 + sp.n_new) return;
                 seen = sp.len - sp.n_new + (int)(t - sp.t0) + 1;
-                const int li = e / per_page;
-                p = a.sel[seg * a.k + li];
-                row0 = (e - li * per_page) * kDecodeTile;
-                if (p == -1) return;
-                if (p < 0 || p >= (seen + page - 1) >> v.shift) {
-                    record_device_error(a.err, MSA_DEV_BAD_INDEX);
-                    return;
-                }
             } else {
                 int lo = 0, n = n_win;
                 while (n > 1) {
@@ -208,23 +213,53 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
                 s = w * kWindow + lo;
                 seen = sm.len[lo];
                 const int per_head = (seen + kDecodeTile - 1) / kDecodeTile;
-                const long long at = g - sm.pre[lo];
-                head = (int)(at / per_head);
-                const int key = (int)(at - (long long)head * per_head) * kDecodeTile;
-                p = key >> v.shift;
-                row0 = key & (page - 1);
+                const long long in_seq = g - sm.pre[lo];
+                head = (int)(in_seq / per_head);
+                at = (int)(in_seq - (long long)head * per_head);
             }
-            const int32_t pid = v.table[(int64_t)s * v.max_pages + p];
-            if (pid < 0 || pid >= v.n_pages) {
-                record_device_error(a.err, MSA_DEV_BAD_INDEX);
-                return;
+            const int n_pages = (seen + page - 1) >> v.shift;
+            const int32_t* table = v.table + (int64_t)s * v.max_pages;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                int p, row0 = 0;
+                if (h == 1 && !pairs) {                    // the other half of the same page's tile
+                    if (ti.rows[0] == 0) break;
+                    ti.key[1] = ti.key[0] + 16;
+                    ti.rows[1] = max(0, min(16, seen - ti.key[1]));
+                    ti.sk[1] = ti.sk[0];
+                    ti.sv[1] = ti.sv[0];
+                    break;
+                }
+                if (LIST) {
+                    const int li = pairs ? 2 * at + h : at / per_page;
+                    if (li >= a.k) break;
+                    p = a.sel[seg * a.k + li];
+                    if (!pairs) row0 = (at - li * per_page) * kDecodeTile;
+                    if (p == -1) continue;
+                    if (p < 0 || p >= n_pages) {
+                        record_device_error(a.err, MSA_DEV_BAD_INDEX);
+                        continue;
+                    }
+                } else {
+                    const int key = at * kDecodeTile + 16 * h;
+                    if (key >= seen) break;
+                    p = key >> v.shift;
+                    row0 = key & (page - 1);
+                }
+                const int32_t pid = table[p];
+                if (pid < 0 || pid >= v.n_pages) {
+                    record_device_error(a.err, MSA_DEV_BAD_INDEX);
+                    continue;
+                }
+                const int64_t slab = (int64_t)pid * 2 * v.hkv + head;
+                ti.key[h] = (p << v.shift) + row0;
+                ti.rows[h] = max(0, min(16, seen - ti.key[h]));
+                ti.sk[h] = v.scales[slab];
+                ti.sv[h] = v.scales[slab + v.hkv];
+                ti_row[h] = (int)(slab * page) + row0;
             }
-            const int64_t slab = (int64_t)pid * 2 * v.hkv + head;
-            ti.key = (p << v.shift) + row0;
-            ti.rows = max(0, min(kDecodeTile, seen - ti.key));
-            ti.sk = v.scales[slab];
-            ti.sv = v.scales[slab + v.hkv];
-            ti_row = (int)(slab * page) + row0;
+            if (ti.rows[0] == 0) ti.sv[0] = ti.sv[1];
+            if (ti.rows[1] == 0) ti.sv[1] = ti.sv[0];
         };
         auto issue = [&]() {
             if (issued >= n_mine) return;
@@ -232,15 +267,19 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
             if ((issued & 31) == 0) look_up();
             const int st = n % kStages;
             if (lane == (issued & 31)) {
-                const uint32_t bar = smem_u32(&sm.bar[warp][st]);
+                const uint32_t bar = smem_u32(&sm.bar[warp][st]), dst = smem_u32(sm.ring[warp][st]);
                 sm.info[warp][st] = ti;
-                if (ti.rows > 0) {
-                    const uint32_t dst = smem_u32(sm.ring[warp][st]);
-                    mbar_expect_tx(bar, kTileBytes);
-                    tma_load_2d(dst, &tm, 0, ti_row, bar);
-                    tma_load_2d(dst + kTileBytes / 2, &tm, 0, ti_row + v.hkv * page, bar);
-                } else {
-                    mbar_arrive(bar);
+                // a box is 32 rows, or where pages have 16, 16
+                const bool one = ti.rows[0] > 0, two = pairs && ti.rows[1] > 0;
+                const uint32_t bytes = (one ? (pairs ? kTileBytes / 2 : kTileBytes) : 0) + (two ? kTileBytes / 2 : 0);
+                mbar_expect_tx(bar, bytes);                // an arrival alone where it is 0
+                if (one) {
+                    tma_load_2d(dst, &tm, 0, ti_row[0], bar);
+                    tma_load_2d(dst + kTileBytes / 2, &tm, 0, ti_row[0] + v.hkv * page, bar);
+                }
+                if (two) {
+                    tma_load_2d(dst + 2048, &tm, 0, ti_row[1], bar);
+                    tma_load_2d(dst + kTileBytes / 2 + 2048, &tm, 0, ti_row[1] + v.hkv * page, bar);
                 }
             }
             ++issued;
@@ -288,9 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
             n_rows = live ? n_new * G : 0;
             const long long g1 = min(B, seg_b);
 
-            // this thread's part of Q^T: row n = r, elements 32 c .. 32 c + 31, times a power of two that brings the
-            // row's largest to [2^14, 2^15); what of the row is below 2^-39 of that is lost
-            uint32_t qf[16];
+            // this thread's part of Q^T: row n = r, elements 32 c .. 32 c + 31
+            uint32_t qh[8], ql[8];
             float f0, f1;                                  // logit factors of rows 2 c and 2 c + 1
             {
                 float x[32];
@@ -306,14 +344,19 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
                 for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = max(-112, min(127, (int)(__float_as_uint(top) >> 23) - 127));
-                const float up = pow2f(14 - e > 127 ? 127 : 14 - e);
+                // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                const uint32_t ub = __float_as_uint(top);
+                const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                const float inv = pow2f(-e);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const __half2 h = __floats2half2_rn(x[2 * i] * up, x[2 * i + 1] * up);
-                    qf[i] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t h0, l0, h1, l1;
+                    split_e4m3(x[4 * i] * inv, x[4 * i + 1] * inv, &h0, &l0);
+                    split_e4m3(x[4 * i + 2] * inv, x[4 * i + 3] * inv, &h1, &l1);
+                    qh[i] = h0 | (h1 << 16);
+                    ql[i] = l0 | (l1 << 16);
                 }
-                const float f = a.scale_log2e * pow2f(e - 14);
+                const float f = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : a.scale_log2e * pow2f(e);
                 f0 = __shfl_sync(0xffffffffu, f, 8 * c);
                 f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
             }
@@ -331,104 +374,149 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
                 const int n = it + taken, st = n % kStages;
                 const bool ok = __all_sync(
                     0xffffffffu, mbar_wait(smem_u32(&sm.bar[warp][st]), (uint32_t)(n / kStages) & 1u, abort_flag));
-                const TileInfo t = sm.info[warp][st];
-                if (ok && t.rows > 0) {
+                const TileInfo& t = sm.info[warp][st];
+                const int rows0 = t.rows[0], rows1 = t.rows[1];
+                if (ok && rows0 + rows1 > 0) {
                     const uint8_t* sk = sm.ring[warp][st];
                     const uint8_t* sv = sk + kTileBytes / 2;
                     // S^T: 16-byte pieces 2 c and 2 c + 1 of key rows r and r + 8 (piece i of row y lies at i ^ y % 8)
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+                    float s[2][4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int off = r * 128 + (((2 * c + h) ^ r) << 4);
-                        const uint4 x = *reinterpret_cast<const uint4*>(sk + off);
-                        const uint4 y = *reinterpret_cast<const uint4*>(sk + 1024 + off);
-                        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+                        float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t f[4];
-                            f[0] = e4m3x2_f16x2(xs[i] & 0xFFFFu);
-                            f[1] = e4m3x2_f16x2(ys[i] & 0xFFFFu);
-                            f[2] = e4m3x2_f16x2(xs[i] >> 16);
-                            f[3] = e4m3x2_f16x2(ys[i] >> 16);
-                            mma_f16_16816(s, f, qf[8 * h + 2 * i], qf[8 * h + 2 * i + 1]);
+                        for (int i = 0; i < 2; ++i) {
+                            const int off = 2048 * h + r * 128 + (((2 * c + i) ^ r) << 4);
+                            const uint4 x = *reinterpret_cast<const uint4*>(sk + off);
+                            const uint4 y = *reinterpret_cast<const uint4*>(sk + 1024 + off);
+                            mma_e4m3_16832(hi, x.x, y.x, x.y, y.y, qh[4 * i], qh[4 * i + 1]);
+                            mma_e4m3_16832(lo, x.x, y.x, x.y, y.y, ql[4 * i], ql[4 * i + 1]);
+                            mma_e4m3_16832(hi, x.z, y.z, x.w, y.w, qh[4 * i + 2], qh[4 * i + 3]);
+                            mma_e4m3_16832(lo, x.z, y.z, x.w, y.w, ql[4 * i + 2], ql[4 * i + 3]);
                         }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[h][i] = hi[i] + lo[i];
                     }
-                    const float k0 = f0 * t.sk, k1 = f1 * t.sk;
-                    float x00 = s[0] * k0, x01 = s[1] * k1, x10 = s[2] * k0, x11 = s[3] * k1;   // [key r, r + 8][row]
-                    if (t.key + kDecodeTile > seen_all) {
-                        const int ka = t.key + r, kb = ka + 8;
-                        x00 = ka < seen0 ? x00 : ninf;
-                        x01 = ka < seen1 ? x01 : ninf;
-                        x10 = kb < seen0 ? x10 : ninf;
-                        x11 = kb < seen1 ? x11 : ninf;
+                    // x: keys r and r + 8 of each half, rows 2 c and 2 c + 1
+                    float x[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float k0 = f0 * t.sk[h], k1 = f1 * t.sk[h];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[h][i] = s[h][i] * ((i & 1) ? k1 : k0);
                     }
-                    float t0m = fmaxf(x00, x10), t1m = fmaxf(x01, x11);
-                    if (__any_sync(0xffffffffu, t0m > m0 + kSlack || t1m > m1 + kSlack)) {
+                    if (rows0 < 16 || rows1 < 16 || max(t.key[0], t.key[1]) + 16 > seen_all) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int y = r + 8 * (i >> 1);
+                                if (y >= (h ? rows1 : rows0) || t.key[h] + y >= ((i & 1) ? seen1 : seen0)) x[h][i] = ninf;
+                            }
+                    }
+                    // V: piece r (d = 16 r ..) of the thread's eight keys, 2 c + {0, 8, 1, 9} and 16 on
+                    uint4 w8[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int key = 2 * c + 8 * (i & 1) + ((i >> 1) & 1) + 16 * (i >> 2);
+                        w8[i] = *reinterpret_cast<const uint4*>(sv + key * 128 + ((r ^ (key & 7)) << 4));
+                    }
+                    if (rows0 < 16 || rows1 < 16) {        // anything may stand where no key is
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (2 * c + 8 * (i & 1) + ((i >> 1) & 1) >= (i >> 2 ? rows1 : rows0)) w8[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    // halves whose scales of V lie far apart go one after the other, each against its own maximum
+                    const float va = t.sv[0], vb = t.sv[1];
+                    const bool apart = va > 16.f * vb || vb > 16.f * va;
+#pragma unroll 1
+                    for (int pass = 0; pass <= (apart ? 1 : 0); ++pass) {
+                        const float vs = apart ? (pass ? vb : va) : fmaxf(va, vb);
+                        float y[2][4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) y[h][i] = apart && h != pass ? ninf : x[h][i];
+                        float ma = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
+                        float mb = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
 #pragma unroll
                         for (int sh = 4; sh <= 16; sh <<= 1) {
-                            t0m = fmaxf(t0m, __shfl_xor_sync(0xffffffffu, t0m, sh));
-                            t1m = fmaxf(t1m, __shfl_xor_sync(0xffffffffu, t1m, sh));
+                            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
+                            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, sh));
                         }
-                        t0m = fmaxf(t0m, m0);
-                        t1m = fmaxf(t1m, m1);
-                        const float a0 = m0 == t0m ? 1.f : ex2(m0 - t0m), a1 = m1 == t1m ? 1.f : ex2(m1 - t1m);
-                        m0 = t0m;
-                        m1 = t1m;
-                        l0 *= a0;
-                        e0 *= a0;
-                        l1 *= a1;
-                        e1 *= a1;
+                        if (__any_sync(0xffffffffu, ma > m0 + kSlack || mb > m1 + kSlack)) {
+                            const float na = fmaxf(ma, m0), nb = fmaxf(mb, m1);
+                            const float a0 = m0 == na ? 1.f : ex2(m0 - na), a1 = m1 == nb ? 1.f : ex2(m1 - nb);
+                            m0 = na;
+                            m1 = nb;
+                            l0 *= a0;
+                            e0 *= a0;
+                            l1 *= a1;
+                            e1 *= a1;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            o[i][0] *= a0;
-                            o[i][1] *= a1;
-                            o[i][2] *= a0;
-                            o[i][3] *= a1;
+                            for (int i = 0; i < 8; ++i) {
+                                o[i][0] *= a0;
+                                o[i][1] *= a1;
+                                o[i][2] *= a0;
+                                o[i][3] *= a1;
+                            }
                         }
-                    }
-                    const float n0 = m0 == ninf ? 0.f : m0, n1 = m1 == ninf ? 0.f : m1;
-                    x00 = ex2(x00 - n0);
-                    x10 = ex2(x10 - n0);
-                    x01 = ex2(x01 - n1);
-                    x11 = ex2(x11 - n1);
-                    {
-                        const float d0 = (x00 + x10) - e0, d1 = (x01 + x11) - e1;
-                        const float s0 = l0 + d0, s1 = l1 + d1;
-                        e0 = (s0 - l0) - d0;
-                        e1 = (s1 - l1) - d1;
-                        l0 = s0;
-                        l1 = s1;
-                    }
-                    const float pv = t.sv * kUnit;
-                    const uint32_t b0 = transpose8x8(pack_bf16(x00 * pv, x01 * pv));
-                    const uint32_t b1 = transpose8x8(pack_bf16(x10 * pv, x11 * pv));
-                    // O^T: piece r (d = 16 r ..) of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9; row r of the fragment of tile i is
-                    // d = 16 r + 2 i, row r + 8 the next
-                    uint4 w4[4];
+                        // P times 2^8, and the weight of this tile's product
+                        const float na = ma == ninf ? 0.f : ma - 8.f, nb = mb == ninf ? 0.f : mb - 8.f;
+                        float wa = ma == ninf ? 0.f : ex2(ma - m0 - 8.f), wb = mb == ninf ? 0.f : ex2(mb - m1 - 8.f);
+                        uint32_t bh[2], bl[2];
+                        float ta = 0.f, tb = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-                        w4[i] = *reinterpret_cast<const uint4*>(sv + key * 128 + ((r ^ (key & 7)) << 4));
-                    }
-                    if (t.rows < kDecodeTile) {            // rows behind the end hold anything
+                        for (int h = 0; h < 2; ++h) {
+                            const float p0 = ex2(y[h][0] - na), p1 = ex2(y[h][1] - nb);
+                            const float p2 = ex2(y[h][2] - na), p3 = ex2(y[h][3] - nb);
+                            ta += p0 + p2;
+                            tb += p1 + p3;
+                            const float fac = __fdividef(h ? vb : va, vs);          // powers of two
+                            uint32_t ha, la, hb, lb;
+                            split_e4m3(p0 * fac, p2 * fac, &ha, &la);
+                            split_e4m3(p1 * fac, p3 * fac, &hb, &lb);
+                            bh[h] = transpose8x8(ha | (hb << 16));
+                            bl[h] = transpose8x8(la | (lb << 16));
+                        }
+                        {
+                            const float d0 = ta * wa - e0, d1 = tb * wb - e1;
+                            const float s0 = l0 + d0, s1 = l1 + d1;
+                            e0 = (s0 - l0) - d0;
+                            e1 = (s1 - l1) - d1;
+                            l0 = s0;
+                            l1 = s1;
+                        }
+                        wa *= vs;
+                        wb *= vs;
+                        // four elements of d of four keys are a 4 x 4 block of bytes; row r of the fragment of tile i is
+                        // d = 16 r + 2 i, row r + 8 the next
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (2 * c + (i & 1) + 8 * (i >> 1) >= t.rows) w4[i] = make_uint4(0, 0, 0, 0);
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t f[2][4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t wa = (&w4[0].x)[i], wb = (&w4[1].x)[i], wc = (&w4[2].x)[i], wd = (&w4[3].x)[i];
-                        uint32_t f[4];
-                        f[0] = e4m3_high_bf16x2(__byte_perm(wa, wb, 0x4000));
-                        f[1] = e4m3_high_bf16x2(__byte_perm(wa, wb, 0x5010));
-                        f[2] = e4m3_high_bf16x2(__byte_perm(wc, wd, 0x4000));
-                        f[3] = e4m3_high_bf16x2(__byte_perm(wc, wd, 0x5010));
-                        mma_bf16_16816(o[2 * i], f, b0, b1);
-                        f[0] = e4m3_high_bf16x2(__byte_perm(wa, wb, 0x6020));
-                        f[1] = e4m3_high_bf16x2(__byte_perm(wa, wb, 0x7030));
-                        f[2] = e4m3_high_bf16x2(__byte_perm(wc, wd, 0x6020));
-                        f[3] = e4m3_high_bf16x2(__byte_perm(wc, wd, 0x7030));
-                        mma_bf16_16816(o[2 * i + 1], f, b0, b1);
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t u0 = (&w8[4 * h].x)[i], u1 = (&w8[4 * h + 1].x)[i];
+                                const uint32_t u2 = (&w8[4 * h + 2].x)[i], u3 = (&w8[4 * h + 3].x)[i];
+                                const uint32_t a0 = __byte_perm(u0, u1, 0x5140), a1 = __byte_perm(u2, u3, 0x5140);
+                                const uint32_t a2 = __byte_perm(u0, u1, 0x7362), a3 = __byte_perm(u2, u3, 0x7362);
+                                f[h][0] = __byte_perm(a0, a1, 0x5410);
+                                f[h][1] = __byte_perm(a0, a1, 0x7632);
+                                f[h][2] = __byte_perm(a2, a3, 0x5410);
+                                f[h][3] = __byte_perm(a2, a3, 0x7632);
+                            }
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_e4m3_16832(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bh[0], bh[1]);
+                                mma_e4m3_16832(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bl[0], bl[1]);
+                                float* oo = o[2 * i + z];
+                                oo[0] = fmaf(d[0], wa, oo[0]);
+                                oo[1] = fmaf(d[1], wb, oo[1]);
+                                oo[2] = fmaf(d[2], wa, oo[2]);
+                                oo[3] = fmaf(d[3], wb, oo[3]);
+                            }
+                        }
                     }
                 }
                 __syncwarp();
@@ -475,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
                 const int d0 = 16 * (lane >> 2) + (lane & 3);
                 if (seg_a == g0 && seg_b == g1) {
                     const int64_t row = (t0 + warp / G) * hq + head * G + warp % G;
-                    const float inv = L == 0.f ? 0.f : kUnit / L;
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) a.out[row * kPagedD + d0 + 4 * i] = __float2bfloat16_rn(res[i] * inv);
                     if (a.lse && lane == 0) a.lse[row] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
@@ -513,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_decode_kernel(const __grid_
 
 msa_status launch_paged_decode(const PagedAttnArgs& a, int grid, cudaStream_t s) {
     constexpr int smem = (int)sizeof(DecodeSmem) + 1024;
-    static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks per SM");
+    static_assert(smem <= 232448, "shared memory");
     static std::mutex mu;
     static bool opted[64] = {false};
     int dev = 0;
@@ -530,7 +618,7 @@ msa_status launch_paged_decode(const PagedAttnArgs& a, int grid, cudaStream_t s)
     CUtensorMap tm{};
     const uint64_t dims[2] = {64, (uint64_t)(a.v.n_pages * 2 * a.v.hkv * a.v.page)};
     const uint64_t strides[1] = {kPagedD};
-    const uint32_t box[2] = {64, kDecodeTile};
+    const uint32_t box[2] = {64, (uint32_t)std::min(a.v.page, kDecodeTile)};
     MSA_RETURN_IF(make_tensor_map_bf16(&tm, a.v.pages, 2, dims, strides, box));
     if (a.sel) paged_decode_kernel<true><<<grid, kThreads, smem, s>>>(tm, a);
     else paged_decode_kernel<false><<<grid, kThreads, smem, s>>>(tm, a);
