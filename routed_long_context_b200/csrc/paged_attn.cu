@@ -56,8 +56,8 @@ AttnPlan attn_plan(int64_t n_tok, int n_seq, int max_new, int hq, int hkv, int m
     if (p.few) {
         p.rows = kDecodeRows;
         const int64_t pages = k > 0 ? n_tok * k : std::min<int64_t>(n_tok, n_seq) * max_pages;
-        tiles = (pages * hkv * std::max(1, page / kDecodeTile) + 7) / 8;
-        most = kSms;              // a tile for each of a block's 8 warps at least
+        tiles = (pages * hkv * std::max(1, page / kDecodeTile) + kMinDecodeTiles - 1) / kMinDecodeTiles;
+        most = kSms;
     } else {
         p.rows = (int64_t)max_new * G <= 128 ? 128 : 256;
         const int64_t blocks = ((int64_t)max_new * G + p.rows - 1) / p.rows * std::min<int64_t>(n_tok, n_seq);

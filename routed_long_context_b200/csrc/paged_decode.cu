@@ -15,8 +15,11 @@
 // rounding to bf16 costs), or of 2^-18 of the tile's largest for small ones. O and the sum are fp32 against a
 // maximum m that moves only when a tile exceeds it by 2^24. The order of d and of the keys inside the products
 // is free: a thread takes the 16-byte pieces that it can read from shared memory without bank conflicts, and V
-// needs no more than 4 x 4 byte transposes. Keys and values come by TMA in the 128-byte swizzle, three tiles of
-// 8 KB deep for each of the 8 warps of an SM (192 KB in flight; 44 KB cover the latency).
+// needs no more than 4 x 4 byte transposes.
+//
+// One block per SM: a warp of its own looks the pages up, 22 tiles at a time, and brings keys and values by TMA in
+// the 128-byte swizzle into a ring of 22 tiles of 8 KB (44 KB cover the latency of memory); 11 warps take the
+// tiles in turns.
 #include <algorithm>
 #include <mutex>
 
@@ -28,25 +31,29 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 3;
+constexpr int kWarps = 11, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;
+constexpr int kSlots = 2 * kWarps;                         // two of its own for each warp
+static_assert(kSlots <= 32, "a lane per slot");
 constexpr int kTileBytes = 2 * kDecodeTile * kPagedD;      // K and V of a tile
-constexpr int kWindow = 256;                               // sequences looked at together
+constexpr int kWindow = kConsumers;                        // sequences looked at together
 constexpr float kSlack = 24.f;
 
-struct TileInfo {     // of the tile's two halves of 16 keys
+struct __align__(16) TileInfo {      // of the tile's two halves of 16 keys
     int key[2];       // first key's place in the sequence
-    int rows[2];      // keys that hold something; 0: nothing was loaded
+    int rows;         // keys that hold something, half 0 + 256 * half 1
+    float vs;         // scale of V: the larger of the two
     float sk[2];      // scales of K
-    float sv[2];      // and of V
+    float fac[2];     // scale of V over vs; below 2^-4 the halves are handled apart
 };
+constexpr int kFull = 16 + 256 * 16;
 
 struct DecodeSmem {
-    uint8_t ring[kWarps][kStages][kTileBytes];
+    uint8_t ring[kSlots][kTileBytes];
     float o[kWarps][kDecodeRows][32];
     float2 ml[kWarps][kDecodeRows];
-    TileInfo info[kWarps][kStages];
-    uint64_t bar[kWarps][kStages];
+    TileInfo info[kSlots];
+    uint64_t full[kSlots], empty[kSlots];
+    int last[kSlots];                                      // loads of a slot so far
     long long pre[kWindow + 1];                            // tiles before each sequence of the window
     int64_t t0[kWindow];
     int n_new[kWindow], len[kWindow];
@@ -62,11 +69,31 @@ __device__ __forceinline__ void mma_e4m3_16832(float* c, uint32_t a0, uint32_t a
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// c[4] = A B
+__device__ __forceinline__ void mma_e4m3_16832_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                     uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 // x0, x1 as e4m3 pairs: the nearest, and the nearest to what that leaves (all within fp16's range)
 __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t* hi, uint32_t* lo) {
     const __half2 y = __floats2half2_rn(x0, x1);
@@ -76,28 +103,19 @@ __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t* hi, uin
                                                __NV_E4M3);
 }
 
-// Prefix sums over the block of one value per thread; returns the block's total.
-__device__ __forceinline__ long long block_prefix(long long x, long long* pre, long long* scan) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long s = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
+// The last i with pre[i] <= g.
+__device__ __forceinline__ int find(const long long* pre, int n, long long g) {
+    int lo = 0;
+    while (n > 1) {
+        const int h = n / 2;
+        if (pre[lo + h] <= g) {
+            lo += h;
+            n -= h;
+        } else {
+            n = h;
+        }
     }
-    __syncthreads();
-    if (lane == 31) scan[warp] = s;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
-    }
-    pre[threadIdx.x + 1] = before + s;
-    if (threadIdx.x == 0) pre[0] = 0;
-    __syncthreads();
-    return total;
+    return lo;
 }
 
 template <bool LIST>
@@ -107,32 +125,52 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     DecodeSmem& sm = *reinterpret_cast<DecodeSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const PagedView& v = a.v;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r = lane >> 2, c = lane & 3;                 // the thread's place in a fragment
-    const int G = a.G, hq = v.hkv * G, page = v.page;
+    const int G = a.G, gs = 31 - __clz(G), hq = v.hkv * G, page = v.page;
     // tiles per page, or two pages per tile
     const bool pairs = page == 16;
     const int per_page = pairs ? 1 : page / kDecodeTile;
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
     if (tid == 0) sm.abort_flag = 0;
-    if (lane == 0) {
-        for (int i = 0; i < kStages; ++i) mbar_init(smem_u32(&sm.bar[warp][i]), 1);
+    if (tid < kSlots) {
+        mbar_init(smem_u32(&sm.full[tid]), 1);
+        mbar_init(smem_u32(&sm.empty[tid]), 1);
+        sm.last[tid] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
 
-    // tiles of all sequences
+    // tiles of all sequences: a thread per sequence of the window
     const int n_windows = LIST ? 1 : (v.n_seq + kWindow - 1) / kWindow;
     auto load_window = [&](int w) -> long long {
         const int s = w * kWindow + tid;
         SeqSpan sp{0, 0, 0};
-        if (s < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, blockIdx.x == 0 ? a.err : nullptr);
+        if (tid < kWindow && s < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, blockIdx.x == 0 ? a.err : nullptr);
+        const long long x = sp.n_new ? (long long)v.hkv * ((sp.len + kDecodeTile - 1) / kDecodeTile) : 0;
+        long long up = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, up, o);
+            if (lane >= o) up += y;
+        }
         __syncthreads();
-        sm.t0[tid] = sp.t0;
-        sm.n_new[tid] = sp.n_new;
-        sm.len[tid] = sp.len;
-        return block_prefix(sp.n_new ? (long long)v.hkv * ((sp.len + kDecodeTile - 1) / kDecodeTile) : 0, sm.pre,
-                            sm.scan);
+        if (tid < kWindow) {
+            sm.t0[tid] = sp.t0;
+            sm.n_new[tid] = sp.n_new;
+            sm.len[tid] = sp.len;
+            if (lane == 31) sm.scan[warp] = up;
+        }
+        __syncthreads();
+        long long before = 0, all = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) before += sm.scan[i];
+            all += sm.scan[i];
+        }
+        if (tid < kWindow) sm.pre[tid + 1] = before + up;
+        if (tid == 0) sm.pre[0] = 0;
+        __syncthreads();
+        return all;
     };
     long long total = 0, first_total = 0;
     const int list_tiles = !LIST ? 1 : pairs ? (a.k + 1) / 2 : a.k * per_page;
@@ -145,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             total += first_total;
         }
     }
-    const int n_cta = (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
+    const int n_cta = (int)min((long long)gridDim.x, (total + kMinDecodeTiles - 1) / kMinDecodeTiles);
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -154,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     const long long my_a = cta_first(total, n_cta, blockIdx.x), my_b = cta_first(total, n_cta, blockIdx.x + 1);
     OpenSegment open{0, 0, 0, 0, 1.f};
 
-    int it = 0;                                            // tiles this warp has taken: ring stage and phase
+    int done = 0;                                          // tiles of earlier windows: they give slot and phase
     long long base = 0;                                    // tiles before the window
     for (int w = 0; w < n_windows; ++w) {
         const long long in_window = (w == 0) ? first_total : load_window(w);
@@ -164,436 +202,444 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             continue;
         }
         const int n_win = LIST ? 0 : min(kWindow, v.n_seq - w * kWindow);
+        const int count = (int)(B - A);
 
-        // Lane l looks up tile l of the warp's next 32; they are issued one by one as ring stages come free.
-        TileInfo ti;
-        int ti_row[2];                                     // tensor-map rows of the halves' first keys
-        const int n_mine = (int)((B - A - warp + kWarps - 1) / kWarps);
-        int issued = 0;
-        auto look_up = [&]() {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ti.key[h] = ti.rows[h] = ti_row[h] = 0;
-                ti.sk[h] = ti.sv[h] = 1.f;
-            }
-            const long long g = A + warp + (long long)kWarps * (issued + lane);
-            if (g >= B) return;
-            int s, head, seen, at;                         // at: the tile's number in its segment
-            long long seg = 0;
-            if (LIST) {
-                seg = g / list_tiles;
-                at = (int)(g - seg * list_tiles);
-                const long long t = seg / v.hkv;
-                head = (int)(seg - t * v.hkv);
-                int lo = 0, n = v.n_seq;                   // the last sequence that starts at or before t
-                while (n > 1) {
-                    const int h = n / 2;
-                    if (a.tok_off[lo + h] <= t) {
-                        lo += h;
-                        n -= h;
+        if (warp == kWarps) {
+            // ------------------------------------------------------------------ loader: a lane per tile
+            // as many at a time as there are slots: two lanes waiting for the same slot, a phase apart, could not
+            // tell by its parity whose turn it is
+            for (int i0 = 0; i0 < count; i0 += kSlots) {
+                const int i = lane < kSlots ? i0 + lane : count;
+                TileInfo ti;
+                int row[2] = {0, 0}, rows[2] = {0, 0};
+                float sv[2] = {1.f, 1.f};
+                ti.key[0] = ti.key[1] = 0;
+                ti.sk[0] = ti.sk[1] = 1.f;
+                auto look_up = [&]() {
+                    const long long g = A + i;
+                    int s, head, seen, at;                 // at: the tile's number in its segment
+                    long long seg = 0;
+                    if (LIST) {
+                        seg = g / list_tiles;
+                        at = (int)(g - seg * list_tiles);
+                        const long long t = seg / v.hkv;
+                        head = (int)(seg - t * v.hkv);
+                        int lo = 0, n = v.n_seq;           // the last sequence that starts at or before t
+                        while (n > 1) {
+                            const int h = n / 2;
+                            if (a.tok_off[lo + h] <= t) {
+                                lo += h;
+                                n -= h;
+                            } else {
+                                n = h;
+                            }
+                        }
+                        s = lo;
+                        SeqSpan sp;
+                        if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, a.err) || t < sp.t0 || t >= sp.t0 + sp.n_new) return;
+                        seen = sp.len - sp.n_new + (int)(t - sp.t0) + 1;
                     } else {
-                        n = h;
+                        const int lo = find(sm.pre, n_win, g);
+                        s = w * kWindow + lo;
+                        seen = sm.len[lo];
+                        const int per_head = (seen + kDecodeTile - 1) / kDecodeTile;
+                        const unsigned in_seq = (unsigned)(g - sm.pre[lo]);
+                        head = (int)(in_seq / (unsigned)per_head);
+                        at = (int)(in_seq - (unsigned)head * per_head);
+                    }
+                    const int n_pages = (seen + page - 1) >> v.shift;
+                    const int32_t* table = v.table + (int64_t)s * v.max_pages;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        int p, row0 = 0;
+                        if (h == 1 && !pairs) {            // the other half of the same page's tile
+                            if (rows[0] == 0) break;
+                            ti.key[1] = ti.key[0] + 16;
+                            rows[1] = max(0, min(16, seen - ti.key[1]));
+                            ti.sk[1] = ti.sk[0];
+                            sv[1] = sv[0];
+                            break;
+                        }
+                        if (LIST) {
+                            const int li = pairs ? 2 * at + h : at / per_page;
+                            if (li >= a.k) break;
+                            p = a.sel[seg * a.k + li];
+                            if (!pairs) row0 = (at - li * per_page) * kDecodeTile;
+                            if (p == -1) continue;
+                            if (p < 0 || p >= n_pages) {
+                                record_device_error(a.err, MSA_DEV_BAD_INDEX);
+                                continue;
+                            }
+                        } else {
+                            const int key = at * kDecodeTile + 16 * h;
+                            if (key >= seen) break;
+                            p = key >> v.shift;
+                            row0 = key & (page - 1);
+                        }
+                        const int32_t pid = table[p];
+                        if (pid < 0 || pid >= v.n_pages) {
+                            record_device_error(a.err, MSA_DEV_BAD_INDEX);
+                            continue;
+                        }
+                        const int64_t slab = (int64_t)pid * 2 * v.hkv + head;
+                        ti.key[h] = (p << v.shift) + row0;
+                        rows[h] = max(0, min(16, seen - ti.key[h]));
+                        ti.sk[h] = v.scales[slab];
+                        sv[h] = v.scales[slab + v.hkv];
+                        row[h] = (int)(slab * page) + row0;
+                    }
+                };
+                if (i < count) look_up();
+                if (rows[0] == 0) sv[0] = sv[1];
+                if (rows[1] == 0) sv[1] = sv[0];
+                ti.vs = fmaxf(sv[0], sv[1]);
+                ti.fac[0] = sv[0] / ti.vs;
+                ti.fac[1] = sv[1] / ti.vs;
+                ti.rows = rows[0] + 256 * rows[1];
+                // each lane brings its tile in as soon as the slot is free
+                const int n = done + i, slot = n % kSlots;      // distinct for the lanes with a tile
+                const uint32_t full = smem_u32(&sm.full[slot]), empty = smem_u32(&sm.empty[slot]), dst = smem_u32(sm.ring[slot]);
+                bool pending = i < count;
+                const uint64_t t_start = globaltimer();
+                for (uint32_t polls = 0; __any_sync(0xffffffffu, pending); ++polls) {
+                    if (pending && mbar_test(empty, ((uint32_t)(n / kSlots) & 1u) ^ 1u)) {
+                        sm.info[slot] = ti;
+                        sm.last[slot] = n / kSlots + 1;
+                        // a box is 32 rows, or where pages have 16, 16
+                        const bool one = rows[0] > 0, two = pairs && rows[1] > 0;
+                        mbar_expect_tx(full, (one ? (pairs ? kTileBytes / 2 : kTileBytes) : 0) + (two ? kTileBytes / 2 : 0));
+                        if (one) {
+                            tma_load_2d(dst, &tm, 0, row[0], full);
+                            tma_load_2d(dst + kTileBytes / 2, &tm, 0, row[0] + v.hkv * page, full);
+                        }
+                        if (two) {
+                            tma_load_2d(dst + 2048, &tm, 0, row[1], full);
+                            tma_load_2d(dst + kTileBytes / 2 + 2048, &tm, 0, row[1] + v.hkv * page, full);
+                        }
+                        pending = false;
+                    }
+                    if ((polls & 63) == 63) {
+                        if (lane == 0 && globaltimer() - t_start > kWaitNs) *abort_flag = 1;
+                        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
                     }
                 }
-                s = lo;
-                SeqSpan sp;
-                if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, a.err) || t < sp.t0 || t >= sp.t0 + sp.n_new) return;
-                seen = sp.len - sp.n_new + (int)(t - sp.t0) + 1;
-            } else {
-                int lo = 0, n = n_win;
-                while (n > 1) {
-                    const int h = n / 2;
-                    if (sm.pre[lo + h] <= g) {
-                        lo += h;
-                        n -= h;
-                    } else {
-                        n = h;
-                    }
-                }
-                s = w * kWindow + lo;
-                seen = sm.len[lo];
-                const int per_head = (seen + kDecodeTile - 1) / kDecodeTile;
-                const long long in_seq = g - sm.pre[lo];
-                head = (int)(in_seq / per_head);
-                at = (int)(in_seq - (long long)head * per_head);
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             }
-            const int n_pages = (seen + page - 1) >> v.shift;
-            const int32_t* table = v.table + (int64_t)s * v.max_pages;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                int p, row0 = 0;
-                if (h == 1 && !pairs) {                    // the other half of the same page's tile
-                    if (ti.rows[0] == 0) break;
-                    ti.key[1] = ti.key[0] + 16;
-                    ti.rows[1] = max(0, min(16, seen - ti.key[1]));
-                    ti.sk[1] = ti.sk[0];
-                    ti.sv[1] = ti.sv[0];
-                    break;
-                }
+        } else {
+            // ------------------------------------------------------------------ segment by segment
+            const int r = lane >> 2, c = lane & 3;         // the thread's place in a fragment
+            // its pieces of K (rows r and r + 8, pieces 2 c and 2 c + 1) and V (piece r of keys 2 c + {0, 8, 1, 9}): piece i
+            // of row y lies at i ^ y % 8
+            const int k_at = r * 128 + (((2 * c) ^ r) << 4);
+            const int v_at0 = kTileBytes / 2 + 2 * c * 128 + ((r ^ (2 * c)) << 4);
+            const int v_at1 = kTileBytes / 2 + (2 * c + 1) * 128 + ((r ^ (2 * c + 1)) << 4);
+            // The warp's tiles are those whose number (over all windows) leaves it as remainder, and so are its slots: with
+            // slots that passed from warp to warp, one that runs ahead could not tell a phase from the next but one.
+            int taken = ((warp - done) % kWarps + kWarps) % kWarps;
+            for (long long g0 = A; g0 < B;) {
+                long long seg_a, seg_b;
+                int64_t t0;
+                int head, n_rows, len, n_new;
+                bool live = true;
                 if (LIST) {
-                    const int li = pairs ? 2 * at + h : at / per_page;
-                    if (li >= a.k) break;
-                    p = a.sel[seg * a.k + li];
-                    if (!pairs) row0 = (at - li * per_page) * kDecodeTile;
-                    if (p == -1) continue;
-                    if (p < 0 || p >= n_pages) {
-                        record_device_error(a.err, MSA_DEV_BAD_INDEX);
-                        continue;
-                    }
+                    const long long seg = g0 / list_tiles;
+                    t0 = seg / v.hkv;
+                    head = (int)(seg - t0 * v.hkv);
+                    seg_a = seg * list_tiles;
+                    seg_b = seg_a + list_tiles;
+                    const int s = seq_of_token(a.tok_off, v.n_seq, t0);
+                    SeqSpan sp;
+                    live = seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) && t0 >= sp.t0 && t0 < sp.t0 + sp.n_new;
+                    len = sp.len - sp.n_new + (int)(t0 - sp.t0) + 1;
+                    n_new = 1;
                 } else {
-                    const int key = at * kDecodeTile + 16 * h;
-                    if (key >= seen) break;
-                    p = key >> v.shift;
-                    row0 = key & (page - 1);
+                    const int lo = find(sm.pre, n_win, g0);
+                    t0 = sm.t0[lo];
+                    n_new = sm.n_new[lo];
+                    len = sm.len[lo];
+                    const int per_head = (len + kDecodeTile - 1) / kDecodeTile;
+                    head = (int)((unsigned)(g0 - sm.pre[lo]) / (unsigned)per_head);
+                    seg_a = sm.pre[lo] + (long long)head * per_head;
+                    seg_b = seg_a + per_head;
                 }
-                const int32_t pid = table[p];
-                if (pid < 0 || pid >= v.n_pages) {
-                    record_device_error(a.err, MSA_DEV_BAD_INDEX);
-                    continue;
-                }
-                const int64_t slab = (int64_t)pid * 2 * v.hkv + head;
-                ti.key[h] = (p << v.shift) + row0;
-                ti.rows[h] = max(0, min(16, seen - ti.key[h]));
-                ti.sk[h] = v.scales[slab];
-                ti.sv[h] = v.scales[slab + v.hkv];
-                ti_row[h] = (int)(slab * page) + row0;
-            }
-            if (ti.rows[0] == 0) ti.sv[0] = ti.sv[1];
-            if (ti.rows[1] == 0) ti.sv[1] = ti.sv[0];
-        };
-        auto issue = [&]() {
-            if (issued >= n_mine) return;
-            const int n = it + issued;                     // it counts the consumed tiles of earlier windows
-            if ((issued & 31) == 0) look_up();
-            const int st = n % kStages;
-            if (lane == (issued & 31)) {
-                const uint32_t bar = smem_u32(&sm.bar[warp][st]), dst = smem_u32(sm.ring[warp][st]);
-                sm.info[warp][st] = ti;
-                // a box is 32 rows, or where pages have 16, 16
-                const bool one = ti.rows[0] > 0, two = pairs && ti.rows[1] > 0;
-                const uint32_t bytes = (one ? (pairs ? kTileBytes / 2 : kTileBytes) : 0) + (two ? kTileBytes / 2 : 0);
-                mbar_expect_tx(bar, bytes);                // an arrival alone where it is 0
-                if (one) {
-                    tma_load_2d(dst, &tm, 0, ti_row[0], bar);
-                    tma_load_2d(dst + kTileBytes / 2, &tm, 0, ti_row[0] + v.hkv * page, bar);
-                }
-                if (two) {
-                    tma_load_2d(dst + 2048, &tm, 0, ti_row[1], bar);
-                    tma_load_2d(dst + kTileBytes / 2 + 2048, &tm, 0, ti_row[1] + v.hkv * page, bar);
-                }
-            }
-            ++issued;
-            __syncwarp();
-        };
-        for (int i = 0; i < kStages; ++i) issue();
-        int taken = 0;
+                n_rows = live ? n_new * G : 0;
+                const long long g1 = min(B, seg_b);
+                const int end = (int)(g1 - A);
 
-        // segment by segment
-        for (long long g0 = A; g0 < B;) {
-            long long seg_a, seg_b;
-            int64_t t0;
-            int head, n_rows, len, n_new;
-            bool live = true;
-            if (LIST) {
-                const long long seg = g0 / list_tiles;
-                t0 = seg / v.hkv;
-                head = (int)(seg - t0 * v.hkv);
-                seg_a = seg * list_tiles;
-                seg_b = seg_a + list_tiles;
-                const int s = seq_of_token(a.tok_off, v.n_seq, t0);
-                SeqSpan sp;
-                live = seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) && t0 >= sp.t0 && t0 < sp.t0 + sp.n_new;
-                len = sp.len - sp.n_new + (int)(t0 - sp.t0) + 1;
-                n_new = 1;
-            } else {
-                int lo = 0, n = n_win;
-                while (n > 1) {
-                    const int h = n / 2;
-                    if (sm.pre[lo + h] <= g0) {
-                        lo += h;
-                        n -= h;
-                    } else {
-                        n = h;
+                // this thread's part of Q^T: row n = r, elements 32 c .. 32 c + 31; the softmax scale's sign is Q's
+                uint32_t qh[8], ql[8];
+                float f0, f1;                              // logit factors of rows 2 c and 2 c + 1
+                {
+                    uint4 x[4];
+                    float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
+                    if (r < n_rows) {
+                        const uint4* src = reinterpret_cast<const uint4*>(
+                            a.q + ((t0 + (r >> gs)) * hq + head * G + (r & (G - 1))) * kPagedD + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = src[i];
                     }
-                }
-                t0 = sm.t0[lo];
-                n_new = sm.n_new[lo];
-                len = sm.len[lo];
-                const int per_head = (len + kDecodeTile - 1) / kDecodeTile;
-                head = (int)((g0 - sm.pre[lo]) / per_head);
-                seg_a = sm.pre[lo] + (long long)head * per_head;
-                seg_b = seg_a + per_head;
-            }
-            n_rows = live ? n_new * G : 0;
-            const long long g1 = min(B, seg_b);
-
-            // this thread's part of Q^T: row n = r, elements 32 c .. 32 c + 31
-            uint32_t qh[8], ql[8];
-            float f0, f1;                                  // logit factors of rows 2 c and 2 c + 1
-            {
-                float x[32];
-                float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = 0.f;
-                if (r < n_rows) {
-                    const __nv_bfloat16* src = a.q + ((t0 + r / G) * hq + head * G + r % G) * kPagedD + 32 * c;
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) load16_f32(src + i, x + i);
-                }
+                        for (int j = 0; j < 4; ++j)
+                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                    const uint32_t ub = __float_as_uint(top);
+                    const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                    const float inv = a.scale_log2e < 0.f ? -pow2f(-e) : pow2f(-e);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
-                const uint32_t ub = __float_as_uint(top);
-                const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
-                const float inv = pow2f(-e);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t h0, l0, h1, l1;
-                    split_e4m3(x[4 * i] * inv, x[4 * i + 1] * inv, &h0, &l0);
-                    split_e4m3(x[4 * i + 2] * inv, x[4 * i + 3] * inv, &h1, &l1);
-                    qh[i] = h0 | (h1 << 16);
-                    ql[i] = l0 | (l1 << 16);
-                }
-                const float f = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : a.scale_log2e * pow2f(e);
-                f0 = __shfl_sync(0xffffffffu, f, 8 * c);
-                f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-            }
-            const int seen0 = 2 * c < n_rows ? len - n_new + 2 * c / G + 1 : 0;
-            const int seen1 = 2 * c + 1 < n_rows ? len - n_new + (2 * c + 1) / G + 1 : 0;
-            const int seen_all = len - n_new + 1;          // keys that every row sees
-
-            float o[8][4], m0 = ninf, m1 = ninf, l0 = 0.f, l1 = 0.f, e0 = 0.f, e1 = 0.f;   // e: roundings of l
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
-
-            for (; A + warp + (long long)kWarps * taken < g1; ++taken) {
-                const int n = it + taken, st = n % kStages;
-                const bool ok = __all_sync(
-                    0xffffffffu, mbar_wait(smem_u32(&sm.bar[warp][st]), (uint32_t)(n / kStages) & 1u, abort_flag));
-                const TileInfo& t = sm.info[warp][st];
-                const int rows0 = t.rows[0], rows1 = t.rows[1];
-                if (ok && rows0 + rows1 > 0) {
-                    const uint8_t* sk = sm.ring[warp][st];
-                    const uint8_t* sv = sk + kTileBytes / 2;
-                    // S^T: 16-byte pieces 2 c and 2 c + 1 of key rows r and r + 8 (piece i of row y lies at i ^ y % 8)
-                    float s[2][4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int off = 2048 * h + r * 128 + (((2 * c + i) ^ r) << 4);
-                            const uint4 x = *reinterpret_cast<const uint4*>(sk + off);
-                            const uint4 y = *reinterpret_cast<const uint4*>(sk + 1024 + off);
-                            mma_e4m3_16832(hi, x.x, y.x, x.y, y.y, qh[4 * i], qh[4 * i + 1]);
-                            mma_e4m3_16832(lo, x.x, y.x, x.y, y.y, ql[4 * i], ql[4 * i + 1]);
-                            mma_e4m3_16832(hi, x.z, y.z, x.w, y.w, qh[4 * i + 2], qh[4 * i + 3]);
-                            mma_e4m3_16832(lo, x.z, y.z, x.w, y.w, ql[4 * i + 2], ql[4 * i + 3]);
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t h0, l0, h1, l1;
+                            split_e4m3(__uint_as_float(u[2 * j] << 16) * inv, __uint_as_float(u[2 * j] & 0xFFFF0000u) * inv, &h0, &l0);
+                            split_e4m3(__uint_as_float(u[2 * j + 1] << 16) * inv, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * inv,
+                                       &h1, &l1);
+                            qh[2 * i + j] = h0 | (h1 << 16);
+                            ql[2 * i + j] = l0 | (l1 << 16);
                         }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[h][i] = hi[i] + lo[i];
                     }
-                    // x: keys r and r + 8 of each half, rows 2 c and 2 c + 1
-                    float x[2][4];
+                    const float f = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fabsf(a.scale_log2e) * pow2f(e);
+                    f0 = __shfl_sync(0xffffffffu, f, 8 * c);
+                    f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+                }
+                const int seen0 = 2 * c < n_rows ? len - n_new + ((2 * c) >> gs) + 1 : 0;
+                const int seen1 = 2 * c + 1 < n_rows ? len - n_new + ((2 * c + 1) >> gs) + 1 : 0;
+                const int seen_all = len - n_new + 1;      // keys that every row sees
+
+                float o[8][4], m0 = ninf, m1 = ninf, l0 = 0.f, l1 = 0.f, e0 = 0.f, e1 = 0.f;   // e: roundings of l
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float k0 = f0 * t.sk[h], k1 = f1 * t.sk[h];
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) x[h][i] = s[h][i] * ((i & 1) ? k1 : k0);
-                    }
-                    if (rows0 < 16 || rows1 < 16 || max(t.key[0], t.key[1]) + 16 > seen_all) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int y = r + 8 * (i >> 1);
-                                if (y >= (h ? rows1 : rows0) || t.key[h] + y >= ((i & 1) ? seen1 : seen0)) x[h][i] = ninf;
-                            }
-                    }
-                    // V: piece r (d = 16 r ..) of the thread's eight keys, 2 c + {0, 8, 1, 9} and 16 on
-                    uint4 w8[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int key = 2 * c + 8 * (i & 1) + ((i >> 1) & 1) + 16 * (i >> 2);
-                        w8[i] = *reinterpret_cast<const uint4*>(sv + key * 128 + ((r ^ (key & 7)) << 4));
-                    }
-                    if (rows0 < 16 || rows1 < 16) {        // anything may stand where no key is
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (2 * c + 8 * (i & 1) + ((i >> 1) & 1) >= (i >> 2 ? rows1 : rows0)) w8[i] = make_uint4(0, 0, 0, 0);
-                    }
-                    // halves whose scales of V lie far apart go one after the other, each against its own maximum
-                    const float va = t.sv[0], vb = t.sv[1];
-                    const bool apart = va > 16.f * vb || vb > 16.f * va;
-#pragma unroll 1
-                    for (int pass = 0; pass <= (apart ? 1 : 0); ++pass) {
-                        const float vs = apart ? (pass ? vb : va) : fmaxf(va, vb);
-                        float y[2][4];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) y[h][i] = apart && h != pass ? ninf : x[h][i];
-                        float ma = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
-                        float mb = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
-#pragma unroll
-                        for (int sh = 4; sh <= 16; sh <<= 1) {
-                            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
-                            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, sh));
-                        }
-                        if (__any_sync(0xffffffffu, ma > m0 + kSlack || mb > m1 + kSlack)) {
-                            const float na = fmaxf(ma, m0), nb = fmaxf(mb, m1);
-                            const float a0 = m0 == na ? 1.f : ex2(m0 - na), a1 = m1 == nb ? 1.f : ex2(m1 - nb);
-                            m0 = na;
-                            m1 = nb;
-                            l0 *= a0;
-                            e0 *= a0;
-                            l1 *= a1;
-                            e1 *= a1;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                o[i][0] *= a0;
-                                o[i][1] *= a1;
-                                o[i][2] *= a0;
-                                o[i][3] *= a1;
-                            }
-                        }
-                        // P times 2^8, and the weight of this tile's product
-                        const float na = ma == ninf ? 0.f : ma - 8.f, nb = mb == ninf ? 0.f : mb - 8.f;
-                        float wa = ma == ninf ? 0.f : ex2(ma - m0 - 8.f), wb = mb == ninf ? 0.f : ex2(mb - m1 - 8.f);
-                        uint32_t bh[2], bl[2];
-                        float ta = 0.f, tb = 0.f;
+                    for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+
+                for (; taken < end; taken += kWarps) {
+                    const int n = done + taken, slot = n % kSlots;
+                    const bool ok = __all_sync(
+                        0xffffffffu, mbar_wait(smem_u32(&sm.full[slot]), (uint32_t)(n / kSlots) & 1u, abort_flag));
+                    const TileInfo t = sm.info[slot];
+                    if (ok && t.rows) {
+                        const uint8_t* tile = sm.ring[slot];
+                        // S^T: keys r and r + 8 of each half, rows 2 c and 2 c + 1
+                        float s[2][4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const float p0 = ex2(y[h][0] - na), p1 = ex2(y[h][1] - nb);
-                            const float p2 = ex2(y[h][2] - na), p3 = ex2(y[h][3] - nb);
-                            ta += p0 + p2;
-                            tb += p1 + p3;
-                            const float fac = __fdividef(h ? vb : va, vs);          // powers of two
-                            uint32_t ha, la, hb, lb;
-                            split_e4m3(p0 * fac, p2 * fac, &ha, &la);
-                            split_e4m3(p1 * fac, p3 * fac, &hb, &lb);
-                            bh[h] = transpose8x8(ha | (hb << 16));
-                            bl[h] = transpose8x8(la | (lb << 16));
-                        }
-                        {
-                            const float d0 = ta * wa - e0, d1 = tb * wb - e1;
-                            const float s0 = l0 + d0, s1 = l1 + d1;
-                            e0 = (s0 - l0) - d0;
-                            e1 = (s1 - l1) - d1;
-                            l0 = s0;
-                            l1 = s1;
-                        }
-                        wa *= vs;
-                        wb *= vs;
-                        // four elements of d of four keys are a 4 x 4 block of bytes; row r of the fragment of tile i is
-                        // d = 16 r + 2 i, row r + 8 the next
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t f[2][4];
+                            for (int i = 0; i < 2; ++i) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(tile + 2048 * h + (k_at ^ (16 * i)));
+                                const uint4 y = *reinterpret_cast<const uint4*>(tile + 2048 * h + 1024 + (k_at ^ (16 * i)));
+                                if (i == 0) mma_e4m3_16832_first(s[h], x.x, y.x, x.y, y.y, qh[0], qh[1]);
+                                else mma_e4m3_16832(s[h], x.x, y.x, x.y, y.y, qh[4], qh[5]);
+                                mma_e4m3_16832(s[h], x.z, y.z, x.w, y.w, qh[4 * i + 2], qh[4 * i + 3]);
+                                mma_e4m3_16832(s[h], x.x, y.x, x.y, y.y, ql[4 * i], ql[4 * i + 1]);
+                                mma_e4m3_16832(s[h], x.z, y.z, x.w, y.w, ql[4 * i + 2], ql[4 * i + 3]);
+                            }
+                        }
+                        uint4 w8[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            w8[i] = *reinterpret_cast<const uint4*>(tile + (i >> 2) * 2048 + (i & 1) * 1024 + ((i >> 1) & 1 ? v_at1 : v_at0));
+                        if (t.rows != kFull || max(t.key[0], t.key[1]) + 16 > seen_all) {
+                            // keys that a row does not see, and places without a key, where anything may stand
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const uint32_t u0 = (&w8[4 * h].x)[i], u1 = (&w8[4 * h + 1].x)[i];
-                                const uint32_t u2 = (&w8[4 * h + 2].x)[i], u3 = (&w8[4 * h + 3].x)[i];
-                                const uint32_t a0 = __byte_perm(u0, u1, 0x5140), a1 = __byte_perm(u2, u3, 0x5140);
-                                const uint32_t a2 = __byte_perm(u0, u1, 0x7362), a3 = __byte_perm(u2, u3, 0x7362);
-                                f[h][0] = __byte_perm(a0, a1, 0x5410);
-                                f[h][1] = __byte_perm(a0, a1, 0x7632);
-                                f[h][2] = __byte_perm(a2, a3, 0x5410);
-                                f[h][3] = __byte_perm(a2, a3, 0x7632);
-                            }
+                                const int rows = h ? t.rows >> 8 : t.rows & 255;
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_e4m3_16832(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bh[0], bh[1]);
-                                mma_e4m3_16832(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bl[0], bl[1]);
-                                float* oo = o[2 * i + z];
-                                oo[0] = fmaf(d[0], wa, oo[0]);
-                                oo[1] = fmaf(d[1], wb, oo[1]);
-                                oo[2] = fmaf(d[2], wa, oo[2]);
-                                oo[3] = fmaf(d[3], wb, oo[3]);
+                                for (int i = 0; i < 4; ++i) {
+                                    const int y = r + 8 * (i >> 1);
+                                    if (y >= rows || t.key[h] + y >= ((i & 1) ? seen1 : seen0)) s[h][i] = ninf;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (2 * c + 8 * (i & 1) + (i >> 1) >= rows) w8[4 * h + i] = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        // halves whose scales of V lie far apart go one after the other, each against its own maximum
+                        const bool apart = fminf(t.fac[0], t.fac[1]) < 0.0625f;
+#pragma unroll 1
+                        for (int pass = 0; pass < (apart ? 2 : 1); ++pass) {
+                            float fac[2] = {t.fac[0], t.fac[1]}, vs = t.vs;
+                            float y[2][4];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) y[h][i] = s[h][i];
+                            if (apart) {
+                                vs *= fac[pass];
+                                fac[0] = fac[1] = 1.f;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    if (pass == 0) y[1][i] = ninf;
+                                    else y[0][i] = ninf;
+                                }
+                            }
+                            const float k0[2] = {f0 * t.sk[0], f0 * t.sk[1]}, k1[2] = {f1 * t.sk[0], f1 * t.sk[1]};
+                            float ma = fmaxf(fmaxf(y[0][0], y[0][2]) * k0[0], fmaxf(y[1][0], y[1][2]) * k0[1]);
+                            float mb = fmaxf(fmaxf(y[0][1], y[0][3]) * k1[0], fmaxf(y[1][1], y[1][3]) * k1[1]);
+#pragma unroll
+                            for (int sh = 4; sh <= 16; sh <<= 1) {
+                                ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
+                                mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, sh));
+                            }
+                            if (__any_sync(0xffffffffu, ma > m0 + kSlack || mb > m1 + kSlack)) {
+                                const float na = fmaxf(ma, m0), nb = fmaxf(mb, m1);
+                                const float a0 = m0 == na ? 1.f : ex2(m0 - na), a1 = m1 == nb ? 1.f : ex2(m1 - nb);
+                                m0 = na;
+                                m1 = nb;
+                                l0 *= a0;
+                                e0 *= a0;
+                                l1 *= a1;
+                                e1 *= a1;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    o[i][0] *= a0;
+                                    o[i][1] *= a1;
+                                    o[i][2] *= a0;
+                                    o[i][3] *= a1;
+                                }
+                            }
+                            // P times 2^8, and the weight of this tile's product
+                            const float na = ma == ninf ? 0.f : 8.f - ma, nb = mb == ninf ? 0.f : 8.f - mb;
+                            float wa = ma == ninf ? 0.f : ex2(-na - m0), wb = mb == ninf ? 0.f : ex2(-nb - m1);
+                            uint32_t bh[2], bl[2];
+                            float ta = 0.f, tb = 0.f;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float p0 = ex2(fmaf(y[h][0], k0[h], na)), p1 = ex2(fmaf(y[h][1], k1[h], nb));
+                                const float p2 = ex2(fmaf(y[h][2], k0[h], na)), p3 = ex2(fmaf(y[h][3], k1[h], nb));
+                                ta += p0 + p2;
+                                tb += p1 + p3;
+                                uint32_t ha, la, hb, lb;
+                                split_e4m3(p0 * fac[h], p2 * fac[h], &ha, &la);
+                                split_e4m3(p1 * fac[h], p3 * fac[h], &hb, &lb);
+                                bh[h] = transpose8x8(__byte_perm(ha, hb, 0x5410));
+                                bl[h] = transpose8x8(__byte_perm(la, lb, 0x5410));
+                            }
+                            {
+                                const float d0 = fmaf(ta, wa, -e0), d1 = fmaf(tb, wb, -e1);
+                                const float s0 = l0 + d0, s1 = l1 + d1;
+                                e0 = (s0 - l0) - d0;
+                                e1 = (s1 - l1) - d1;
+                                l0 = s0;
+                                l1 = s1;
+                            }
+                            wa *= vs;
+                            wb *= vs;
+                            // four elements of d of four keys are a 4 x 4 block of bytes; row r of the fragment of tile i is
+                            // d = 16 r + 2 i, row r + 8 the next
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t f[2][4];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t u0 = (&w8[4 * h].x)[i], u1 = (&w8[4 * h + 1].x)[i];
+                                    const uint32_t u2 = (&w8[4 * h + 2].x)[i], u3 = (&w8[4 * h + 3].x)[i];
+                                    const uint32_t a0 = __byte_perm(u0, u1, 0x5140), a1 = __byte_perm(u2, u3, 0x5140);
+                                    const uint32_t a2 = __byte_perm(u0, u1, 0x7362), a3 = __byte_perm(u2, u3, 0x7362);
+                                    f[h][0] = __byte_perm(a0, a1, 0x5410);
+                                    f[h][1] = __byte_perm(a0, a1, 0x7632);
+                                    f[h][2] = __byte_perm(a2, a3, 0x5410);
+                                    f[h][3] = __byte_perm(a2, a3, 0x7632);
+                                }
+#pragma unroll
+                                for (int z = 0; z < 2; ++z) {
+                                    float d[4];
+                                    mma_e4m3_16832_first(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bh[0], bh[1]);
+                                    mma_e4m3_16832(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bl[0], bl[1]);
+                                    float* oo = o[2 * i + z];
+                                    oo[0] = fmaf(d[0], wa, oo[0]);
+                                    oo[1] = fmaf(d[1], wb, oo[1]);
+                                    oo[2] = fmaf(d[2], wa, oo[2]);
+                                    oo[3] = fmaf(d[3], wb, oo[3]);
+                                }
                             }
                         }
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.empty[slot]));
                 }
-                __syncwarp();
-                issue();
-            }
 
-            // join the warps: row n of the segment by warp n, 32 columns at a time
+                // join the warps: row n of the segment by warp n, 32 columns at a time
 #pragma unroll
-            for (int sh = 4; sh <= 16; sh <<= 1) {
-                l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
-                l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
-            }
-            __syncthreads();                               // the last segment's values have been read
-            if (lane < 4) {
-                sm.ml[warp][2 * c] = make_float2(m0, l0);
-                sm.ml[warp][2 * c + 1] = make_float2(m1, l1);
-            }
-            __syncthreads();
-            float M = ninf, L = 0.f, wt[kWarps], res[4];
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm.ml[i][warp].x);
-#pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const float2 x = sm.ml[i][warp];
-                wt[i] = x.x == ninf ? 0.f : ex2(x.x - M);
-                L += x.x == ninf ? x.y : wt[i] * x.y;      // a sum without a maximum is 0 or NaN
-            }
-#pragma unroll
-            for (int part = 0; part < 4; ++part) {
-                if (part) __syncthreads();
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float* x = o[2 * part];
-                    const float* y = o[2 * part + 1];
-                    *reinterpret_cast<float4*>(&sm.o[warp][2 * c + j][4 * r]) = make_float4(x[j], x[2 + j], y[j], y[2 + j]);
+                for (int sh = 4; sh <= 16; sh <<= 1) {
+                    l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
+                    l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
                 }
-                __syncthreads();
-                float x = 0.f;
-#pragma unroll
-                for (int i = 0; i < kWarps; ++i) x += wt[i] * sm.o[i][warp][lane];
-                res[part] = x;                             // d = 16 (lane / 4) + 4 part + lane % 4
-            }
-            if (warp < n_rows) {
-                const int d0 = 16 * (lane >> 2) + (lane & 3);
-                if (seg_a == g0 && seg_b == g1) {
-                    const int64_t row = (t0 + warp / G) * hq + head * G + warp % G;
-                    const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) a.out[row * kPagedD + d0 + 4 * i] = __float2bfloat16_rn(res[i] * inv);
-                    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
-                } else {
-                    const int64_t row = ((int64_t)blockIdx.x * 2 + (seg_a == g0 ? 1 : 0)) * a.rows + warp;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) a.part_o[row * kPagedD + d0 + 4 * i] = res[i];
-                    if (lane == 0) a.part_ml[row] = make_float2(M, L);
+                consumers_sync();                          // the last segment's values have been read
+                if (lane < 4) {
+                    sm.ml[warp][2 * c] = make_float2(m0, l0);
+                    sm.ml[warp][2 * c + 1] = make_float2(m1, l1);
                 }
+                consumers_sync();
+                const int mine = warp & 7;
+                float M = ninf, L = 0.f;
+                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm.ml[i][mine].x);
+                // lane i: the weight of warp i
+                float wt = 0.f;
+                for (int i = 0; i < kWarps; ++i) {
+                    const float2 x = sm.ml[i][mine];
+                    const float y = x.x == ninf ? 0.f : ex2(x.x - M);
+                    L += x.x == ninf ? x.y : y * x.y;      // a sum without a maximum is 0 or NaN
+                    if (lane == i) wt = y;
+                }
+                float res[4];
+#pragma unroll
+                for (int part = 0; part < 4; ++part) {
+                    if (part) consumers_sync();
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float* x = o[2 * part];
+                        const float* y = o[2 * part + 1];
+                        *reinterpret_cast<float4*>(&sm.o[warp][2 * c + j][4 * r]) = make_float4(x[j], x[2 + j], y[j], y[2 + j]);
+                    }
+                    consumers_sync();
+                    float x = 0.f;
+                    if (warp < kDecodeRows)
+#pragma unroll
+                        for (int i = 0; i < kWarps; ++i) x += __shfl_sync(0xffffffffu, wt, i) * sm.o[i][mine][lane];
+                    res[part] = x;                         // d = 16 (lane / 4) + 4 part + lane % 4
+                }
+                if (warp < n_rows) {
+                    const int d0 = 16 * (lane >> 2) + (lane & 3);
+                    if (seg_a == g0 && seg_b == g1) {
+                        const int64_t row = (t0 + (warp >> gs)) * hq + head * G + (warp & (G - 1));
+                        const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) a.out[row * kPagedD + d0 + 4 * i] = __float2bfloat16_rn(res[i] * inv);
+                        if (a.lse && lane == 0) a.lse[row] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
+                    } else {
+                        const int64_t row = ((int64_t)blockIdx.x * 2 + (seg_a == g0 ? 1 : 0)) * a.rows + warp;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) a.part_o[row * kPagedD + d0 + 4 * i] = res[i];
+                        if (lane == 0) a.part_ml[row] = make_float2(M, L);
+                    }
+                }
+                if (seg_a == g0 && seg_b > g1 && live) {
+                    open.t0 = t0;
+                    open.head = head;
+                    open.rows = n_rows;
+                    open.n_more = cta_of_tile(total, n_cta, base + seg_b - 1) - (int)blockIdx.x;
+                }
+                g0 = g1;
             }
-            if (seg_a == g0 && seg_b > g1 && live) {
-                open.t0 = t0;
-                open.head = head;
-                open.rows = n_rows;
-                open.n_more = cta_of_tile(total, n_cta, base + seg_b - 1) - (int)blockIdx.x;
-            }
-            g0 = g1;
         }
-        it += n_mine;
+        done += count;
         base += in_window;
         __syncthreads();
     }
     if (tid == 0) a.open[blockIdx.x] = open;
-    __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (*abort_flag && lane == 0) {
-        record_device_error(a.err, MSA_DEV_WAIT_TIMEOUT);
-        // leave no copy in flight: the last phase of each stage
-        for (int i = 0; i < kStages; ++i)
-            if (it > i) mbar_wait_drain(smem_u32(&sm.bar[warp][i]), (uint32_t)((it - 1 - i) / kStages) & 1u);
+    if (*abort_flag) {
+        if (tid == 0) record_device_error(a.err, MSA_DEV_WAIT_TIMEOUT);
+        // leave no copy in flight: each slot's last load
+        if (tid < kSlots && sm.last[tid] > 0) mbar_wait_drain(smem_u32(&sm.full[tid]), (uint32_t)(sm.last[tid] - 1) & 1u);
     }
 }
 
@@ -614,7 +660,7 @@ msa_status launch_paged_decode(const PagedAttnArgs& a, int grid, cudaStream_t s)
             if (dev >= 0 && dev < 64) opted[dev] = true;
         }
     }
-    // the pages as rows of 128 bytes (64 two-byte elements); a box is one tile of keys or of values
+    // the pages as rows of 128 bytes (64 two-byte elements); a box is a tile of keys or of values, or half of one
     CUtensorMap tm{};
     const uint64_t dims[2] = {64, (uint64_t)(a.v.n_pages * 2 * a.v.hkv * a.v.page)};
     const uint64_t strides[1] = {kPagedD};

@@ -169,6 +169,44 @@ def test_attention_ignores_what_lies_behind_the_end(m, page, new):
     _check_attn(c, news, off, q, out, lse, 8, 1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("new", [1, 2, 30, 300])
+def test_attention_over_far_more_keys_than_a_block_holds(m, new, page):
+    """Every ring of buffers goes round many times; the reference is computed in 64 bits on the GPU, bounds as in
+    _check_attn with the largest delta of the case."""
+    lens, hkv, G = [41003, 300, 22222, 9000], 8, 4
+    g = torch.Generator(device="cuda").manual_seed(new + page)
+    counts = [-(-n // page) for n in lens]
+    kv = m.PagedKV.empty(sum(counts), len(lens), max(counts), hkv, page, bounds=False)
+    perm = torch.randperm(sum(counts), generator=g, device="cuda").int()
+    for s, c in enumerate(counts):
+        kv.page_table[s, :c] = perm[sum(counts[:s]):sum(counts[:s]) + c]
+    kv.seq_len.copy_(torch.tensor(lens))
+    kv.pages.copy_((torch.randn(kv.pages.shape, generator=g, device="cuda") * 60).to(torch.float8_e4m3fn))
+    kv.scales.copy_(torch.exp2(torch.randint(-8, -4, kv.scales.shape, generator=g, device="cuda").float()))
+    news = [new, 1, min(new, 7), new]
+    off_d, off = _offsets(news)
+    q = torch.randn((off[-1], hkv * G, D), generator=g, device="cuda").bfloat16()
+    out, lse = m.msa_paged_attn(kv, q, off_d, max(news), want_lse=True)
+    assert m.device_status() == 0
+    for s, n in enumerate(news):
+        ids = kv.page_table[s, :counts[s]].long()
+        x = kv.pages.view(torch.uint8)[ids].view(torch.float8_e4m3fn).double() * kv.scales[ids].double()[..., None, None]
+        for h in range(hkv):
+            k, v = (x[:, i, h].reshape(-1, D)[:lens[s]] for i in range(2))
+            qq = q[off[s]:off[s + 1], h * G:h * G + G].double()
+            z = torch.einsum("tgd,kd->tgk", qq, k) / math.sqrt(D)
+            hide = torch.arange(lens[s], device="cuda") > lens[s] - n + torch.arange(n, device="cuda")[:, None]
+            z.masked_fill_(hide[:, None], -math.inf)
+            p = torch.softmax(z, -1)
+            ref, a = p @ v, p @ v.abs()
+            delta = 2.0 ** -17 / math.sqrt(D) * float((qq.abs().amax(-1).max() * k.abs().sum(-1).max()) * 2)
+            mine = out[off[s]:off[s + 1], h * G:h * G + G].double()
+            assert ((mine - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12 + math.expm1(2 * delta)) * a).all()
+            z = torch.logsumexp(z, -1)
+            assert ((lse[off[s]:off[s + 1], h * G:h * G + G].double() - z).abs() <= delta + 2.0 ** -20 * (z.abs() + 20)).all()
+
+
 @pytest.mark.parametrize("new", [1, 10])
 def test_attention_of_many_sequences(m, new):
     """More sequences than any kernel looks at together, most of them short, some with nothing new."""
