@@ -8,37 +8,56 @@
 #include <algorithm>
 
 #include "kernels.cuh"
+#include "mma.cuh"
 #include "paged.cuh"
 
 namespace msa {
 namespace {
 
-// The combine pass, a programmatic dependent of the attention kernel: block (i, y) joins 16 rows of the segment
-// that starts in CTA i and goes on in later ones, two at a time, in the CTAs' order.
-constexpr int kCombineRows = 16;
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedAttnArgs a) {
+// The combine pass, a programmatic dependent of the attention kernel: warp w of block (i, y) joins row 8 y + w of the
+// segment that starts in CTA i and goes on in later ones, in the CTAs' order, four columns a lane. Up to 32 pieces'
+// maxima and sums come at once, a lane each, and the pieces' rows four at a time: a handful of latencies in all.
+constexpr int kCombineRows = 8;
+__global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const PagedAttnArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const OpenSegment seg = a.open[blockIdx.x];
-    if (seg.n_more == 0) return;
-    const int d = threadIdx.x & 127;
-    const int end = min(seg.rows, (int)(blockIdx.y + 1) * kCombineRows);
-    for (int n = blockIdx.y * kCombineRows + (threadIdx.x >> 7); n < end; n += 2) {
-        const int64_t first = ((int64_t)blockIdx.x * 2 + 1) * a.rows + n;    // slot 1, then slot 0 of the next CTAs
-        float M = -INFINITY;
-        for (int i = 0; i <= seg.n_more; ++i) M = fmaxf(M, a.part_ml[first + (i ? 2 * i - 1 : 0) * a.rows].x);
-        float L = 0.f, x = 0.f;
+    const int n = blockIdx.y * kCombineRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (seg.n_more == 0 || n >= seg.rows) return;
+    // piece 0 is in slot 1 of CTA i, piece j in slot 0 of CTA i + j
+    const int64_t first = (int64_t)blockIdx.x * 2 * a.rows + n;
+    auto row_of = [&](int j) -> int64_t { return first + (int64_t)(j ? 2 * j : 1) * a.rows; };
+    const int pieces = seg.n_more + 1;
+    float M = -INFINITY;
+    for (int j = lane; j < pieces; j += 32) M = fmaxf(M, a.part_ml[row_of(j)].x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < pieces; j0 += 32) {
+        const float2 ml = j0 + lane < pieces ? a.part_ml[row_of(j0 + lane)] : make_float2(-INFINITY, 0.f);
+        const bool none = ml.x == -INFINITY;               // a sum without a maximum is 0 or NaN
+        const float w = none ? 0.f : exp2f(ml.x - M), part = none ? ml.y : w * ml.y;
+        const int m = min(32, pieces - j0);
 #pragma unroll 4
-        for (int i = 0; i <= seg.n_more; ++i) {
-            const int64_t row = first + (i ? 2 * i - 1 : 0) * a.rows;
-            const float2 ml = a.part_ml[row];
-            const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-            L += ml.x == -INFINITY ? ml.y : w * ml.y;                          // a sum without a maximum is 0 or NaN
-            if (ml.x != -INFINITY) x += w * a.part_o[row * kPagedD + d];
+        for (int j = 0; j < m; ++j) {
+            const float4 y = reinterpret_cast<const float4*>(a.part_o + row_of(j0 + j) * kPagedD)[lane];
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            L += __shfl_sync(0xffffffffu, part, j);
+            if (wj != 0.f) {                               // a piece without a key may hold anything
+                x.x = fmaf(wj, y.x, x.x);
+                x.y = fmaf(wj, y.y, x.y);
+                x.z = fmaf(wj, y.z, x.z);
+                x.w = fmaf(wj, y.w, x.w);
+            }
         }
-        const int64_t row = (seg.t0 + n / a.G) * (a.v.hkv * a.G) + seg.head * a.G + n % a.G;
-        a.out[row * kPagedD + d] = __float2bfloat16_rn(L == 0.f ? 0.f : x * (seg.unit / L));
-        if (a.lse && d == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     }
+    const int64_t row = (seg.t0 + n / a.G) * (a.v.hkv * a.G) + seg.head * a.G + n % a.G;
+    const float inv = L == 0.f ? 0.f : seg.unit / L;       // NaN where a query row holds one
+    uint2 u;
+    u.x = pack_bf16(x.x * inv, x.y * inv);
+    u.y = pack_bf16(x.z * inv, x.w * inv);
+    reinterpret_cast<uint2*>(a.out + row * kPagedD)[lane] = u;
+    if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 constexpr int kSms = 148;
@@ -144,7 +163,7 @@ extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((rows + kCombineRows - 1) / kCombineRows));
-        cfg.blockDim = dim3(256);
+        cfg.blockDim = dim3(32 * kCombineRows);
         cfg.stream = s;
         cfg.attrs = attr;
         cfg.numAttrs = 1;

@@ -13,9 +13,9 @@
 //    sum of magnitudes (2^-24 would be a rounding, the tensor cores may truncate), 2^-18 over 16 steps. Bound
 //    by the bytes of the bounds: 512 per page and kv head.
 // 2. page_pick_kernel: one block per (token, kv head). T = the k-th best fp32 score, by its bits from the top, two
-//    at a time (counting only: no histogram, whose counters equal leading bits would all hit). Pages above
-//    T + 2 E are in, those below T - 2 E are out, and where more than k remain those in between are summed again
-//    in 64 bits and ranked.
+//    at a time (counting only: no histogram, whose counters equal leading bits would all hit), among the scores
+//    that reach the k-th best of the 256 threads' maxima where k is at most 256. Pages above T + 2 E are in, those
+//    below T - 2 E are out, and where more than k remain those in between are summed again in 64 bits and ranked.
 #include <algorithm>
 #include <mutex>
 
@@ -44,6 +44,7 @@ constexpr int kScorePages = 128;   // pages per block of the scoring kernel, 16 
 constexpr int kGroup = 8;          // query row tiles staged together
 constexpr int kPickThreads = 256;
 constexpr int kNear = kPickThreads;            // border pages that are ranked in shared memory
+constexpr int kCand = 1023;                    // candidates for the k best that are kept there
 constexpr size_t kPickSmem = 200 * 1024;       // of scores; more pages are all summed in 64 bits
 constexpr float kNoPage = -3.402823466e38f;    // score of a page that is not there
 
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(256) page_score_kernel(const SelectArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int s = blockIdx.x / a.chunks, chunk = blockIdx.x - s * a.chunks;
     const int g = blockIdx.y / a.token_parts, part = blockIdx.y - g * a.token_parts;
-    const int G = a.G, hq = v.hkv * G;
+    const int G = a.G, gs = 31 - __clz(G), hq = v.hkv * G;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     SeqSpan sp;
     if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) || sp.n_new == 0) return;
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(256) page_score_kernel(const SelectArgs a) {
             const int row = (rt + warp) * 8 + r;
             const bool valid = row < sp.n_new * G;
             const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + ((sp.t0 + (valid ? row / G : 0)) * hq + g * G + (valid ? row % G : 0)) * kPagedD) + c;
+                a.q + ((sp.t0 + (valid ? row >> gs : 0)) * hq + g * G + (valid ? row & (G - 1) : 0)) * kPagedD) + c;
             const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -125,36 +126,44 @@ __global__ void __launch_bounds__(256) page_score_kernel(const SelectArgs a) {
             }
         }
         __syncthreads();
-        for (int t = 0; t < n_rt; ++t) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
+        // two row tiles at a time: two chains of products
+        for (int t0 = 0; t0 < n_rt; t0 += 2) {
+            float x2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint4 b = s_q[t][i][lane];
+                const uint4 b0 = s_q[t0][i][lane], b1 = s_q[t0 + 1][i][lane];      // kGroup is even
                 const uint32_t a0[4] = {w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y};
                 const uint32_t a1[4] = {w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w};
-                mma_bf16_16816(x, a0, b.x, b.y);
-                mma_bf16_16816(x, a1, b.z, b.w);
+                mma_bf16_16816(x2[0], a0, b0.x, b0.y);
+                mma_bf16_16816(x2[1], a0, b1.x, b1.y);
+                mma_bf16_16816(x2[0], a1, b0.z, b0.w);
+                mma_bf16_16816(x2[1], a1, b1.z, b1.w);
             }
             // x: page r, rows 2 c and 2 c + 1; page r + 8, the same rows. The largest of a token's rows:
-            const int row = (rt + t) * 8 + 2 * c;
-            if (G == 1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = p0 + 16 * warp + 8 * (i >> 1) + r, tok = row + (i & 1);
-                    if (p < n_pages && tok < sp.n_new)
-                        reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] =
-                            there[i >> 1] ? x[i] : kNoPage;
+            for (int t = 0; t < 2; ++t) {
+                const float* x = x2[t];
+                const int row = (rt + t0 + t) * 8 + 2 * c;
+                const bool mine = t0 + t < n_rt;
+                if (G == 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int p = p0 + 16 * warp + 8 * (i >> 1) + r, tok = row + (i & 1);
+                        if (mine && p < n_pages && tok < sp.n_new)
+                            reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] =
+                                there[i >> 1] ? x[i] : kNoPage;
+                    }
+                    continue;
                 }
-                continue;
-            }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float y = fmaxf(x[2 * h], x[2 * h + 1]);
-                if (G >= 4) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-                if (G >= 8) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-                const int p = p0 + 16 * warp + 8 * h + r, tok = row / G;
-                if (row % G == 0 && p < n_pages && tok < sp.n_new)
-                    reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] = there[h] ? y : kNoPage;
+                for (int h = 0; h < 2; ++h) {
+                    float y = fmaxf(x[2 * h], x[2 * h + 1]);
+                    if (G >= 4) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+                    if (G >= 8) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                    const int p = p0 + 16 * warp + 8 * h + r, tok = row >> gs;
+                    if (mine && (row & (G - 1)) == 0 && p < n_pages && tok < sp.n_new)
+                        reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] = there[h] ? y : kNoPage;
+                }
             }
         }
     }
@@ -183,7 +192,32 @@ struct PickSmem {
     int hist[256];
     unsigned long long prefix;
     int want, done;
+    uint32_t top[kPickThreads], cand[kCand];
+    int cand_page[kCand], n_cand, n_near, n_in;
+    uint32_t floor;
 };
+
+// The k-th largest of v[0 .. n), n < 1024, by one warp: two bits at a time from the top, three counts in one sum.
+__device__ __forceinline__ uint32_t warp_kth(const uint32_t* v, int n, int k) {
+    const int lane = threadIdx.x & 31;
+    uint32_t x[4];                                         // the first 128 stay in registers
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < n ? v[lane + 32 * i] : 0;
+    uint32_t T = 0;
+    for (int shift = 30; shift >= 0; shift -= 2) {
+        const uint32_t t1 = T | (1u << shift), t2 = T | (2u << shift), t3 = T | (3u << shift);
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c += (x[i] >= t1) + ((x[i] >= t2) << 10) + ((x[i] >= t3) << 20);
+        for (int i = lane + 128; i < n; i += 32) {
+            const uint32_t y = v[i];
+            c += (y >= t1) + ((y >= t2) << 10) + ((y >= t3) << 20);
+        }
+        c = __reduce_add_sync(0xffffffffu, c);
+        T = (int)(c >> 20) >= k ? t3 : (int)(c >> 10 & 1023) >= k ? t2 : (int)(c & 1023) >= k ? t1 : T;
+    }
+    return T;
+}
 
 // Sum over the block of three counts per thread; `turn` alternates, so that one barrier a call is enough.
 __device__ __forceinline__ int3 block_count(PickSmem& sm, int turn, int x, int y, int z) {
@@ -375,8 +409,12 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     const float* score = reinterpret_cast<const float*>(row64);
     const float* bmax = a.bmax + (sp.t0 * v.hkv + g) * v.max_pages;
     float bm = 0.f;
+    uint32_t mine = 0;
+#pragma unroll 8
     for (int i = tid; i < n; i += kPickThreads) {
-        s_score[i] = i >= newest ? 0xFFFFFFFFu : ordered32(score[i]);
+        const uint32_t x = i >= newest ? 0xFFFFFFFFu : ordered32(score[i]);
+        s_score[i] = x;
+        mine = max(mine, x);
         const float b = bmax[i];
         bm = b <= bm ? bm : b;                             // a NaN stays
     }
@@ -405,6 +443,112 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     }
     const float E = qs * bm * 6.103515625e-05f + 1e-36f;   // 2^-14, and what underflow may lose
 
+    // Few candidates first, where k allows: at least k scores reach the k-th best of the threads' own maxima.
+    const bool few = a.k <= kPickThreads;
+    if (few) {
+        sm.top[tid] = mine;
+        if (tid == 0) sm.n_cand = 0;
+        __syncthreads();
+        if (warp == 0) {
+            const uint32_t t = warp_kth(sm.top, kPickThreads, a.k);
+            if (lane == 0) sm.floor = t;
+        }
+        __syncthreads();
+        const float f = unordered32(sm.floor);
+        // everything near the border, wherever above it that turns out to be, and all that compares with nothing
+        const uint32_t floor = sm.floor == 0xFFFFFFFFu ? sm.floor : (f - 2.f * E > -3.402823466e38f) ? ordered32(f - 2.f * E) : 0u;
+        for (int i = tid; i < n; i += kPickThreads) {
+            const uint32_t x = s_score[i];
+            const bool yes = x >= floor || x == 0;
+            const unsigned m = __ballot_sync(__activemask(), yes);
+            if (yes) {
+                const int leader = __ffs(m) - 1;
+                int at = 0;
+                if (lane == leader) at = atomicAdd(&sm.n_cand, __popc(m));
+                at = __shfl_sync(m, at, leader) + __popc(m & ((1u << lane) - 1));
+                if (at < kCand) {
+                    sm.cand[at] = x;
+                    sm.cand_page[at] = i;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (few && sm.n_cand <= kCand) {
+        const int n_cand = sm.n_cand;
+        if (warp == 0) {
+            const uint32_t t = warp_kth(sm.cand, n_cand, a.k);
+            if (lane == 0) {
+                sm.floor = t;
+                sm.n_near = sm.n_in = 0;
+            }
+        }
+        const int words = (n + 31) / 32;                   // a bit per page, in the place of the scores
+        __syncthreads();
+        uint32_t* bits = s_score;
+        for (int i = tid; i < words; i += kPickThreads) bits[i] = 0;
+        const uint32_t T = sm.floor;
+        const float edge = unordered32(T), low = edge - 2.f * E, high = edge + 2.f * E;
+        __syncthreads();
+        for (int i = tid; i < n_cand; i += kPickThreads) {
+            const uint32_t x = sm.cand[i];
+            const float y = unordered32(x);
+            const int p = sm.cand_page[i];
+            if (x == 0xFFFFFFFFu || (T != 0xFFFFFFFFu && x != 0 && y > high)) {
+                atomicOr(&bits[p >> 5], 1u << (p & 31));
+                atomicAdd(&sm.n_in, 1);
+            } else if (T != 0xFFFFFFFFu && !(x != 0 && y < low)) {
+                const int at = atomicAdd(&sm.n_near, 1);
+                if (at < kNear) sm.near[at] = p;
+            }
+        }
+        __syncthreads();
+        const int want = a.k - sm.n_in, n_near = sm.n_near;
+        if (n_near <= kNear) {
+            if (n_near > want) {
+                for (int j = warp; j < n_near; j += kPickThreads / 32) {
+                    const unsigned long long x = exact(sm.near[j]);
+                    if (lane == 0) sm.key[j] = x;
+                }
+                __syncthreads();
+            }
+            if (tid < n_near) {
+                const int p = sm.near[tid];
+                int rank = 0;
+                if (n_near > want) {
+                    const unsigned long long x = sm.key[tid];
+                    for (int j = 0; j < n_near; ++j) {
+                        const unsigned long long y = sm.key[j];
+                        rank += y > x || (y == x && sm.near[j] < p);
+                    }
+                }
+                if (rank < want) atomicOr(&bits[p >> 5], 1u << (p & 31));
+            }
+            __syncthreads();
+            // the set bits in ascending order: each thread a run of words
+            const int run = (words + kPickThreads - 1) / kPickThreads;
+            const int w0 = min(words, tid * run), w1 = min(words, w0 + run);
+            int c = 0;
+            for (int i = w0; i < w1; ++i) c += __popc(bits[i]);
+            int up = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, up, o);
+                if (lane >= o) up += y;
+            }
+            if (lane == 31) sm.cnt[0][0][warp] = up;
+            __syncthreads();
+            int at = up - c;
+            for (int i = 0; i < warp; ++i) at += sm.cnt[0][0][i];
+            for (int i = w0; i < w1; ++i)
+                for (uint32_t m = bits[i]; m; m &= m - 1) sel[at++] = i * 32 + __ffs(m) - 1;
+            return;
+        }
+        // too many: the scores again, for the passes over all of them
+        __syncthreads();
+        for (int i = tid; i < n; i += kPickThreads) s_score[i] = i >= newest ? 0xFFFFFFFFu : ordered32(score[i]);
+        __syncthreads();
+    }
     uint32_t T = 0;                                        // the k-th largest, two bits at a time
     for (int shift = 30, turn = 0; shift >= 0; shift -= 2, turn ^= 1) {
         const uint32_t t1 = T | (1u << shift), t2 = T | (2u << shift), t3 = T | (3u << shift);
@@ -528,7 +672,7 @@ extern "C" msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa
         // blocks for every SM: where pages and heads do not give enough, a sequence's query rows are parted too
         const int64_t blocks = (int64_t)a.chunks * kv->n_seq * kv->hkv;
         const int64_t groups = ((int64_t)std::min<int64_t>(max_new, n_tok) * a.G + 8 * kGroup - 1) / (8 * kGroup);
-        a.token_parts = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 592 / std::max<int64_t>(blocks, 1), 65535 / kv->hkv}));
+        a.token_parts = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 1184 / std::max<int64_t>(blocks, 1), 65535 / kv->hkv}));
         page_score_kernel<<<dim3((unsigned)(a.chunks * kv->n_seq), (unsigned)(kv->hkv * a.token_parts)), 256, 0, s>>>(a);
         MSA_LAUNCH_CHECK();
     }
