@@ -120,7 +120,10 @@ struct OpenSegment {         // the segment that starts in a CTA and ends in a l
 };
 
 // CTA i of n takes tiles total * i / n .. total * (i + 1) / n - 1; the one that holds tile x:
-__device__ __forceinline__ int64_t cta_first(int64_t total, int n, int i) { return total * i / n; }
+__device__ __forceinline__ int64_t cta_first(int64_t total, int n, int i) {
+    if (total < (1 << 23)) return (uint32_t)total * (uint32_t)i / (uint32_t)n;       // n < 256; a 64-bit division is slow
+    return total * i / n;
+}
 __device__ __forceinline__ int cta_of_tile(int64_t total, int n, int64_t x) {
     int i = (int)(x * n / total);
     while (cta_first(total, n, i + 1) <= x) ++i;

@@ -49,13 +49,13 @@ constexpr int kFull = 16 + 256 * 16;
 
 struct DecodeSmem {
     uint8_t ring[kSlots][kTileBytes];
-    float o[kWarps][kDecodeRows][32];
+    float o[kWarps][kDecodeRows][64];
     float2 ml[kWarps][kDecodeRows];
     TileInfo info[kSlots];
     uint64_t full[kSlots], empty[kSlots];
     int last[kSlots];                                      // loads of a slot so far
     long long pre[kWindow + 1];                            // tiles before each sequence of the window
-    int64_t t0[kWindow];
+    int64_t t0[kWindow], first[kWindow];
     int n_new[kWindow], len[kWindow];
     long long scan[kWarps];
     int abort_flag;
@@ -131,6 +131,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     const int per_page = pairs ? 1 : page / kDecodeTile;
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
+    // the combine pass may be launched: it waits for this grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) sm.abort_flag = 0;
     if (tid < kSlots) {
         mbar_init(smem_u32(&sm.full[tid]), 1);
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
 
     // tiles of all sequences: a thread per sequence of the window
     const int n_windows = LIST ? 1 : (v.n_seq + kWindow - 1) / kWindow;
+    const bool at_hand = LIST && v.n_seq <= kWindow;       // the offsets and lengths of all sequences in shared memory
     auto load_window = [&](int w) -> long long {
         const int s = w * kWindow + tid;
         SeqSpan sp{0, 0, 0};
@@ -156,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
         __syncthreads();
         if (tid < kWindow) {
             sm.t0[tid] = sp.t0;
+            if (LIST && s < v.n_seq) sm.first[tid] = a.tok_off[s];
             sm.n_new[tid] = sp.n_new;
             sm.len[tid] = sp.len;
             if (lane == 31) sm.scan[warp] = up;
@@ -175,8 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     long long total = 0, first_total = 0;
     const int list_tiles = !LIST ? 1 : pairs ? (a.k + 1) / 2 : a.k * per_page;
     if (LIST) {
+        if (at_hand) load_window(0);
+        else __syncthreads();
         total = first_total = a.n_tok * v.hkv * (long long)list_tiles;
-        __syncthreads();
     } else {
         for (int w = n_windows - 1; w >= 0; --w) {
             first_total = load_window(w);
@@ -186,7 +191,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     const int n_cta = (int)min((long long)gridDim.x, (total + kMinDecodeTiles - 1) / kMinDecodeTiles);
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         return;
     }
     const long long my_a = cta_first(total, n_cta, blockIdx.x), my_b = cta_first(total, n_cta, blockIdx.x + 1);
@@ -204,6 +208,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
         const int n_win = LIST ? 0 : min(kWindow, v.n_seq - w * kWindow);
         const int count = (int)(B - A);
 
+        // the sequence of packed row t; false where there is none
+        auto seq_of = [&](long long t, int* s, SeqSpan* sp, int* err) -> bool {
+            int lo = 0, n = v.n_seq;
+            while (n > 1) {                                // the last that starts at or before t
+                const int h = n / 2;
+                if ((at_hand ? sm.first[lo + h] : a.tok_off[lo + h]) <= t) {
+                    lo += h;
+                    n -= h;
+                } else {
+                    n = h;
+                }
+            }
+            *s = lo;
+            if (at_hand) {                                 // a sequence that contradicts itself has no tokens here
+                sp->t0 = sm.t0[lo];
+                sp->n_new = sm.n_new[lo];
+                sp->len = sm.len[lo];
+            } else if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, lo, sp, err)) {
+                return false;
+            }
+            return t >= sp->t0 && t < sp->t0 + sp->n_new;
+        };
         if (warp == kWarps) {
             // ------------------------------------------------------------------ loader: a lane per tile
             // as many at a time as there are slots: two lanes waiting for the same slot, a phase apart, could not
@@ -212,9 +238,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 const int i = lane < kSlots ? i0 + lane : count;
                 TileInfo ti;
                 int row[2] = {0, 0}, rows[2] = {0, 0};
-                float sv[2] = {1.f, 1.f};
+                int64_t slabs[2] = {-1, -1};
                 ti.key[0] = ti.key[1] = 0;
-                ti.sk[0] = ti.sk[1] = 1.f;
+                int32_t listed[2] = {-1, -1};              // asked for before the sequence is looked for
+                if (LIST && i < count) {
+                    const long long g = A + i, seg = g / list_tiles;
+                    const int at = (int)(g - seg * list_tiles), li = pairs ? 2 * at : at / per_page;
+                    listed[0] = a.sel[seg * a.k + li];
+                    if (pairs && li + 1 < a.k) listed[1] = a.sel[seg * a.k + li + 1];
+                }
                 auto look_up = [&]() {
                     const long long g = A + i;
                     int s, head, seen, at;                 // at: the tile's number in its segment
@@ -224,19 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                         at = (int)(g - seg * list_tiles);
                         const long long t = seg / v.hkv;
                         head = (int)(seg - t * v.hkv);
-                        int lo = 0, n = v.n_seq;           // the last sequence that starts at or before t
-                        while (n > 1) {
-                            const int h = n / 2;
-                            if (a.tok_off[lo + h] <= t) {
-                                lo += h;
-                                n -= h;
-                            } else {
-                                n = h;
-                            }
-                        }
-                        s = lo;
                         SeqSpan sp;
-                        if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, a.err) || t < sp.t0 || t >= sp.t0 + sp.n_new) return;
+                        if (!seq_of(t, &s, &sp, a.err)) return;
                         seen = sp.len - sp.n_new + (int)(t - sp.t0) + 1;
                     } else {
                         const int lo = find(sm.pre, n_win, g);
@@ -256,15 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                             if (rows[0] == 0) break;
                             ti.key[1] = ti.key[0] + 16;
                             rows[1] = max(0, min(16, seen - ti.key[1]));
-                            ti.sk[1] = ti.sk[0];
-                            sv[1] = sv[0];
                             break;
                         }
                         if (LIST) {
-                            const int li = pairs ? 2 * at + h : at / per_page;
-                            if (li >= a.k) break;
-                            p = a.sel[seg * a.k + li];
-                            if (!pairs) row0 = (at - li * per_page) * kDecodeTile;
+                            p = listed[h];
+                            if (!pairs) row0 = (at - at / per_page * per_page) * kDecodeTile;
                             if (p == -1) continue;
                             if (p < 0 || p >= n_pages) {
                                 record_device_error(a.err, MSA_DEV_BAD_INDEX);
@@ -284,18 +301,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                         const int64_t slab = (int64_t)pid * 2 * v.hkv + head;
                         ti.key[h] = (p << v.shift) + row0;
                         rows[h] = max(0, min(16, seen - ti.key[h]));
-                        ti.sk[h] = v.scales[slab];
-                        sv[h] = v.scales[slab + v.hkv];
                         row[h] = (int)(slab * page) + row0;
+                        slabs[h] = slab;
                     }
                 };
                 if (i < count) look_up();
-                if (rows[0] == 0) sv[0] = sv[1];
-                if (rows[1] == 0) sv[1] = sv[0];
-                ti.vs = fmaxf(sv[0], sv[1]);
-                ti.fac[0] = sv[0] / ti.vs;
-                ti.fac[1] = sv[1] / ti.vs;
                 ti.rows = rows[0] + 256 * rows[1];
+                float sk[2] = {1.f, 1.f}, sv[2] = {1.f, 1.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (slabs[h] >= 0) {                   // used after the copies have been issued
+                        sk[h] = v.scales[slabs[h]];
+                        sv[h] = v.scales[slabs[h] + v.hkv];
+                    }
                 // each lane brings its tile in as soon as the slot is free
                 const int n = done + i, slot = n % kSlots;      // distinct for the lanes with a tile
                 const uint32_t full = smem_u32(&sm.full[slot]), empty = smem_u32(&sm.empty[slot]), dst = smem_u32(sm.ring[slot]);
@@ -303,11 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 const uint64_t t_start = globaltimer();
                 for (uint32_t polls = 0; __any_sync(0xffffffffu, pending); ++polls) {
                     if (pending && mbar_test(empty, ((uint32_t)(n / kSlots) & 1u) ^ 1u)) {
-                        sm.info[slot] = ti;
                         sm.last[slot] = n / kSlots + 1;
                         // a box is 32 rows, or where pages have 16, 16
                         const bool one = rows[0] > 0, two = pairs && rows[1] > 0;
-                        mbar_expect_tx(full, (one ? (pairs ? kTileBytes / 2 : kTileBytes) : 0) + (two ? kTileBytes / 2 : 0));
                         if (one) {
                             tma_load_2d(dst, &tm, 0, row[0], full);
                             tma_load_2d(dst + kTileBytes / 2, &tm, 0, row[0] + v.hkv * page, full);
@@ -316,6 +332,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                             tma_load_2d(dst + 2048, &tm, 0, row[1], full);
                             tma_load_2d(dst + kTileBytes / 2 + 2048, &tm, 0, row[1] + v.hkv * page, full);
                         }
+                        if (!pairs) {
+                            sk[1] = sk[0];
+                            sv[1] = sv[0];
+                        }
+                        if (rows[0] == 0) sv[0] = sv[1];
+                        if (rows[1] == 0) sv[1] = sv[0];
+                        ti.sk[0] = sk[0];
+                        ti.sk[1] = sk[1];
+                        ti.vs = fmaxf(sv[0], sv[1]);
+                        ti.fac[0] = sv[0] / ti.vs;
+                        ti.fac[1] = sv[1] / ti.vs;
+                        sm.info[slot] = ti;
+                        // the arrival, without which the phase cannot end however many bytes are in
+                        mbar_expect_tx(full, (one ? (pairs ? kTileBytes / 2 : kTileBytes) : 0) + (two ? kTileBytes / 2 : 0));
                         pending = false;
                     }
                     if ((polls & 63) == 63) {
@@ -347,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                     head = (int)(seg - t0 * v.hkv);
                     seg_a = seg * list_tiles;
                     seg_b = seg_a + list_tiles;
-                    const int s = seq_of_token(a.tok_off, v.n_seq, t0);
+                    int s;
                     SeqSpan sp;
-                    live = seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) && t0 >= sp.t0 && t0 < sp.t0 + sp.n_new;
+                    live = seq_of(t0, &s, &sp, nullptr);
                     len = sp.len - sp.n_new + (int)(t0 - sp.t0) + 1;
                     n_new = 1;
                 } else {
@@ -578,46 +608,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                     sm.ml[warp][2 * c + 1] = make_float2(m1, l1);
                 }
                 consumers_sync();
+                // lane i: warp i's maximum, sum and weight
                 const int mine = warp & 7;
-                float M = ninf, L = 0.f;
-                for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sm.ml[i][mine].x);
-                // lane i: the weight of warp i
-                float wt = 0.f;
-                for (int i = 0; i < kWarps; ++i) {
-                    const float2 x = sm.ml[i][mine];
-                    const float y = x.x == ninf ? 0.f : ex2(x.x - M);
-                    L += x.x == ninf ? x.y : y * x.y;      // a sum without a maximum is 0 or NaN
-                    if (lane == i) wt = y;
-                }
-                float res[4];
+                const float2 ml = lane < kWarps ? sm.ml[lane][mine] : make_float2(ninf, 0.f);
+                float M = ml.x;
 #pragma unroll
-                for (int part = 0; part < 4; ++part) {
+                for (int sh = 16; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+                const float wt = ml.x == ninf ? 0.f : ex2(ml.x - M);
+                float L = ml.x == ninf ? ml.y : wt * ml.y;             // a sum without a maximum is 0 or NaN
+#pragma unroll
+                for (int sh = 16; sh >= 1; sh >>= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
+                float2 res[2];                                         // d = 16 (lane / 4) + 8 part + 2 (lane % 4) and the next
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
                     if (part) consumers_sync();
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float* x = o[2 * part];
-                        const float* y = o[2 * part + 1];
-                        *reinterpret_cast<float4*>(&sm.o[warp][2 * c + j][4 * r]) = make_float4(x[j], x[2 + j], y[j], y[2 + j]);
-                    }
-                    consumers_sync();
-                    float x = 0.f;
-                    if (warp < kDecodeRows)
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int i = 0; i < kWarps; ++i) x += __shfl_sync(0xffffffffu, wt, i) * sm.o[i][mine][lane];
-                    res[part] = x;                         // d = 16 (lane / 4) + 4 part + lane % 4
+                        for (int i = 0; i < 2; ++i) {
+                            const float* x = o[4 * part + 2 * i];
+                            const float* y = o[4 * part + 2 * i + 1];
+                            *reinterpret_cast<float4*>(&sm.o[warp][2 * c + j][8 * r + 4 * i]) =
+                                make_float4(x[j], x[2 + j], y[j], y[2 + j]);
+                        }
+                    consumers_sync();
+                    res[part] = make_float2(0.f, 0.f);
+                    if (warp < n_rows) {
+#pragma unroll
+                        for (int i = 0; i < kWarps; ++i) {
+                            const float2 x = *reinterpret_cast<const float2*>(&sm.o[i][mine][2 * lane]);
+                            const float y = __shfl_sync(0xffffffffu, wt, i);
+                            res[part].x = fmaf(y, x.x, res[part].x);
+                            res[part].y = fmaf(y, x.y, res[part].y);
+                        }
+                    }
                 }
                 if (warp < n_rows) {
-                    const int d0 = 16 * (lane >> 2) + (lane & 3);
+                    const int d0 = 16 * (lane >> 2) + 2 * (lane & 3);
                     if (seg_a == g0 && seg_b == g1) {
                         const int64_t row = (t0 + (warp >> gs)) * hq + head * G + (warp & (G - 1));
                         const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) a.out[row * kPagedD + d0 + 4 * i] = __float2bfloat16_rn(res[i] * inv);
+                        for (int i = 0; i < 2; ++i)
+                            *reinterpret_cast<uint32_t*>(a.out + row * kPagedD + d0 + 8 * i) = pack_bf16(res[i].x * inv, res[i].y * inv);
                         if (a.lse && lane == 0) a.lse[row] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
                     } else {
                         const int64_t row = ((int64_t)blockIdx.x * 2 + (seg_a == g0 ? 1 : 0)) * a.rows + warp;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) a.part_o[row * kPagedD + d0 + 4 * i] = res[i];
+                        for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(a.part_o + row * kPagedD + d0 + 8 * i) = res[i];
                         if (lane == 0) a.part_ml[row] = make_float2(M, L);
                     }
                 }
@@ -635,7 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
         __syncthreads();
     }
     if (tid == 0) a.open[blockIdx.x] = open;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (*abort_flag) {
         if (tid == 0) record_device_error(a.err, MSA_DEV_WAIT_TIMEOUT);
         // leave no copy in flight: each slot's last load

@@ -173,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     const int tpb = (SPLIT ? kRowsTile : 2 * kRowsTile) / G;       // tokens of a row block
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
+    // the combine pass may be launched: it waits for this grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (tid == 0) {
         for (int i = 0; i < kKStages; ++i) mbar_init(smem_u32(&sm.k_full[i]), 1), mbar_init(smem_u32(&sm.k_empty[i]), 1);
@@ -232,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
         if (alloc) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         return;
     }
     __syncthreads();
@@ -842,7 +843,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         }
     }
     __syncthreads();
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (*abort_flag) {
         if (tid == 0) record_device_error(a.err, MSA_DEV_WAIT_TIMEOUT);
         if (warp == 1 && lane == 0) {

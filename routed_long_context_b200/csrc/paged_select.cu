@@ -34,22 +34,23 @@ struct SelectArgs {
     int max_new, G, k, recent;
     int32_t* sel;
     unsigned long long* rows;      // [n_tok][hkv][max_pages]: fp32 scores in a row's first half, later 64-bit keys
-    float* bmax;                   // [n_tok][hkv][max_pages], row of a sequence's first token: largest |bound| of a page
+    float* bmax;                   // [n_tok][hkv][chunks], row of a sequence's first token: largest |bound| of 128 pages
     int chunks, token_parts;       // of the scoring grid
     int scores_in_smem;
     int* err;
 };
 
-constexpr int kScorePages = 128;   // pages per block of the scoring kernel, 16 per warp
-constexpr int kGroup = 8;          // query row tiles staged together
+constexpr int kScorePages = 128;   // pages per block of the scoring kernel
+constexpr int kGroup = 8;          // query row tiles staged together, one per warp
 constexpr int kPickThreads = 256;
 constexpr int kNear = kPickThreads;            // border pages that are ranked in shared memory
 constexpr int kCand = 1023;                    // candidates for the k best that are kept there
 constexpr size_t kPickSmem = 200 * 1024;       // of scores; more pages are all summed in 64 bits
 constexpr float kNoPage = -3.402823466e38f;    // score of a page that is not there
 
-__global__ void __launch_bounds__(256) page_score_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) {
     __shared__ uint4 s_q[kGroup][8][32];       // B fragments: [row tile][16-byte piece][lane]
+    __shared__ float s_top[8];
     const PagedView& v = a.v;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     const int s = blockIdx.x / a.chunks, chunk = blockIdx.x - s * a.chunks;
@@ -66,105 +67,119 @@ __global__ void __launch_bounds__(256) page_score_kernel(const SelectArgs a) {
     const int rt0 = part * per, rt1 = min(row_tiles, rt0 + per);
     if (rt0 >= rt1) return;
 
+    // A warp lays out one tile of 8 query rows of a group; its elements are on their way while the group before is
+    // multiplied.
+    uint4 next[4];
+    auto fetch = [&](int rt) {
+        const int row = (rt + warp) * 8 + r;
+        const bool valid = rt + warp < rt1 && row < sp.n_new * G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            a.q + ((sp.t0 + (valid ? row >> gs : 0)) * hq + g * G + (valid ? row & (G - 1) : 0)) * kPagedD) + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) next[i] = valid ? src[4 * i] : make_uint4(0, 0, 0, 0);
+    };
+    fetch(rt0);
     // A: bounds of pages r and r + 8 of the warp's 16; the thread's 16-byte pieces are 4 i + c
     uint4 w[2][8];
     bool there[2];
-    float top[2];
+    int32_t pid[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int p = p0 + 16 * warp + 8 * h + r;
-        there[h] = false;
-        if (p < n_pages) {
-            const int32_t pid = v.table[(int64_t)s * v.max_pages + p];
-            there[h] = pid >= 0 && pid < v.n_pages;
-            if (!there[h] && c == 0) record_device_error(a.err, MSA_DEV_BAD_INDEX);
-            const uint4* b = reinterpret_cast<const uint4*>(v.bounds + ((int64_t)pid * v.hkv + g) * 2 * kPagedD) + c;
+        pid[h] = p < n_pages ? v.table[(int64_t)s * v.max_pages + p] : -1;
+        there[h] = pid[h] >= 0 && pid[h] < v.n_pages;
+        if (p < n_pages && !there[h] && c == 0) record_device_error(a.err, MSA_DEV_BAD_INDEX);
+    }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[h][i] = there[h] ? b[4 * i] : make_uint4(0, 0, 0, 0);
-        } else {
+    for (int h = 0; h < 2; ++h) {
+        const uint4* b = reinterpret_cast<const uint4*>(v.bounds + ((int64_t)pid[h] * v.hkv + g) * 2 * kPagedD) + c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[h][i] = make_uint4(0, 0, 0, 0);
-        }
-        if (part == 0) {
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t u[4] = {w[h][i].x, w[h][i].y, w[h][i].z, w[h][i].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
-            }
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            top[h] = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            if (p < n_pages && c == 0) a.bmax[(sp.t0 * v.hkv + g) * v.max_pages + p] = top[h];
-        }
+        for (int i = 0; i < 8; ++i) w[h][i] = there[h] ? b[4 * i] : make_uint4(0, 0, 0, 0);
     }
 
     for (int rt = rt0; rt < rt1; rt += kGroup) {
         const int n_rt = min(kGroup, rt1 - rt);
         __syncthreads();
-        if (warp < n_rt) {                                 // a warp lays out one tile of 8 query rows
-            const int row = (rt + warp) * 8 + r;
-            const bool valid = row < sp.n_new * G;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + ((sp.t0 + (valid ? row >> gs : 0)) * hq + g * G + (valid ? row & (G - 1) : 0)) * kPagedD) + c;
-            const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 x = valid ? src[4 * i] : make_uint4(0, 0, 0, 0);
-                uint4 neg, pos;
-                const uint32_t* xs = &x.x;
+        for (int i = 0; i < 4; ++i) {
+            uint4 neg, pos;
+            const uint32_t* xs = &next[i].x;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&xs[j]);
-                    const __nv_bfloat162 lo = __hmin2(y, zero), hi = __hmax2(y, zero);
-                    (&neg.x)[j] = *reinterpret_cast<const uint32_t*>(&lo);
-                    (&pos.x)[j] = *reinterpret_cast<const uint32_t*>(&hi);
-                }
-                s_q[warp][i][lane] = neg;                  // against the minima, the first 128 elements
-                s_q[warp][4 + i][lane] = pos;
+            for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 y = *reinterpret_cast<const __nv_bfloat162*>(&xs[j]);
+                const __nv_bfloat162 lo = __hmin2_nan(y, zero), hi = __hmax2_nan(y, zero);
+                (&neg.x)[j] = *reinterpret_cast<const uint32_t*>(&lo);
+                (&pos.x)[j] = *reinterpret_cast<const uint32_t*>(&hi);
             }
+            s_q[warp][i][lane] = neg;                      // against the minima, the first 128 elements
+            s_q[warp][4 + i][lane] = pos;
         }
         __syncthreads();
+        if (rt + kGroup < rt1) fetch(rt + kGroup);
         // two row tiles at a time: two chains of products
         for (int t0 = 0; t0 < n_rt; t0 += 2) {
-            float x2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint4 b0 = s_q[t0][i][lane], b1 = s_q[t0 + 1][i][lane];      // kGroup is even
                 const uint32_t a0[4] = {w[0][i].x, w[1][i].x, w[0][i].y, w[1][i].y};
                 const uint32_t a1[4] = {w[0][i].z, w[1][i].z, w[0][i].w, w[1][i].w};
-                mma_bf16_16816(x2[0], a0, b0.x, b0.y);
-                mma_bf16_16816(x2[1], a0, b1.x, b1.y);
-                mma_bf16_16816(x2[0], a1, b0.z, b0.w);
-                mma_bf16_16816(x2[1], a1, b1.z, b1.w);
+                mma_bf16_16816(x[0], a0, b0.x, b0.y);
+                mma_bf16_16816(x[1], a0, b1.x, b1.y);
+                mma_bf16_16816(x[0], a1, b0.z, b0.w);
+                mma_bf16_16816(x[1], a1, b1.z, b1.w);
             }
             // x: page r, rows 2 c and 2 c + 1; page r + 8, the same rows. The largest of a token's rows:
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const float* x = x2[t];
                 const int row = (rt + t0 + t) * 8 + 2 * c;
                 const bool mine = t0 + t < n_rt;
-                if (G == 1) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int p = p0 + 16 * warp + 8 * (i >> 1) + r, tok = row + (i & 1);
-                        if (mine && p < n_pages && tok < sp.n_new)
-                            reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] =
-                                there[i >> 1] ? x[i] : kNoPage;
-                    }
-                    continue;
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float y = fmaxf(x[2 * h], x[2 * h + 1]);
-                    if (G >= 4) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-                    if (G >= 8) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-                    const int p = p0 + 16 * warp + 8 * h + r, tok = row >> gs;
+                    const int p = p0 + 16 * warp + 8 * h + r;
+                    float y = x[t][2 * h];
+                    if (G == 1) {
+                        if (mine && p < n_pages && row + 1 < sp.n_new)
+                            reinterpret_cast<float*>(a.rows + ((sp.t0 + row + 1) * v.hkv + g) * v.max_pages)[p] =
+                                there[h] ? x[t][2 * h + 1] : kNoPage;
+                    } else {
+                        y = fmaxf(y, x[t][2 * h + 1]);
+                        if (G >= 4) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+                        if (G >= 8) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+                    }
+                    const int tok = row >> gs;
                     if (mine && (row & (G - 1)) == 0 && p < n_pages && tok < sp.n_new)
                         reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] = there[h] ? y : kNoPage;
                 }
             }
+        }
+    }
+    if (part == 0) {
+        float top = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u[4] = {w[h][i].x, w[h][i].y, w[h][i].z, w[h][i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = fabsf(__uint_as_float(u[j] << 16)), y = fabsf(__uint_as_float(u[j] & 0xFFFF0000u));
+                    top = x <= top ? top : x;              // a NaN stays
+                    top = y <= top ? top : y;
+                }
+            }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            const float x = __shfl_xor_sync(0xffffffffu, top, o);
+            top = x <= top ? top : x;
+        }
+        if (lane == 0) s_top[warp] = top;
+        __syncthreads();
+        if (tid == 0) {
+            float x = 0.f;
+            for (int i = 0; i < 8; ++i) x = s_top[i] <= x ? x : s_top[i];
+            a.bmax[(sp.t0 * v.hkv + g) * a.chunks + chunk] = x;
         }
     }
 }
@@ -407,7 +422,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
 
     // the scores, and how far they may be off
     const float* score = reinterpret_cast<const float*>(row64);
-    const float* bmax = a.bmax + (sp.t0 * v.hkv + g) * v.max_pages;
+    const float* bmax = a.bmax + (sp.t0 * v.hkv + g) * a.chunks;
     float bm = 0.f;
     uint32_t mine = 0;
 #pragma unroll 8
@@ -415,6 +430,8 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
         const uint32_t x = i >= newest ? 0xFFFFFFFFu : ordered32(score[i]);
         s_score[i] = x;
         mine = max(mine, x);
+    }
+    for (int i = tid; i < (n + kScorePages - 1) / kScorePages; i += kPickThreads) {
         const float b = bmax[i];
         bm = b <= bm ? bm : b;                             // a NaN stays
     }
@@ -672,8 +689,9 @@ extern "C" msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa
         // blocks for every SM: where pages and heads do not give enough, a sequence's query rows are parted too
         const int64_t blocks = (int64_t)a.chunks * kv->n_seq * kv->hkv;
         const int64_t groups = ((int64_t)std::min<int64_t>(max_new, n_tok) * a.G + 8 * kGroup - 1) / (8 * kGroup);
-        a.token_parts = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 1184 / std::max<int64_t>(blocks, 1), 65535 / kv->hkv}));
-        page_score_kernel<<<dim3((unsigned)(a.chunks * kv->n_seq), (unsigned)(kv->hkv * a.token_parts)), 256, 0, s>>>(a);
+        a.token_parts = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 592 / std::max<int64_t>(blocks, 1), 65535 / kv->hkv}));
+        const dim3 grid((unsigned)(a.chunks * kv->n_seq), (unsigned)(kv->hkv * a.token_parts));
+        page_score_kernel<<<grid, 256, 0, s>>>(a);
         MSA_LAUNCH_CHECK();
     }
     static std::mutex mu;
