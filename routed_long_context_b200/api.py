@@ -313,13 +313,6 @@ def msa_sparse_attn_split(q, mem_kv, mem_len, local_k, local_v, L: int, q_start:
 
 
 # ------------------------------------------------------------------------------------------------ paged cache
-def _on_current(who: str, dev: int, *tensors) -> None:
-    """The kernels run on the current device and read plain memory of it: anything else is refused."""
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{who}: a tensor of shape {tuple(t.shape)} is on {t.device}, the current CUDA device is {dev}")
-
-
 def _want(who: str, name: str, t: torch.Tensor, dtype, shape) -> None:
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{who}: {name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of {tuple(t.shape)}")
@@ -343,7 +336,8 @@ class PagedKV:
             _want("PagedKV", "bounds", bounds, torch.bfloat16, (n_pages, hkv, 2, d))
         self.pages, self.scales, self.page_table, self.seq_len, self.bounds = pages, scales, page_table, seq_len, bounds
         self.n_seq, self.max_pages, self.page, self.hkv, self.d = n_seq, max_pages, page, hkv, d
-        self.device, self._index = pages.device, pages.get_device()
+        self.device, self._index, self._off_shape = pages.device, pages.get_device(), (n_seq + 1,)
+        self._u8 = pages.view(torch.uint8)       # for its new_empty: cheaper than torch.empty with a device to parse
         for name, t in (("scales", scales), ("page_table", page_table), ("seq_len", seq_len), ("bounds", bounds)):
             if t is not None and t.device != pages.device:
                 raise ValueError(f"PagedKV: {name} is on {t.device}, pages on {pages.device}")
@@ -362,13 +356,17 @@ class PagedKV:
                    torch.zeros((n_pages, hkv, 2, d), dtype=torch.bfloat16, device=device) if bounds else None)
 
     def _check(self, who: str, tok_off, x, heads: int, *others) -> None:
-        if self._index < 0:
+        """The kernels run on the current device and read plain memory of it: anything else is refused."""
+        dev = self._index
+        if dev < 0 or dev != torch.cuda.current_device():
             raise ValueError(f"{who}: the cache is on {self.device}, not on the current CUDA device")
-        _on_current(who, torch.cuda.current_device(), self.pages, tok_off, x, *others)
-        if tok_off.dtype != torch.int64 or tok_off.shape != (self.n_seq + 1,):
+        for t in (tok_off, x, *others):
+            if t is not None and t.get_device() != dev:
+                raise ValueError(f"{who}: a tensor of shape {tuple(t.shape)} is on {t.device}, the cache on {self.device}")
+        if tok_off.dtype != torch.int64 or tok_off.shape != self._off_shape:
             raise ValueError(f"{who}: tok_off must be int64 [{self.n_seq + 1}], got {tok_off.dtype} of "
                              f"{tuple(tok_off.shape)}")
-        if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != self.d:
+        if x.shape[1:] != (heads, self.d):
             raise ValueError(f"{who}: expected [n_tok, {heads}, {self.d}], got {tuple(x.shape)}")
 
 
@@ -387,7 +385,8 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
         _want("msa_paged_append", "q", q, k.dtype, (k.shape[0], hq, kv.d))
         if q_rot is None:
             q_rot = torch.empty_like(q)
-        _want("msa_paged_append", "q_rot", q_rot, q.dtype, q.shape)
+        else:
+            _want("msa_paged_append", "q_rot", q_rot, q.dtype, q.shape)
     check(lib.msa_paged_append(kv._ref, _ptr(k), _ptr(v), _ptr(q), _dt(k), k.shape[0], hq, _ptr(tok_off), max_new,
                                pos_offset, _ptr(cos_sin), cos_sin.shape[0], _ptr(q_rot) if q is not None else None,
                                _stream(stream)), "msa_paged_append")
@@ -407,11 +406,11 @@ def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int =
     n_tok, hq = q.shape[:2]
     kv._check("msa_page_select", tok_off, q, hq, sel, ws)
     if sel is None:
-        sel = torch.empty((n_tok, kv.hkv, k), dtype=torch.int32, device=kv.device)
+        sel = kv.seq_len.new_empty((n_tok, kv.hkv, k))
     else:
         _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
-        ws = _ws(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages), kv.device)
+        ws = kv._u8.new_empty(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages) or 256)
     check(lib.msa_page_select(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, k, recent, _ptr(sel),
                               _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "msa_page_select")
     return sel
@@ -440,13 +439,13 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     if lse is not None:
         _want("msa_paged_attn", "lse", lse, torch.float32, (n_tok, hq))
     elif want_lse:
-        lse = torch.empty((n_tok, hq), dtype=torch.float32, device=kv.device)
+        lse = kv.scales.new_empty((n_tok, hq))
     k = 0
     if sel is not None:
         k = sel.shape[-1]
         _want("msa_paged_attn", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
-        ws = _ws(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k), kv.device)
+        ws = kv._u8.new_empty(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k))
     scale = 1.0 / math.sqrt(kv.d) if scale is None else scale
     check(lib.msa_paged_attn(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, _ptr(sel), k, scale,
                              _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
