@@ -61,7 +61,7 @@ struct PromptSmem {
     int64_t t0[kWin];
     int n_new[kWin], len[kWin];
     long long scan[kThreads / 32];
-    float2 ml[kRowsTile];
+    float2 ml[2][kRowsTile];
     float fr[2][kRowsTile];
 };
 
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                             // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
                             const uint32_t ub = __float_as_uint(top);
                             const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
-                            const float inv = pow2f(-e);
+                            const float inv = a.scale_log2e < 0.f ? -pow2f(-e) : pow2f(-e);
                             uint32_t h[4], l[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                             const int at = rr * kPagedD + (((piece >> 1) ^ (rr & 7)) << 4) + 8 * (piece & 1);
                             *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
                             *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-                            if (piece == 0) sm.fr[SPLIT ? 0 : wg][rr] = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : a.scale_log2e * pow2f(e);
+                            if (piece == 0) sm.fr[SPLIT ? 0 : wg][rr] = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fabsf(a.scale_log2e) * pow2f(e);
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -617,22 +617,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                         uint32_t xa[32], xb[32], pk[64];
                         if (__any_sync(0xffffffffu, m == ninf)) {      // the row's first keys
                             float mt = m;
-                            auto part = [&](uint32_t (&x)[32], int at) {
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                tmem_issue32(ts + 32 * c, xa);
+                                tmem_wait32(xa);
+                                float y = ninf, z = ninf;
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) mt = fmaxf(mt, __uint_as_float(x[i]) * f[2 * at + (i >> 4)]);
-                            };
-                            tmem_issue32(ts, xa);
-                            tmem_wait32(xa);
-                            tmem_issue32(ts + 32, xb);
-                            part(xa, 0);
-                            tmem_wait32(xb);
-                            tmem_issue32(ts + 64, xa);
-                            part(xb, 1);
-                            tmem_wait32(xa);
-                            tmem_issue32(ts + 96, xb);
-                            part(xa, 2);
-                            tmem_wait32(xb);
-                            part(xb, 3);
+                                for (int i = 0; i < 16; ++i) {
+                                    y = fmaxf(y, __uint_as_float(xa[i]));
+                                    z = fmaxf(z, __uint_as_float(xa[16 + i]));
+                                }
+                                mt = fmaxf(mt, fmaxf(y * (fr * sm.sk[info][2 * c]), z * (fr * sm.sk[info][2 * c + 1])));   // f > 0
+                            }
                             move_max(mt);
                         }
                         // against the reference maximum as it is; V's scale goes into P's exponent
@@ -734,95 +730,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
 
                 // out, or the workspace
                 const bool whole = p.starts && p.ends;
-                float w0 = 1.f, w1 = 0.f;
-                float* xch = reinterpret_cast<float*>(sm.q[1][0]) + rl * 64;
-                if (SPLIT) {
-                    // join the odd tiles' part to the even tiles': 64 columns at a time through the second row block's
-                    // place; named barrier 1 holds both warpgroups together
-                    const bool two = p.n > 1;
-                    if (wg == 1) sm.ml[rl] = make_float2(m, l);
-                    if (wg == 1 && two) {
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            float x[32];
-                            tmem_ld32(to + 32 * part, x);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<float4*>(xch + (((8 * part + i) ^ (rl & 15)) << 2)) =
-                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                        }
-                    }
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
-                    if (wg == 0) {
-                        const float2 other = sm.ml[rl];
-                        const float M = fmaxf(m, other.x);
-                        w0 = m == ninf ? 0.f : ex2(m - M);
-                        w1 = other.x == ninf ? 0.f : ex2(other.x - M);
-                        l = (m == ninf ? l : w0 * l) + (!two ? 0.f : other.x == ninf ? other.y : w1 * other.y);
-                        if (!two) w1 = 0.f;
-                        m = M;
-                    }
-                }
-                const float inv_l = l == 0.f ? 0.f : kUnit / l;
                 const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (p.starts ? 1 : 0)) * a.rows + row0;
-                // 32 columns of the warp's rows at a time, through the place of its queries (which no product reads any
-                // more), so that eight lanes write a row's piece
-#pragma unroll
-                for (int part = 0; part < 4; ++part) {
-                    if (SPLIT && part == 2) {
-                        asm volatile("bar.sync 1, 256;" ::: "memory");
-                        if (wg == 1 && p.n > 1) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float x[32];
-                                tmem_ld32(to + 64 + 32 * h, x);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    *reinterpret_cast<float4*>(xch + (((8 * h + i) ^ (rl & 15)) << 2)) =
-                                        make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                            }
-                        }
-                        asm volatile("bar.sync 1, 256;" ::: "memory");
-                    }
-                    if (SPLIT && wg == 1) continue;
-                    float x[32];
-                    tmem_ld32(to + 32 * part, x);
-                    if (SPLIT && p.n > 1) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 y = *reinterpret_cast<const float4*>(xch + (((8 * (part & 1) + i) ^ (rl & 15)) << 2));
-                            x[4 * i] = w0 * x[4 * i] + w1 * y.x;
-                            x[4 * i + 1] = w0 * x[4 * i + 1] + w1 * y.y;
-                            x[4 * i + 2] = w0 * x[4 * i + 2] + w1 * y.z;
-                            x[4 * i + 3] = w0 * x[4 * i + 3] + w1 * y.w;
-                        }
-                    }
+                // a piece of a row: four columns from `col` on of row r of the warp's
+                auto put = [&](int r, int col, float4 y) {
+                    const int rr = row0 + r;
+                    if (rr >= p.rows) return;
                     if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] *= inv_l;
+                        uint2 u;
+                        u.x = pack_bf16(y.x, y.y);
+                        u.y = pack_bf16(y.z, y.w);
+                        const int off = ((rr >> gs) * hq + (rr & (G - 1))) * kPagedD + col;
+                        *reinterpret_cast<uint2*>(a.out + (p.t0 * hq + p.head * G) * kPagedD + off) = u;
+                    } else {
+                        *reinterpret_cast<float4*>(a.part_o + slot0 * kPagedD + r * kPagedD + col) = y;
                     }
-                    uint8_t* stage = sm.q[SPLIT ? 0 : wg][part & 1] + (warp & 3) * 32 * kPagedD;
+                };
+                if (SPLIT) {
+                    // Both warpgroups' parts are joined, each warpgroup for half of the columns: the other half goes to the
+                    // other one through the place of the queries (the first row block's for columns 0 .. 63, which
+                    // warpgroup 1 writes). Named barrier 1 holds the two together.
+                    sm.ml[wg][rl] = make_float2(m, l);
+                    asm volatile("bar.sync 1, 256;" ::: "memory");     // no product reads the queries any more
+                    const float2 other = sm.ml[wg ^ 1][rl];
+                    const float M = fmaxf(m, other.x);
+                    float w0 = m == ninf ? 0.f : ex2(m - M), w1 = other.x == ninf ? 0.f : ex2(other.x - M);
+                    l = (m == ninf ? l : w0 * l) + (other.x == ninf ? other.y : w1 * other.y);
+                    m = M;
+                    float x[64];
+                    tmem_ld64(to + 64 * (wg ^ 1), x);
+                    float4* theirs = reinterpret_cast<float4*>(sm.q[wg ^ 1][0]) + rl * 16;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<float4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
-                            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    for (int i = 0; i < 16; ++i) theirs[i ^ (rl & 15)] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    tmem_ld64(to + 64 * wg, x);
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    const float f = !whole ? 1.f : l == 0.f ? 0.f : kUnit / l;
+                    w0 *= f;
+                    w1 *= f;
+                    float4* mine = reinterpret_cast<float4*>(sm.q[wg][0]) + rl * 16;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 y = mine[i ^ (rl & 15)];          // a part without a key may hold anything
+                        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (w0 != 0.f) z = make_float4(w0 * x[4 * i], w0 * x[4 * i + 1], w0 * x[4 * i + 2], w0 * x[4 * i + 3]);
+                        if (w1 != 0.f) z = make_float4(fmaf(w1, y.x, z.x), fmaf(w1, y.y, z.y), fmaf(w1, y.z, z.z), fmaf(w1, y.w, z.w));
+                        mine[i ^ (rl & 15)] = z;
+                    }
                     __syncwarp();
+                    // sixteen lanes write a row's half
+#pragma unroll 4
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 2 * i + (lane >> 4), c = lane & 15;
+                        put(r, 64 * wg + 4 * c, reinterpret_cast<const float4*>(sm.q[wg][0])[((warp & 3) * 32 + r) * 16 + (c ^ (r & 15))]);
+                    }
+                } else {
+                    // 32 columns of the warp's rows at a time, through the place of its queries (which no product reads any
+                    // more), so that eight lanes write a row's piece
+                    const float f = !whole ? 1.f : l == 0.f ? 0.f : kUnit / l;
+#pragma unroll 1
+                    for (int part = 0; part < 4; ++part) {
+                        float x[32];
+                        tmem_ld32(to + 32 * part, x);
+                        float4* stage = reinterpret_cast<float4*>(sm.q[wg][part & 1] + (warp & 3) * 32 * kPagedD);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3), col = 32 * part + 4 * (lane & 7), rr = row0 + r;
-                        const float4 y = *reinterpret_cast<const float4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                        if (rr >= p.rows) continue;
-                        if (whole) {
-                            uint2 u;
-                            u.x = pack_bf16(y.x, y.y);
-                            u.y = pack_bf16(y.z, y.w);
-                            *reinterpret_cast<uint2*>(
-                                a.out + ((p.t0 + (rr >> gs)) * hq + p.head * G + (rr & (G - 1))) * kPagedD + col) = u;
-                        } else {
-                            *reinterpret_cast<float4*>(a.part_o + (slot0 + r) * kPagedD + col) = y;
+                        for (int i = 0; i < 8; ++i)
+                            stage[lane * 8 + (i ^ (lane & 7))] = make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
+                        __syncwarp();
+#pragma unroll 4
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3), c = lane & 7;
+                            put(r, 32 * part + 4 * c, stage[r * 8 + (c ^ (r & 7))]);
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
                 if (valid && (!SPLIT || wg == 0)) {
                     if (whole) {
