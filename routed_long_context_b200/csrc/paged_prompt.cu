@@ -39,6 +39,7 @@ constexpr int kKStages = 3, kVStages = 2, kV16Stages = 2, kInfo = 8;
 constexpr int kWin = kPromptSeqs;                          // sequences of a launch, a thread each
 static_assert(kWin == kThreads, "a thread per sequence");
 constexpr float kTrigger = 32768.f;                        // a tile's sum above it moves the reference maximum
+constexpr float kSlack = 8.f;                            // log2 of how far logits may lie above the reference
 
 constexpr float kUnit = 1152921504606846976.f;             // 2^60, the unit in which O is kept
 
@@ -594,8 +595,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                     }
                     const int key0 = (p.k0 + j) * kKT;
                     float sum = 0.f;
-                    // a new reference maximum: of sum and O
+                    // a new reference maximum, of sum and O, unless the old one will do for all of the warp's rows
                     auto move_max = [&](float mt) {
+                        if (!__any_sync(0xffffffffu, mt > m + kSlack)) return;
+                        mt = fmaxf(mt, m);
                         const float al = m == mt ? 1.f : ex2(m - mt);
                         m = mt;
                         l *= al;
