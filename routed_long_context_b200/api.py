@@ -355,6 +355,16 @@ class PagedKV:
                    torch.zeros(n_seq, dtype=torch.int32, device=device),
                    torch.zeros((n_pages, hkv, 2, d), dtype=torch.bfloat16, device=device) if bounds else None)
 
+    def _scratch(self, nbytes: int, stream, *results) -> torch.Tensor:
+        """A workspace; it and the results allocated with it stay reserved until the stream that uses them, where that is
+        not the current one, is done."""
+        ws = self._u8.new_empty(nbytes)
+        if stream is not None:
+            for t in (ws, *results):
+                if t is not None:
+                    t.record_stream(stream)
+        return ws
+
     def _check(self, who: str, tok_off, x, heads: int, *others) -> None:
         """The kernels run on the current device and read plain memory of it: anything else is refused."""
         dev = self._index
@@ -385,6 +395,8 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
         _want("msa_paged_append", "q", q, k.dtype, (k.shape[0], hq, kv.d))
         if q_rot is None:
             q_rot = torch.empty_like(q)
+            if stream is not None:
+                q_rot.record_stream(stream)
         else:
             _want("msa_paged_append", "q_rot", q_rot, q.dtype, q.shape)
     check(lib.msa_paged_append(kv._ref, _ptr(k), _ptr(v), _ptr(q), _dt(k), k.shape[0], hq, _ptr(tok_off), max_new,
@@ -410,7 +422,7 @@ def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int =
     else:
         _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
-        ws = kv._u8.new_empty(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages) or 256)
+        ws = kv._scratch(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages) or 256, stream, sel)
     check(lib.msa_page_select(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, k, recent, _ptr(sel),
                               _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "msa_page_select")
     return sel
@@ -445,7 +457,8 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
         k = sel.shape[-1]
         _want("msa_paged_attn", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
-        ws = kv._u8.new_empty(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k))
+        ws = kv._scratch(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k), stream,
+                         out, lse)
     scale = 1.0 / math.sqrt(kv.d) if scale is None else scale
     check(lib.msa_paged_attn(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, _ptr(sel), k, scale,
                              _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),

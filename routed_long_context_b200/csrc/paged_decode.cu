@@ -103,6 +103,10 @@ __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t* hi, uin
                                                __NV_E4M3);
 }
 
+// x / d; the short division where it will do
+__device__ __forceinline__ int quotient(long long x, int d) {
+    return (unsigned long long)x >> 32 ? (int)(x / d) : (int)((unsigned)x / (unsigned)d);
+}
 // The last i with pre[i] <= g.
 __device__ __forceinline__ int find(const long long* pre, int n, long long g) {
     int lo = 0;
@@ -264,9 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                         s = w * kWindow + lo;
                         seen = sm.len[lo];
                         const int per_head = (seen + kDecodeTile - 1) / kDecodeTile;
-                        const unsigned in_seq = (unsigned)(g - sm.pre[lo]);
-                        head = (int)(in_seq / (unsigned)per_head);
-                        at = (int)(in_seq - (unsigned)head * per_head);
+                        const long long in_seq = g - sm.pre[lo];
+                        head = quotient(in_seq, per_head);
+                        at = (int)(in_seq - (long long)head * per_head);
                     }
                     const int n_pages = (seen + page - 1) >> v.shift;
                     const int32_t* table = v.table + (int64_t)s * v.max_pages;
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                     n_new = sm.n_new[lo];
                     len = sm.len[lo];
                     const int per_head = (len + kDecodeTile - 1) / kDecodeTile;
-                    head = (int)((unsigned)(g0 - sm.pre[lo]) / (unsigned)per_head);
+                    head = quotient(g0 - sm.pre[lo], per_head);
                     seg_a = sm.pre[lo] + (long long)head * per_head;
                     seg_b = seg_a + per_head;
                 }

@@ -661,6 +661,102 @@ def test_a_captured_step_replays_on_new_lengths(m):
     assert m.device_status() == 0
 
 
+def test_a_stream_of_the_callers_own(m):
+    """Calls on a stream that is not the current one, with scratch and results allocated by the call, while the current
+    stream allocates and overwrites memory of the same sizes; two such streams at once."""
+    c = Cache(m, 80, [3000, 700], 32, 4)
+    off_d, off = _offsets([1, 1])
+    q_d, q = _queries(81, 2, 16)
+    off_l, _ = _offsets([40, 30])
+    q_l, _ = _queries(82, 70, 16)
+    sel = m.msa_page_select(c.kv, q_d, off_d, 1, 6)
+    want = (m.msa_paged_attn(c.kv, q_d, off_d, 1), m.msa_paged_attn(c.kv, q_d, off_d, 1, sel=sel),
+            m.msa_paged_attn(c.kv, q_l, off_l, 40))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(20):
+        s = streams[i % 2]
+        picked = m.msa_page_select(c.kv, q_d, off_d, 1, 6, stream=s)
+        got.append((m.msa_paged_attn(c.kv, q_d, off_d, 1, stream=s), m.msa_paged_attn(c.kv, q_d, off_d, 1, sel=picked, stream=s),
+                    m.msa_paged_attn(c.kv, q_l, off_l, 40, stream=s)))
+        for _ in range(3):
+            torch.empty(1 << 20, device="cuda").fill_(math.nan)
+            torch.empty_like(q_l).fill_(math.nan)
+    torch.cuda.synchronize()
+    assert m.device_status() == 0
+    for g in got:
+        for x, y in zip(g, want):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(m, new, bad):
+    c = Cache(m, 83, [500], 64, 2)
+    off_d, _ = _offsets([new])
+    q_d, _ = _queries(84, new, 8)
+    want, wlse = m.msa_paged_attn(c.kv, q_d, off_d, new, want_lse=True)
+    q_d[new // 2, 3, 5] = bad
+    out, lse = m.msa_paged_attn(c.kv, q_d, off_d, new, want_lse=True)
+    assert torch.isnan(out[new // 2, 3]).all() and torch.isnan(lse[new // 2, 3])
+    keep = torch.ones((new, 8), dtype=torch.bool, device="cuda")
+    keep[new // 2, 3] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], wlse[keep])
+    assert m.device_status() == 0
+
+
+def test_selection_leaves_rows_outside_the_sequences(m):
+    c = Cache(m, 85, [300, 500], 16, 2)
+    off_d, off = _offsets([2, 1], first=3)
+    q_d, q = _queries(86, 9, 8)
+    sel = torch.full((9, 2, 5), 77, dtype=torch.int32, device="cuda")
+    m.msa_page_select(c.kv, q_d, off_d, 2, 5, sel=sel)
+    assert m.device_status() == 0
+    assert (sel[:3] == 77).all() and (sel[6:] == 77).all() and (sel[3:6] < 77).all()
+
+
+def test_attention_records_more_tokens_than_it_was_told(m):
+    c = Cache(m, 87, [300, 100], 32, 2)
+    for news, told in (([3, 1], 2), ([40, 1], 39)):
+        off_d, off = _offsets(news)
+        q_d, q = _queries(88, off[-1], 8)
+        out = torch.full_like(q_d, 7.0)
+        lse = torch.full((off[-1], 8), 9.0, device="cuda")
+        m.msa_paged_attn(c.kv, q_d, off_d, told, out=out, lse=lse)
+        assert m.device_status() == 3
+        assert (out[:off[1]] == 7.0).all() and (lse[:off[1]] == 9.0).all()
+        _check_attn(c, [0, 1], [0, off[1]], q, out, lse, 8, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("new,page,G", [(1, 16, 4), (1, 64, 8), (3, 32, 2), (30, 16, 4), (70, 128, 4), (300, 64, 1)])
+def test_nothing_is_written_beside_the_outputs(m, new, page, G):
+    """Workspaces of exactly the size asked for, and outputs, between guards."""
+    hkv, k = 2, 4
+    c = Cache(m, 89, [3000, 331], page, hkv)
+    off_d, off = _offsets([new, min(new, 331)])
+    n = int(off[-1])
+    q_d, _ = _queries(90, n, hkv * G)
+
+    def guarded(nbytes):
+        buf = torch.full((nbytes + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+        return buf, buf[256:256 + nbytes]
+
+    sizes = [m.page_select_workspace_size(n, hkv, c.kv.max_pages),
+             m.paged_attn_workspace_size(n, 2, new, hkv * G, hkv, c.kv.max_pages, page),
+             m.paged_attn_workspace_size(n, 2, new, hkv * G, hkv, c.kv.max_pages, page, k),
+             n * hkv * k * 4, n * hkv * G * D * 2, n * hkv * G * 4]
+    bufs = [guarded(x) for x in sizes]
+    w1, w2, w3, sel, out, lse = (b[1] for b in bufs)
+    sel, out, lse = sel.view(torch.int32).view(n, hkv, k), out.view(torch.bfloat16).view(q_d.shape), lse.view(torch.float32).view(n, -1)
+    m.msa_page_select(c.kv, q_d, off_d, new, k, sel=sel, ws=w1)
+    m.msa_paged_attn(c.kv, q_d, off_d, new, sel=sel, out=out, lse=lse, ws=w3)
+    m.msa_paged_attn(c.kv, q_d, off_d, new, out=out, lse=lse, ws=w2)
+    assert m.device_status() == 0
+    for b, inner in bufs:
+        assert (b[:256] == 0x5A).all() and (b[256 + inner.numel():] == 0x5A).all()
+
+
 def test_offsets_past_32_bits(m):
     """A cache of more than 4 GB: pages at its far end."""
     hkv, page, n_pages = 8, 128, 17000                      # 17000 * 2 * 8 * 128 * 128 B = 4.5 GB
