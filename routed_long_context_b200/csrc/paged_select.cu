@@ -9,12 +9,12 @@
 // 1. page_score_kernel: all scores in fp32 on the tensor cores. max(q lo, q hi) = min(q, 0) lo + max(q, 0) hi
 //    where lo <= hi, so the scores of 16 pages and 8 query rows are one product over 2 * 128 elements whose page
 //    operand is the bounds as they lie in memory. The products of two bf16 are exact; the sums are off by at
-//    most E = 2^-14 sum|q_d| max|bound|: each of the 16 steps adds 17 numbers and loses at most 2^-22 of the
-//    sum of magnitudes (2^-24 would be a rounding, the tensor cores may truncate), 2^-18 over 16 steps. Bound
-//    by the bytes of the bounds: 512 per page and kv head.
+//    most E = 2^-14 sum|q_d| max|bound|: a step adds 17 numbers, and if each is cut off at 2^-23 of the largest,
+//    16 steps lose 2^-14.9 of the sum of magnitudes. Bound by the bytes of the bounds, 512 per page and kv head,
+//    where there are few query rows; 64 tokens of 32 heads over 6,250 pages take 25 us, half of it products.
 // 2. page_pick_kernel: one block per (token, kv head). T = the k-th best fp32 score, by its bits from the top, two
 //    at a time (counting only: no histogram, whose counters equal leading bits would all hit), among the scores
-//    that reach the k-th best of the 256 threads' maxima where k is at most 256. Pages above T + 2 E are in, those
+//    that reach the k-th best of the threads' maxima where k is at most 256. Pages above T + 2 E are in, those
 //    below T - 2 E are out, and where more than k remain those in between are summed again in 64 bits and ranked.
 #include <algorithm>
 #include <mutex>
@@ -207,24 +207,39 @@ struct PickSmem {
     int hist[256];
     unsigned long long prefix;
     int want, done;
-    uint32_t top[kPickThreads], cand[kCand];
+    alignas(16) uint32_t top[kPickThreads], cand[kCand + 1];
     int cand_page[kCand], n_cand, n_near, n_in;
-    uint32_t floor;
+    uint32_t floor, kth;
 };
 
+// The k-th largest of v[0 .. n), n <= kPickThreads: every thread counts how many come before its own (equal ones by
+// place); the one that finds k - 1 tells. One barrier; v[n ..] up to a multiple of 4 may hold anything.
+__device__ __forceinline__ uint32_t block_kth(const uint32_t* v, int n, int k, uint32_t* told) {
+    const int tid = threadIdx.x;
+    if (tid < n) {
+        const uint32_t x = v[tid];
+        int before = 0;
+#pragma unroll 4
+        for (int i = 0; i < n; i += 4) {
+            const uint4 y = *reinterpret_cast<const uint4*>(v + i);
+            before += (i < n) & (y.x > x || (y.x == x && i < tid));
+            before += (i + 1 < n) & (y.y > x || (y.y == x && i + 1 < tid));
+            before += (i + 2 < n) & (y.z > x || (y.z == x && i + 2 < tid));
+            before += (i + 3 < n) & (y.w > x || (y.w == x && i + 3 < tid));
+        }
+        if (before == k - 1) *told = x;
+    }
+    __syncthreads();
+    return *told;
+}
 // The k-th largest of v[0 .. n), n < 1024, by one warp: two bits at a time from the top, three counts in one sum.
 __device__ __forceinline__ uint32_t warp_kth(const uint32_t* v, int n, int k) {
     const int lane = threadIdx.x & 31;
-    uint32_t x[4];                                         // the first 128 stay in registers
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < n ? v[lane + 32 * i] : 0;
     uint32_t T = 0;
     for (int shift = 30; shift >= 0; shift -= 2) {
         const uint32_t t1 = T | (1u << shift), t2 = T | (2u << shift), t3 = T | (3u << shift);
         uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c += (x[i] >= t1) + ((x[i] >= t2) << 10) + ((x[i] >= t3) << 20);
-        for (int i = lane + 128; i < n; i += 32) {
+        for (int i = lane; i < n; i += 32) {
             const uint32_t y = v[i];
             c += (y >= t1) + ((y >= t2) << 10) + ((y >= t3) << 20);
         }
@@ -460,20 +475,19 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     }
     const float E = qs * bm * 6.103515625e-05f + 1e-36f;   // 2^-14, and what underflow may lose
 
-    // Few candidates first, where k allows: at least k scores reach the k-th best of the threads' own maxima.
+    // Few candidates first, where k allows: at least k scores reach the k-th best of the threads' own maxima, folded to
+    // 2 k of them or a little more (about 1.4 k scores reach that; fewer maxima are quicker to rank).
     const bool few = a.k <= kPickThreads;
     if (few) {
-        sm.top[tid] = mine;
+        const int fold = a.k > 64 ? 0 : a.k > 32 ? 1 : a.k > 16 ? 2 : 3;
+        for (int o = 0; o < fold; ++o) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1 << o));
+        if ((tid & ((1 << fold) - 1)) == 0) sm.top[tid >> fold] = mine;
         if (tid == 0) sm.n_cand = 0;
         __syncthreads();
-        if (warp == 0) {
-            const uint32_t t = warp_kth(sm.top, kPickThreads, a.k);
-            if (lane == 0) sm.floor = t;
-        }
-        __syncthreads();
-        const float f = unordered32(sm.floor);
+        const uint32_t t = block_kth(sm.top, kPickThreads >> fold, a.k, &sm.floor);
+        const float f = unordered32(t);
         // everything near the border, wherever above it that turns out to be, and all that compares with nothing
-        const uint32_t floor = sm.floor == 0xFFFFFFFFu ? sm.floor : (f - 2.f * E > -3.402823466e38f) ? ordered32(f - 2.f * E) : 0u;
+        const uint32_t floor = t == 0xFFFFFFFFu ? t : (f - 2.f * E > -3.402823466e38f) ? ordered32(f - 2.f * E) : 0u;
         for (int i = tid; i < n; i += kPickThreads) {
             const uint32_t x = s_score[i];
             const bool yes = x >= floor || x == 0;
@@ -493,20 +507,22 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     }
     if (few && sm.n_cand <= kCand) {
         const int n_cand = sm.n_cand;
-        if (warp == 0) {
-            const uint32_t t = warp_kth(sm.cand, n_cand, a.k);
-            if (lane == 0) {
-                sm.floor = t;
-                sm.n_near = sm.n_in = 0;
-            }
-        }
+        if (tid == 0) sm.n_near = sm.n_in = 0;
         const int words = (n + 31) / 32;                   // a bit per page, in the place of the scores
-        __syncthreads();
         uint32_t* bits = s_score;
         for (int i = tid; i < words; i += kPickThreads) bits[i] = 0;
-        const uint32_t T = sm.floor;
+        uint32_t T;
+        if (n_cand <= kPickThreads) {
+            T = block_kth(sm.cand, n_cand, a.k, &sm.kth);
+        } else {
+            if (warp == 0) {
+                const uint32_t t = warp_kth(sm.cand, n_cand, a.k);
+                if (lane == 0) sm.kth = t;
+            }
+            __syncthreads();
+            T = sm.kth;
+        }
         const float edge = unordered32(T), low = edge - 2.f * E, high = edge + 2.f * E;
-        __syncthreads();
         for (int i = tid; i < n_cand; i += kPickThreads) {
             const uint32_t x = sm.cand[i];
             const float y = unordered32(x);
