@@ -134,7 +134,7 @@ __device__ __forceinline__ int cta_of_tile(int64_t total, int n, int64_t x) {
 // The few-rows kernel (paged_decode.cu) and the many-rows kernel (paged_prompt.cu).
 constexpr int kDecodeRows = 8;
 constexpr int kDecodeTile = 32;
-constexpr int kMinDecodeTiles = 8;   // tiles that are worth a CTA
+constexpr int kMinDecodeTiles = 1;   // tiles that are worth a CTA
 constexpr int kPromptTile = 128;
 constexpr int kPromptSeqs = 512;     // sequences per launch
 msa_status launch_paged_decode(const PagedAttnArgs& a, int grid, cudaStream_t s);
