@@ -17,8 +17,9 @@
 // is free: a thread takes the 16-byte pieces that it can read from shared memory without bank conflicts, and V
 // needs no more than 4 x 4 byte transposes.
 //
-// One block per SM: a warp of its own looks the pages up, 22 tiles at a time, and brings keys and values by TMA in
-// the 128-byte swizzle into a ring of 22 tiles of 8 KB (44 KB cover the latency of memory); 11 warps take the
+// One block per SM: a warp of its own looks the pages up, 20 tiles at a time, and brings keys and values by TMA in
+// the 128-byte swizzle into a ring of 20 tiles of 8 KB (44 KB cover the latency of memory); another
+// lays out the queries of the segment after the one in work; 10 warps take the
 // tiles in turns.
 #include <algorithm>
 #include <mutex>
@@ -31,11 +32,13 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 11, kConsumers = 32 * kWarps, kThreads = kConsumers + 32;
+constexpr int kWarps = 10, kConsumers = 32 * kWarps, kThreads = kConsumers + 64;   // and loader and query warps
 constexpr int kSlots = 2 * kWarps;                         // two of its own for each warp
 static_assert(kSlots <= 32, "a lane per slot");
 constexpr int kTileBytes = 2 * kDecodeTile * kPagedD;      // K and V of a tile
 constexpr int kWindow = kConsumers;                        // sequences looked at together
+constexpr int kSegs = 2;                                   // segments whose queries are ready
+constexpr int kSegWeight = 8;                              // what starting and ending one costs, in tiles
 constexpr float kSlack = 24.f;
 
 struct __align__(16) TileInfo {      // of the tile's two halves of 16 keys
@@ -47,17 +50,27 @@ struct __align__(16) TileInfo {      // of the tile's two halves of 16 keys
 };
 constexpr int kFull = 16 + 256 * 16;
 
+struct __align__(16) Segment {       // a block's piece of one
+    int64_t t0;
+    int head, n_rows, len, n_new;
+    int end;                         // one past its last tile, counted from the block's first of the window
+    int whole, starts;               // holds all tiles, the first one
+};
+
 struct DecodeSmem {
     uint8_t ring[kSlots][kTileBytes];
-    float o[kWarps][kDecodeRows][64];
+    float4 o[kWarps][kDecodeRows][kPagedD / 4];            // chunk i of row n at i ^ n / 2
+    uint4 q[kSegs][4][32];                                 // fragments of Q^T by lane: high parts, low parts
+    float f[kSegs][kDecodeRows];                           // logit factors of the rows
+    Segment seg[kSegs];
     float2 ml[kWarps][kDecodeRows];
     TileInfo info[kSlots];
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t full[kSlots], empty[kSlots], seg_full[kSegs], seg_empty[kSegs], joined;
     int last[kSlots];                                      // loads of a slot so far
-    long long pre[kWindow + 1];                            // tiles before each sequence of the window
+    long long pre[kWindow + 1], pre_u[kWindow + 1];        // tiles before each sequence of the window, and units
     int64_t t0[kWindow], first[kWindow];
     int n_new[kWindow], len[kWindow];
-    long long scan[kWarps];
+    long long scan[kWarps], scan_u[kWarps];
     int abort_flag;
 };
 
@@ -93,7 +106,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 // x0, x1 as e4m3 pairs: the nearest, and the nearest to what that leaves (all within fp16's range)
 __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t* hi, uint32_t* lo) {
     const __half2 y = __floats2half2_rn(x0, x1);
@@ -138,6 +150,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     // the combine pass may be launched: it waits for this grid's end before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) sm.abort_flag = 0;
+    if (tid == 0) mbar_init(smem_u32(&sm.joined), kWarps);
+    if (tid < kSegs) {
+        mbar_init(smem_u32(&sm.seg_full[tid]), 1);
+        mbar_init(smem_u32(&sm.seg_empty[tid]), kWarps);
+    }
     if (tid < kSlots) {
         mbar_init(smem_u32(&sm.full[tid]), 1);
         mbar_init(smem_u32(&sm.empty[tid]), 1);
@@ -146,19 +163,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
 
-    // tiles of all sequences: a thread per sequence of the window
+    // Tiles of all sequences, a thread per sequence of the window; and units, in which the blocks' shares are measured: a
+    // segment's tiles and kSegWeight more, so that a block with many short segments gets fewer tiles.
     const int n_windows = LIST ? 1 : (v.n_seq + kWindow - 1) / kWindow;
     const bool at_hand = LIST && v.n_seq <= kWindow;       // the offsets and lengths of all sequences in shared memory
-    auto load_window = [&](int w) -> long long {
+    struct Sums {
+        long long tiles, units;
+    };
+    auto load_window = [&](int w) -> Sums {
         const int s = w * kWindow + tid;
         SeqSpan sp{0, 0, 0};
         if (tid < kWindow && s < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, blockIdx.x == 0 ? a.err : nullptr);
-        const long long x = sp.n_new ? (long long)v.hkv * ((sp.len + kDecodeTile - 1) / kDecodeTile) : 0;
-        long long up = x;
+        const int per_head = sp.n_new ? (sp.len + kDecodeTile - 1) / kDecodeTile : 0;
+        long long up = (long long)v.hkv * per_head, up_u = per_head ? up + (long long)v.hkv * kSegWeight : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, up, o);
-            if (lane >= o) up += y;
+            const long long y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_up_sync(0xffffffffu, up_u, o);
+            if (lane >= o) {
+                up += y;
+                up_u += z;
+            }
         }
         __syncthreads();
         if (tid < kWindow) {
@@ -166,50 +190,78 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             if (LIST && s < v.n_seq) sm.first[tid] = a.tok_off[s];
             sm.n_new[tid] = sp.n_new;
             sm.len[tid] = sp.len;
-            if (lane == 31) sm.scan[warp] = up;
+            if (lane == 31) {
+                sm.scan[warp] = up;
+                sm.scan_u[warp] = up_u;
+            }
         }
         __syncthreads();
-        long long before = 0, all = 0;
+        long long before = 0, before_u = 0;
+        Sums all{0, 0};
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) before += sm.scan[i];
-            all += sm.scan[i];
+            const long long x = sm.scan[i], y = sm.scan_u[i];
+            if (i < warp) {
+                before += x;
+                before_u += y;
+            }
+            all.tiles += x;
+            all.units += y;
         }
-        if (tid < kWindow) sm.pre[tid + 1] = before + up;
-        if (tid == 0) sm.pre[0] = 0;
+        if (tid < kWindow) {
+            sm.pre[tid + 1] = before + up;
+            sm.pre_u[tid + 1] = before_u + up_u;
+        }
+        if (tid == 0) sm.pre[0] = sm.pre_u[0] = 0;
         __syncthreads();
         return all;
     };
-    long long total = 0, first_total = 0;
+    Sums total{0, 0}, first_total{0, 0};
     const int list_tiles = !LIST ? 1 : pairs ? (a.k + 1) / 2 : a.k * per_page;
     if (LIST) {
         if (at_hand) load_window(0);
         else __syncthreads();
-        total = first_total = a.n_tok * v.hkv * (long long)list_tiles;
+        total.tiles = total.units = a.n_tok * v.hkv * (long long)list_tiles;       // all segments are alike
+        first_total = total;
     } else {
         for (int w = n_windows - 1; w >= 0; --w) {
             first_total = load_window(w);
-            total += first_total;
+            total.tiles += first_total.tiles;
+            total.units += first_total.units;
         }
     }
-    const int n_cta = (int)min((long long)gridDim.x, (total + kMinDecodeTiles - 1) / kMinDecodeTiles);
+    // tiles of the window before its unit u
+    auto tiles_before = [&](long long u, int n_win) -> long long {
+        if (LIST) return u;
+        if (u >= sm.pre_u[n_win]) return sm.pre[n_win];
+        const int lo = find(sm.pre_u, n_win, u);
+        const int per_head = (sm.len[lo] + kDecodeTile - 1) / kDecodeTile;
+        const int head = quotient(u - sm.pre_u[lo], per_head + kSegWeight);
+        const int r = (int)(u - sm.pre_u[lo] - (long long)head * (per_head + kSegWeight));
+        return sm.pre[lo] + (long long)head * per_head + min(r, per_head);
+    };
+    const int n_cta = (int)min((long long)gridDim.x, total.tiles);
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
         return;
     }
-    const long long my_a = cta_first(total, n_cta, blockIdx.x), my_b = cta_first(total, n_cta, blockIdx.x + 1);
-    OpenSegment open{0, 0, 0, 0, 1.f};
+    const long long my_a = cta_first(total.units, n_cta, blockIdx.x), my_b = cta_first(total.units, n_cta, blockIdx.x + 1);
 
-    int done = 0;                                          // tiles of earlier windows: they give slot and phase
-    long long base = 0;                                    // tiles before the window
+    uint32_t joins = 0;
+    // the consuming warps have come this far; bounded, like every wait
+    auto join = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.joined));
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.joined), joins++ & 1u, abort_flag));
+    };
+    int done = 0, segs = 0;                                // tiles and segments of earlier windows: slots and phases
+    long long base = 0;                                    // units before the window
+    OpenSegment open{0, 0, 0, 0, 1.f};                     // the query warp's
     for (int w = 0; w < n_windows; ++w) {
-        const long long in_window = (w == 0) ? first_total : load_window(w);
-        const long long A = max(my_a - base, 0LL), B = min(my_b - base, in_window);
-        if (A >= B) {
-            base += in_window;
-            continue;
-        }
+        const Sums in_window = (w == 0) ? first_total : load_window(w);
+        const long long ua = max(my_a - base, 0LL), ub = min(my_b - base, in_window.units);
         const int n_win = LIST ? 0 : min(kWindow, v.n_seq - w * kWindow);
+        const long long A = ua < ub ? tiles_before(ua, n_win) : 0, B = ua < ub ? tiles_before(ub, n_win) : 0;
         const int count = (int)(B - A);
 
         // the sequence of packed row t; false where there is none
@@ -359,6 +411,100 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 }
                 if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             }
+        } else if (warp == kWarps + 1) {
+            // ------------------------------------------------------------------ queries: a segment ahead
+            const int r = lane >> 2, c = lane & 3;
+            int n_seg = segs;
+            for (long long g0 = A; g0 < B; ++n_seg) {
+                Segment sg;
+                long long seg_a, seg_b;
+                if (LIST) {
+                    const long long seg = g0 / list_tiles;
+                    sg.t0 = seg / v.hkv;
+                    sg.head = (int)(seg - sg.t0 * v.hkv);
+                    seg_a = seg * list_tiles;
+                    seg_b = seg_a + list_tiles;
+                    int s;
+                    SeqSpan sp;
+                    const bool live = seq_of(sg.t0, &s, &sp, nullptr);
+                    sg.len = sp.len - sp.n_new + (int)(sg.t0 - sp.t0) + 1;
+                    sg.n_new = live ? 1 : 0;
+                } else {
+                    const int lo = find(sm.pre, n_win, g0);
+                    sg.t0 = sm.t0[lo];
+                    sg.n_new = sm.n_new[lo];
+                    sg.len = sm.len[lo];
+                    const int per_head = (sg.len + kDecodeTile - 1) / kDecodeTile;
+                    sg.head = quotient(g0 - sm.pre[lo], per_head);
+                    seg_a = sm.pre[lo] + (long long)sg.head * per_head;
+                    seg_b = seg_a + per_head;
+                    if (seg_a == g0 && seg_b > B) {        // it goes on in other blocks: what the combine pass needs to know
+                        const long long u = base + sm.pre_u[lo] + (long long)sg.head * (per_head + kSegWeight) + per_head - 1;
+                        open = OpenSegment{sg.t0, sg.head, sg.n_new * G, cta_of_tile(total.units, n_cta, u) - (int)blockIdx.x, 1.f};
+                    }
+                }
+                if (LIST && sg.n_new && seg_a == g0 && seg_b > B)
+                    open = OpenSegment{sg.t0, sg.head, G, cta_of_tile(total.units, n_cta, seg_b - 1) - (int)blockIdx.x, 1.f};
+                const long long g1 = min(B, seg_b);
+                sg.n_rows = sg.n_new * G;
+                sg.end = (int)(g1 - A);
+                sg.starts = seg_a == g0;
+                sg.whole = sg.starts && seg_b == g1;
+
+                // the thread's part of Q^T: row n = r, elements 32 c .. 32 c + 31; the softmax scale's sign is Q's
+                uint4 x[4];
+                uint32_t qh[8], ql[8];
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
+                if (r < sg.n_rows) {
+                    const uint4* src = reinterpret_cast<const uint4*>(
+                        a.q + ((sg.t0 + (r >> gs)) * hq + sg.head * G + (r & (G - 1))) * kPagedD + 32 * c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = src[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                const uint32_t ub = __float_as_uint(top);
+                const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                const float inv = a.scale_log2e < 0.f ? -pow2f(-e) : pow2f(-e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t h0, l0, h1, l1;
+                        split_e4m3(__uint_as_float(u[2 * j] << 16) * inv, __uint_as_float(u[2 * j] & 0xFFFF0000u) * inv, &h0, &l0);
+                        split_e4m3(__uint_as_float(u[2 * j + 1] << 16) * inv, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * inv,
+                                   &h1, &l1);
+                        qh[2 * i + j] = h0 | (h1 << 16);
+                        ql[2 * i + j] = l0 | (l1 << 16);
+                    }
+                }
+                const float f = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fabsf(a.scale_log2e) * pow2f(e);
+                const int at = n_seg % kSegs;
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait(smem_u32(&sm.seg_empty[at]), ((uint32_t)(n_seg / kSegs) & 1u) ^ 1u, abort_flag)))
+                    break;
+                sm.q[at][0][lane] = make_uint4(qh[0], qh[1], qh[2], qh[3]);
+                sm.q[at][1][lane] = make_uint4(qh[4], qh[5], qh[6], qh[7]);
+                sm.q[at][2][lane] = make_uint4(ql[0], ql[1], ql[2], ql[3]);
+                sm.q[at][3][lane] = make_uint4(ql[4], ql[5], ql[6], ql[7]);
+                if (c == 0) sm.f[at][r] = f;
+                if (lane == 0) sm.seg[at] = sg;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.seg_full[at]));
+                g0 = g1;
+            }
+            segs = n_seg;
         } else {
             // ------------------------------------------------------------------ segment by segment
             const int r = lane >> 2, c = lane & 3;         // the thread's place in a fragment
@@ -370,80 +516,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             // The warp's tiles are those whose number (over all windows) leaves it as remainder, and so are its slots: with
             // slots that passed from warp to warp, one that runs ahead could not tell a phase from the next but one.
             int taken = ((warp - done) % kWarps + kWarps) % kWarps;
-            for (long long g0 = A; g0 < B;) {
-                long long seg_a, seg_b;
-                int64_t t0;
-                int head, n_rows, len, n_new;
-                bool live = true;
-                if (LIST) {
-                    const long long seg = g0 / list_tiles;
-                    t0 = seg / v.hkv;
-                    head = (int)(seg - t0 * v.hkv);
-                    seg_a = seg * list_tiles;
-                    seg_b = seg_a + list_tiles;
-                    int s;
-                    SeqSpan sp;
-                    live = seq_of(t0, &s, &sp, nullptr);
-                    len = sp.len - sp.n_new + (int)(t0 - sp.t0) + 1;
-                    n_new = 1;
-                } else {
-                    const int lo = find(sm.pre, n_win, g0);
-                    t0 = sm.t0[lo];
-                    n_new = sm.n_new[lo];
-                    len = sm.len[lo];
-                    const int per_head = (len + kDecodeTile - 1) / kDecodeTile;
-                    head = quotient(g0 - sm.pre[lo], per_head);
-                    seg_a = sm.pre[lo] + (long long)head * per_head;
-                    seg_b = seg_a + per_head;
-                }
-                n_rows = live ? n_new * G : 0;
-                const long long g1 = min(B, seg_b);
-                const int end = (int)(g1 - A);
-
-                // this thread's part of Q^T: row n = r, elements 32 c .. 32 c + 31; the softmax scale's sign is Q's
+            for (int end = 0; end < count;) {
+                const int at = segs % kSegs;
+                const bool ready = mbar_wait(smem_u32(&sm.seg_full[at]), (uint32_t)(segs / kSegs) & 1u, abort_flag);
+                if (__any_sync(0xffffffffu, !ready)) break;
+                ++segs;
+                const int64_t t0 = sm.seg[at].t0;
+                const int head = sm.seg[at].head, n_rows = sm.seg[at].n_rows, len = sm.seg[at].len, n_new = sm.seg[at].n_new;
+                const int whole = sm.seg[at].whole, starts = sm.seg[at].starts;
+                end = sm.seg[at].end;
                 uint32_t qh[8], ql[8];
-                float f0, f1;                              // logit factors of rows 2 c and 2 c + 1
                 {
-                    uint4 x[4];
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
-                    if (r < n_rows) {
-                        const uint4* src = reinterpret_cast<const uint4*>(
-                            a.q + ((t0 + (r >> gs)) * hq + head * G + (r & (G - 1))) * kPagedD + 32 * c);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = src[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[j] << 16)), fabsf(__uint_as_float(u[j] & 0xFFFF0000u))));
-                    }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
-                    const uint32_t ub = __float_as_uint(top);
-                    const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
-                    const float inv = a.scale_log2e < 0.f ? -pow2f(-e) : pow2f(-e);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t h0, l0, h1, l1;
-                            split_e4m3(__uint_as_float(u[2 * j] << 16) * inv, __uint_as_float(u[2 * j] & 0xFFFF0000u) * inv, &h0, &l0);
-                            split_e4m3(__uint_as_float(u[2 * j + 1] << 16) * inv, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * inv,
-                                       &h1, &l1);
-                            qh[2 * i + j] = h0 | (h1 << 16);
-                            ql[2 * i + j] = l0 | (l1 << 16);
-                        }
-                    }
-                    const float f = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fabsf(a.scale_log2e) * pow2f(e);
-                    f0 = __shfl_sync(0xffffffffu, f, 8 * c);
-                    f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+                    const uint4 x = sm.q[at][0][lane], y = sm.q[at][1][lane], z = sm.q[at][2][lane], u = sm.q[at][3][lane];
+                    qh[0] = x.x, qh[1] = x.y, qh[2] = x.z, qh[3] = x.w, qh[4] = y.x, qh[5] = y.y, qh[6] = y.z, qh[7] = y.w;
+                    ql[0] = z.x, ql[1] = z.y, ql[2] = z.z, ql[3] = z.w, ql[4] = u.x, ql[5] = u.y, ql[6] = u.z, ql[7] = u.w;
                 }
+                const float f0 = sm.f[at][2 * c], f1 = sm.f[at][2 * c + 1];    // logit factors of rows 2 c and 2 c + 1
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[at]));
                 const int seen0 = 2 * c < n_rows ? len - n_new + ((2 * c) >> gs) + 1 : 0;
                 const int seen1 = 2 * c + 1 < n_rows ? len - n_new + ((2 * c + 1) >> gs) + 1 : 0;
                 const int seen_all = len - n_new + 1;      // keys that every row sees
@@ -606,77 +696,61 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                     l0 += __shfl_xor_sync(0xffffffffu, l0, sh);
                     l1 += __shfl_xor_sync(0xffffffffu, l1, sh);
                 }
-                consumers_sync();                          // the last segment's values have been read
+                if (!join()) break;                        // the last segment's values have been read
                 if (lane < 4) {
                     sm.ml[warp][2 * c] = make_float2(m0, l0);
                     sm.ml[warp][2 * c + 1] = make_float2(m1, l1);
                 }
-                consumers_sync();
-                // lane i: warp i's maximum, sum and weight
-                const int mine = warp & 7;
-                const float2 ml = lane < kWarps ? sm.ml[lane][mine] : make_float2(ninf, 0.f);
-                float M = ml.x;
 #pragma unroll
-                for (int sh = 16; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
-                const float wt = ml.x == ninf ? 0.f : ex2(ml.x - M);
-                float L = ml.x == ninf ? ml.y : wt * ml.y;             // a sum without a maximum is 0 or NaN
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int sh = 16; sh >= 1; sh >>= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
-                float2 res[2];                                         // d = 16 (lane / 4) + 8 part + 2 (lane % 4) and the next
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    if (part) consumers_sync();
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float* x = o[4 * part + 2 * i];
-                            const float* y = o[4 * part + 2 * i + 1];
-                            *reinterpret_cast<float4*>(&sm.o[warp][2 * c + j][8 * r + 4 * i]) =
-                                make_float4(x[j], x[2 + j], y[j], y[2 + j]);
-                        }
-                    consumers_sync();
-                    res[part] = make_float2(0.f, 0.f);
-                    if (warp < n_rows) {
-#pragma unroll
-                        for (int i = 0; i < kWarps; ++i) {
-                            const float2 x = *reinterpret_cast<const float2*>(&sm.o[i][mine][2 * lane]);
-                            const float y = __shfl_sync(0xffffffffu, wt, i);
-                            res[part].x = fmaf(y, x.x, res[part].x);
-                            res[part].y = fmaf(y, x.y, res[part].y);
-                        }
-                    }
-                }
+                    for (int i = 0; i < 4; ++i)            // d = 16 r + 4 i
+                        sm.o[warp][2 * c + j][(4 * r + i) ^ c] =
+                            make_float4(o[2 * i][j], o[2 * i][2 + j], o[2 * i + 1][j], o[2 * i + 1][2 + j]);
+                if (!join()) break;
                 if (warp < n_rows) {
-                    const int d0 = 16 * (lane >> 2) + 2 * (lane & 3);
-                    if (seg_a == g0 && seg_b == g1) {
+                    // lane i: warp i's maximum, sum and weight
+                    const float2 ml = lane < kWarps ? sm.ml[lane][warp] : make_float2(ninf, 0.f);
+                    float M = ml.x;
+#pragma unroll
+                    for (int sh = 8; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, sh));
+                    const float wt = ml.x == ninf ? 0.f : ex2(ml.x - M);
+                    float L = ml.x == ninf ? ml.y : wt * ml.y;         // a sum without a maximum is 0 or NaN
+#pragma unroll
+                    for (int sh = 8; sh >= 1; sh >>= 1) L += __shfl_xor_sync(0xffffffffu, L, sh);
+                    M = __shfl_sync(0xffffffffu, M, 0);
+                    L = __shfl_sync(0xffffffffu, L, 0);
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < kWarps; ++i) {
+                        const float4 y = sm.o[i][warp][lane ^ (warp >> 1)];
+                        const float z = __shfl_sync(0xffffffffu, wt, i);
+                        x.x = fmaf(z, y.x, x.x);
+                        x.y = fmaf(z, y.y, x.y);
+                        x.z = fmaf(z, y.z, x.z);
+                        x.w = fmaf(z, y.w, x.w);
+                    }
+                    if (whole) {
                         const int64_t row = (t0 + (warp >> gs)) * hq + head * G + (warp & (G - 1));
                         const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            *reinterpret_cast<uint32_t*>(a.out + row * kPagedD + d0 + 8 * i) = pack_bf16(res[i].x * inv, res[i].y * inv);
+                        uint2 u;
+                        u.x = pack_bf16(x.x * inv, x.y * inv);
+                        u.y = pack_bf16(x.z * inv, x.w * inv);
+                        reinterpret_cast<uint2*>(a.out + row * kPagedD)[lane] = u;
                         if (a.lse && lane == 0) a.lse[row] = L == 0.f ? ninf : (M + log2f(L)) * 0.6931471805599453f;
                     } else {
-                        const int64_t row = ((int64_t)blockIdx.x * 2 + (seg_a == g0 ? 1 : 0)) * a.rows + warp;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(a.part_o + row * kPagedD + d0 + 8 * i) = res[i];
+                        const int64_t row = ((int64_t)blockIdx.x * 2 + starts) * a.rows + warp;
+                        reinterpret_cast<float4*>(a.part_o + row * kPagedD)[lane] = x;
                         if (lane == 0) a.part_ml[row] = make_float2(M, L);
                     }
                 }
-                if (seg_a == g0 && seg_b > g1 && live) {
-                    open.t0 = t0;
-                    open.head = head;
-                    open.rows = n_rows;
-                    open.n_more = cta_of_tile(total, n_cta, base + seg_b - 1) - (int)blockIdx.x;
-                }
-                g0 = g1;
             }
         }
         done += count;
-        base += in_window;
+        base += in_window.units;
         __syncthreads();
     }
-    if (tid == 0) a.open[blockIdx.x] = open;
+    if (tid == kConsumers + 32) a.open[blockIdx.x] = open;
     if (*abort_flag) {
         if (tid == 0) record_device_error(a.err, MSA_DEV_WAIT_TIMEOUT);
         // leave no copy in flight: each slot's last load
