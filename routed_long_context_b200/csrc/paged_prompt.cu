@@ -38,6 +38,7 @@ constexpr int kRowsTile = 128;                             // MMA M
 constexpr int kKStages = 3, kVStages = 2, kV16Stages = 2, kInfo = 8;
 constexpr int kWin = kPromptSeqs;                          // sequences of a launch, a thread each
 static_assert(kWin == kThreads, "a thread per sequence");
+constexpr int kSegWeight = 8;                              // what starting and ending a segment costs, in tiles
 constexpr float kTrigger = 32768.f;                        // a tile's sum above it moves the reference maximum
 constexpr float kSlack = 8.f;                            // log2 of how far logits may lie above the reference
 
@@ -58,7 +59,7 @@ struct PromptSmem {
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     int abort_flag, stop;
-    long long pre[kWin + 1];
+    long long pre[kWin + 1];                               // units before each sequence: a segment's tiles and kSegWeight more
     int64_t t0[kWin];
     int n_new[kWin], len[kWin];
     long long scan[kThreads / 32];
@@ -156,7 +157,7 @@ struct Piece {
     int s;                 // sequence
     int k0, n;             // first key tile, number of them
     bool starts, ends;     // holds the segment's first tile, its last
-    long long seg_end;     // one past the segment's last tile
+    long long seg_end;     // one past the unit of the segment's last tile
 };
 
 __device__ __forceinline__ int seg_tiles(int base, int n_new, int tpb, int rb) {
@@ -202,13 +203,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         tc_fence_before();
     }
 
-    // tiles of all sequences
+    // units of all sequences: a thread per sequence
     long long total = 0;
     {
         SeqSpan sp{0, 0, 0};
         if (tid < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, tid, &sp, blockIdx.x == 0 ? a.err : nullptr);
         long long x = 0;
-        for (int rb = 0; rb * tpb < sp.n_new; ++rb) x += seg_tiles(sp.len - sp.n_new, sp.n_new, tpb, rb);
+        for (int rb = 0; rb * tpb < sp.n_new; ++rb) x += seg_tiles(sp.len - sp.n_new, sp.n_new, tpb, rb) + kSegWeight;
         x *= v.hkv;
         long long up = x;
 #pragma unroll
@@ -230,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         sm.pre[tid + 1] = before + up;
         if (tid == 0) sm.pre[0] = 0;
     }
-    constexpr int kMinTiles = SPLIT ? 2 : 1;
-    const int n_cta = (int)min((long long)gridDim.x, (total + kMinTiles - 1) / kMinTiles);
+    constexpr int kMinUnits = 1 + kSegWeight;              // no block with a segment's weight alone
+    const int n_cta = (int)min((long long)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
         if (alloc) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     int pieces = 0;                                        // pieces (softmax: those in which the warpgroup had a tile)
     int loading_k = 0, loading_v = 0;                      // loader: tiles under way or in
     {
-        // the pieces of [A, B), in order; every role walks them for itself
+        // the pieces of units [A, B), in order; every role walks them for itself
         auto walk = [&](auto&& body) {
             int lo = 0, n = v.n_seq;
             while (n > 1) {
@@ -263,14 +264,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             int n_new = sm.n_new[lo], len = sm.len[lo];
             int tiles = seg_tiles(len - n_new, n_new, tpb, 0);
             long long start = sm.pre[lo];
-            while (start + (long long)tiles * v.hkv <= A) {
-                start += (long long)tiles * v.hkv;
+            while (start + (long long)(tiles + kSegWeight) * v.hkv <= A) {
+                start += (long long)(tiles + kSegWeight) * v.hkv;
                 tiles = seg_tiles(len - n_new, n_new, tpb, ++rb);
             }
-            head = (int)((A - start) / tiles);
-            start += (long long)head * tiles;
-            for (long long g = A; g < B;) {
-                const long long g1 = min(B, start + tiles);
+            head = (int)((A - start) / (tiles + kSegWeight));
+            start += (long long)head * (tiles + kSegWeight);
+            while (true) {
                 Piece p;
                 p.t0 = sm.t0[lo] + rb * tpb;
                 p.head = head;
@@ -278,19 +278,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 p.seen0 = len - n_new + rb * tpb + 1;
                 p.len = len;
                 p.s = lo;
-                p.k0 = (int)(g - start);
-                p.n = (int)(g1 - g);
-                p.starts = g == start;
-                p.ends = g1 == start + tiles;
+                p.k0 = (int)min((long long)tiles, max(0LL, A - start));
+                p.n = (int)min((long long)tiles, B - start) - p.k0;
+                p.starts = p.k0 == 0;
+                p.ends = p.k0 + p.n == tiles;
                 p.seg_end = start + tiles;
-                if (!body(p)) return;
-                g = g1;
-                if (!p.ends) return;
-                start = g1;
+                if (p.n > 0 && !body(p)) return;
+                start += tiles + kSegWeight;
+                if (start >= B) return;
                 if (++head == v.hkv) {
                     head = 0;
                     if (++rb * tpb >= n_new) {
-                        if (g >= B) return;                // there may be no further sequence
                         rb = 0;
                         do ++lo;
                         while (sm.n_new[lo] == 0);
@@ -301,7 +299,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                 }
             }
         };
-
         // 72 + 88 + 2 * 176 = 4 * 128 registers, what the block starts with
         if (warp < 4) {
         fewer_registers<72>();
@@ -633,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                                 mt = fmaxf(mt, fmaxf(y * (fr * sm.sk[info][2 * c]), z * (fr * sm.sk[info][2 * c + 1])));   // f > 0
                             }
                             move_max(mt);
+                            if (m == ninf) m = 0.f;                    // a row of NaN: it need not come here again
                         }
                         // against the reference maximum as it is; V's scale goes into P's exponent
                         const float ref = m == ninf ? 0.f : m;
