@@ -16,7 +16,13 @@
 // Two warpgroups take the two row blocks of 256 rows in turns (their products and exponentials overlap), or, of a
 // 128-row block, the even and the odd key tiles, joined at the end.
 // The products cost 8 * 128^3 flops a tile and row block, 1,024 cycles at the tensor peak; 128 * 128 exponentials take
-// as long on the special-function units: both bound it.
+// as long on the special-function units: both bound it. Measured, a tile of both row blocks takes 4,200 cycles: a
+// warpgroup's exponentials and their reading and writing of TMEM 2,100, its products 1,300 (shared memory feeds Q K^T no
+// faster), and what passes between them. 2,000 tokens of 32 heads over 18,000: 606 us, 918 TFLOP/s. Not faster: an issuer
+// of products for each warpgroup (764 us; in strict turns 655), steps of 64 keys with S ahead (738), part of the
+// exponentials by arithmetic (641 and more), waits by one lane of a warp (741).
+// With few tiles to a block, what starts and ends a segment is most of it: 8 sequences of up to 32 tokens over up to
+// 8,096 take 45 us, 57 where a segment's cost is left out of the blocks' shares.
 //
 // Roles of the 512 threads: warp 0 loads pages by TMA (128-byte swizzle, K three tiles deep, V two), warp 1 issues the
 // products, warps 4..11 run the softmax, warps 12..15 convert V. Every wait is bounded; when one runs out the block
@@ -40,7 +46,7 @@ constexpr int kWin = kPromptSeqs;                          // sequences of a lau
 static_assert(kWin == kThreads, "a thread per sequence");
 constexpr int kSegWeight = 8;                              // what starting and ending a segment costs, in tiles
 constexpr float kTrigger = 32768.f;                        // a tile's sum above it moves the reference maximum
-constexpr float kSlack = 8.f;                            // log2 of how far logits may lie above the reference
+constexpr float kSlack = 8.f;                              // log2 of how far logits may lie above the reference
 
 constexpr float kUnit = 1152921504606846976.f;             // 2^60, the unit in which O is kept
 
@@ -247,60 +253,59 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     int cnt = 0;                                           // tiles of earlier pieces
     int pieces = 0;                                        // pieces (softmax: those in which the warpgroup had a tile)
     int loading_k = 0, loading_v = 0;                      // loader: tiles under way or in
-    {
-        // the pieces of units [A, B), in order; every role walks them for itself
-        auto walk = [&](auto&& body) {
-            int lo = 0, n = v.n_seq;
-            while (n > 1) {
-                const int h = n / 2;
-                if (sm.pre[lo + h] <= A) {
-                    lo += h;
-                    n -= h;
-                } else {
-                    n = h;
+    // the pieces of units [A, B), in order; every role walks them for itself
+    auto walk = [&](auto&& body) {
+        int lo = 0, n = v.n_seq;
+        while (n > 1) {
+            const int h = n / 2;
+            if (sm.pre[lo + h] <= A) {
+                lo += h;
+                n -= h;
+            } else {
+                n = h;
+            }
+        }
+        int rb = 0, head = 0;
+        int n_new = sm.n_new[lo], len = sm.len[lo];
+        int tiles = seg_tiles(len - n_new, n_new, tpb, 0);
+        long long start = sm.pre[lo];
+        while (start + (long long)(tiles + kSegWeight) * v.hkv <= A) {
+            start += (long long)(tiles + kSegWeight) * v.hkv;
+            tiles = seg_tiles(len - n_new, n_new, tpb, ++rb);
+        }
+        head = (int)((A - start) / (tiles + kSegWeight));
+        start += (long long)head * (tiles + kSegWeight);
+        while (true) {
+            Piece p;
+            p.t0 = sm.t0[lo] + rb * tpb;
+            p.head = head;
+            p.rows = min(tpb, n_new - rb * tpb) * G;
+            p.seen0 = len - n_new + rb * tpb + 1;
+            p.len = len;
+            p.s = lo;
+            p.k0 = (int)min((long long)tiles, max(0LL, A - start));
+            p.n = (int)min((long long)tiles, B - start) - p.k0;
+            p.starts = p.k0 == 0;
+            p.ends = p.k0 + p.n == tiles;
+            p.seg_end = start + tiles;
+            if (p.n > 0 && !body(p)) return;
+            start += tiles + kSegWeight;
+            if (start >= B) return;
+            if (++head == v.hkv) {
+                head = 0;
+                if (++rb * tpb >= n_new) {
+                    rb = 0;
+                    do ++lo;
+                    while (sm.n_new[lo] == 0);
+                    n_new = sm.n_new[lo];
+                    len = sm.len[lo];
                 }
+                tiles = seg_tiles(len - n_new, n_new, tpb, rb);
             }
-            int rb = 0, head = 0;
-            int n_new = sm.n_new[lo], len = sm.len[lo];
-            int tiles = seg_tiles(len - n_new, n_new, tpb, 0);
-            long long start = sm.pre[lo];
-            while (start + (long long)(tiles + kSegWeight) * v.hkv <= A) {
-                start += (long long)(tiles + kSegWeight) * v.hkv;
-                tiles = seg_tiles(len - n_new, n_new, tpb, ++rb);
-            }
-            head = (int)((A - start) / (tiles + kSegWeight));
-            start += (long long)head * (tiles + kSegWeight);
-            while (true) {
-                Piece p;
-                p.t0 = sm.t0[lo] + rb * tpb;
-                p.head = head;
-                p.rows = min(tpb, n_new - rb * tpb) * G;
-                p.seen0 = len - n_new + rb * tpb + 1;
-                p.len = len;
-                p.s = lo;
-                p.k0 = (int)min((long long)tiles, max(0LL, A - start));
-                p.n = (int)min((long long)tiles, B - start) - p.k0;
-                p.starts = p.k0 == 0;
-                p.ends = p.k0 + p.n == tiles;
-                p.seg_end = start + tiles;
-                if (p.n > 0 && !body(p)) return;
-                start += tiles + kSegWeight;
-                if (start >= B) return;
-                if (++head == v.hkv) {
-                    head = 0;
-                    if (++rb * tpb >= n_new) {
-                        rb = 0;
-                        do ++lo;
-                        while (sm.n_new[lo] == 0);
-                        n_new = sm.n_new[lo];
-                        len = sm.len[lo];
-                    }
-                    tiles = seg_tiles(len - n_new, n_new, tpb, rb);
-                }
-            }
-        };
-        // 72 + 88 + 2 * 176 = 4 * 128 registers, what the block starts with
-        if (warp < 4) {
+        }
+    };
+    // 72 + 88 + 2 * 176 = 4 * 128 registers, what the block starts with
+    if (warp < 4) {
         fewer_registers<72>();
         if (warp == 0) {
             // ------------------------------------------------------------------ loader
@@ -446,381 +451,380 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             });
             a.open[blockIdx.x] = open;
         }
-        } else if (warp >= 12) {
-            fewer_registers<88>();
-            // ------------------------------------------------------------------ V to bf16
-            // Thread (row y of 16, piece c of 8): 16 values of rows y, y + 16, ...; the 32 bytes go to two 16-byte places
-            // of the swizzled bf16 tile, in an order that keeps the eight threads of a row on distinct banks.
-            const int ct = tid - 384, c = ct & 7, y = ct >> 3;
-            walk([&](const Piece& p) -> bool {
-                for (int j = 0; j < p.n; ++j) {
-                    const int n = cnt + j, vs = n % kVStages, v2 = n % kV16Stages;
-                    const bool in = mbar_wait(smem_u32(&sm.v8_full[vs]), (uint32_t)(n / kVStages) & 1u, abort_flag) &&
-                                    mbar_wait(smem_u32(&sm.v16_empty[v2]), ((uint32_t)(n / kV16Stages) & 1u) ^ 1u, abort_flag);
-                    if (!__all_sync(0xffffffffu, in)) return false;
-                    const int left = p.len - (p.k0 + j) * kKT;         // keys of the tile that the sequence has
-                    uint8_t* dst = sm.v16[v2] + (c >> 2) * (kKT * 128);
-                    const int odd = c >> 2;                            // values 8 .. 15 are written first
-                    uint4 u[8];
+    } else if (warp >= 12) {
+        fewer_registers<88>();
+        // ------------------------------------------------------------------ V to bf16
+        // Thread (row y of 16, piece c of 8): 16 values of rows y, y + 16, ...; the 32 bytes go to two 16-byte places
+        // of the swizzled bf16 tile, in an order that keeps the eight threads of a row on distinct banks.
+        const int ct = tid - 384, c = ct & 7, y = ct >> 3;
+        walk([&](const Piece& p) -> bool {
+            for (int j = 0; j < p.n; ++j) {
+                const int n = cnt + j, vs = n % kVStages, v2 = n % kV16Stages;
+                const bool in = mbar_wait(smem_u32(&sm.v8_full[vs]), (uint32_t)(n / kVStages) & 1u, abort_flag) &&
+                                mbar_wait(smem_u32(&sm.v16_empty[v2]), ((uint32_t)(n / kV16Stages) & 1u) ^ 1u, abort_flag);
+                if (!__all_sync(0xffffffffu, in)) return false;
+                const int left = p.len - (p.k0 + j) * kKT;         // keys of the tile that the sequence has
+                uint8_t* dst = sm.v16[v2] + (c >> 2) * (kKT * 128);
+                const int odd = c >> 2;                            // values 8 .. 15 are written first
+                uint4 u[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = 16 * i + y;
-                        u[i] = *reinterpret_cast<const uint4*>(sm.v8[vs] + row * 128 + ((c ^ (row & 7)) << 4));
-                    }
-                    const bool hole = left < kKT || sm.sk[n % kInfo][lane & 7] == 0.f;
-                    if (__any_sync(0xffffffffu, hole)) {               // anything may stand where no key is
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (16 * i + y >= left || sm.sk[n % kInfo][i] == 0.f) u[i] = make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = 16 * i + y;
-                        const uint32_t us[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            // high and low bytes of four bf16, sign and 0000eee, emmm0000: 2^-120 times the values
-                            const uint32_t h = (us[x] & 0x80808080u) | ((us[x] >> 4) & 0x07070707u);
-                            const uint32_t l = (us[x] << 4) & 0xF0F0F0F0u;
-                            o[2 * x] = __byte_perm(l, h, 0x5140);
-                            o[2 * x + 1] = __byte_perm(l, h, 0x7362);
-                        }
-                        const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
-                        const int at = ((2 * (c & 3) + odd) ^ (row & 7)) << 4;
-                        *reinterpret_cast<uint4*>(dst + row * 128 + at) = odd ? hi4 : lo4;
-                        *reinterpret_cast<uint4*>(dst + row * 128 + (at ^ 16)) = odd ? lo4 : hi4;
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(smem_u32(&sm.v16_full[v2]));
-                    mbar_arrive(smem_u32(&sm.v8_empty[vs]));
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 16 * i + y;
+                    u[i] = *reinterpret_cast<const uint4*>(sm.v8[vs] + row * 128 + ((c ^ (row & 7)) << 4));
                 }
-                cnt += p.n;
-                return true;
-            });
-        } else {
-            more_registers<176>();
-            // ------------------------------------------------------------------ softmax
-            const int wg = (warp - 4) >> 2, rl = (warp & 3) * 32 + lane;
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t ts = tmem + lanes + 128 * wg, to = tmem + lanes + 256 + 128 * wg;
-            uint32_t taken = 0;                            // tiles of this warpgroup
-            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag));
-                if (ok) tc_fence_after();
-                return ok;
-            };
-            walk([&](const Piece& p) -> bool {
-                const int row0 = (SPLIT ? 0 : wg * kRowsTile) + (warp & 3) * 32, row = row0 + lane;
-                const bool valid = row < p.rows;
-                const int seen = valid ? p.seen0 + (row >> gs) : 0;
-                const int seen_warp = p.seen0 + (row0 >> gs);              // of the warp's first row: the fewest of all
-                const int64_t gr = valid ? (p.t0 + (row >> gs)) * hq + p.head * G + (row & (G - 1)) : 0;
+                const bool hole = left < kKT || sm.sk[n % kInfo][lane & 7] == 0.f;
+                if (__any_sync(0xffffffffu, hole)) {               // anything may stand where no key is
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (16 * i + y >= left || sm.sk[n % kInfo][i] == 0.f) u[i] = make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 16 * i + y;
+                    const uint32_t us[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        // high and low bytes of four bf16, sign and 0000eee, emmm0000: 2^-120 times the values
+                        const uint32_t h = (us[x] & 0x80808080u) | ((us[x] >> 4) & 0x07070707u);
+                        const uint32_t l = (us[x] << 4) & 0xF0F0F0F0u;
+                        o[2 * x] = __byte_perm(l, h, 0x5140);
+                        o[2 * x + 1] = __byte_perm(l, h, 0x7362);
+                    }
+                    const uint4 lo4 = make_uint4(o[0], o[1], o[2], o[3]), hi4 = make_uint4(o[4], o[5], o[6], o[7]);
+                    const int at = ((2 * (c & 3) + odd) ^ (row & 7)) << 4;
+                    *reinterpret_cast<uint4*>(dst + row * 128 + at) = odd ? hi4 : lo4;
+                    *reinterpret_cast<uint4*>(dst + row * 128 + (at ^ 16)) = odd ? lo4 : hi4;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(smem_u32(&sm.v16_full[v2]));
+                mbar_arrive(smem_u32(&sm.v8_empty[vs]));
+            }
+            cnt += p.n;
+            return true;
+        });
+    } else {
+        more_registers<176>();
+        // ------------------------------------------------------------------ softmax
+        const int wg = (warp - 4) >> 2, rl = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128 * wg, to = tmem + lanes + 256 + 128 * wg;
+        uint32_t taken = 0;                            // tiles of this warpgroup
+        auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag));
+            if (ok) tc_fence_after();
+            return ok;
+        };
+        walk([&](const Piece& p) -> bool {
+            const int row0 = (SPLIT ? 0 : wg * kRowsTile) + (warp & 3) * 32, row = row0 + lane;
+            const bool valid = row < p.rows;
+            const int seen = valid ? p.seen0 + (row >> gs) : 0;
+            const int seen_warp = p.seen0 + (row0 >> gs);              // of the warp's first row: the fewest of all
+            const int64_t gr = valid ? (p.t0 + (row >> gs)) * hq + p.head * G + (row & (G - 1)) : 0;
 
-                // queries: half a warp per row, eight elements a lane, the two parts in 8-byte pieces; of a shared row block
-                // each warpgroup does half
+            // queries: half a warp per row, eight elements a lane, the two parts in 8-byte pieces; of a shared row block
+            // each warpgroup does half
+            {
+                const int half = lane >> 4, piece = lane & 15;
+                uint8_t* hi = sm.q[SPLIT ? 0 : wg][0];
+                uint8_t* lo = sm.q[SPLIT ? 0 : wg][1];
+                const int first = (warp & 3) * 32 + (SPLIT ? 16 * wg : 0);
+                constexpr int kIter = SPLIT ? 8 : 16;
+#pragma unroll 1
+                for (int i0 = 0; i0 < kIter; i0 += 8) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = (SPLIT ? 0 : wg * kRowsTile) + first + 2 * (i0 + i) + half;
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (r < p.rows)
+                            x[i] = *reinterpret_cast<const uint4*>(
+                                a.q + ((p.t0 + (r >> gs)) * hq + p.head * G + (r & (G - 1))) * kPagedD + 8 * piece);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(u);
+                        const __nv_bfloat162 t2 = __hmax2(__hmax2(__habs2(b[0]), __habs2(b[1])), __hmax2(__habs2(b[2]), __habs2(b[3])));
+                        float top = fmaxf(__low2float(t2), __high2float(t2));
+#pragma unroll
+                        for (int o = 8; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                        const uint32_t ub = __float_as_uint(top);
+                        const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                        const float inv = a.scale_log2e < 0.f ? -pow2f(-e) : pow2f(-e);
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2 y = __floats2half2_rn(__uint_as_float(u[k] << 16) * inv,
+                                                                __uint_as_float(u[k] & 0xFFFF0000u) * inv);
+                            h[k] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                            const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h[k], __NV_E4M3);
+                            l[k] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(
+                                __hsub2(y, *reinterpret_cast<const __half2*>(&back)), __NV_SATFINITE, __NV_E4M3);
+                        }
+                        const int rr = first + 2 * (i0 + i) + half;
+                        const int at = rr * kPagedD + (((piece >> 1) ^ (rr & 7)) << 4) + 8 * (piece & 1);
+                        *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+                        *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+                        if (piece == 0) sm.fr[SPLIT ? 0 : wg][rr] = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fabsf(a.scale_log2e) * pow2f(e);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(smem_u32(&sm.q_full[SPLIT ? 0 : wg]));
+                __syncwarp();
+            }
+
+            float m = valid ? ninf : 0.f, l = 0.f, le = 0.f;       // le: roundings of l
+            bool any = false;                                      // O holds something
+            bool ok = true;
+            for (int j = SPLIT ? wg : 0; j < p.n; j += SPLIT ? 2 : 1) {
+                if (!(ok = wait(&sm.s_full[wg], taken & 1u))) break;
+                ++taken;
+                const float fr = sm.fr[SPLIT ? 0 : wg][rl];        // written before the products that s_full reports
+                const int info = (cnt + j) % kInfo;
+                float f[8];                                        // logit factors, 16 columns each
+                bool hole = false;                                 // a page that is not there
                 {
-                    const int half = lane >> 4, piece = lane & 15;
-                    uint8_t* hi = sm.q[SPLIT ? 0 : wg][0];
-                    uint8_t* lo = sm.q[SPLIT ? 0 : wg][1];
-                    const int first = (warp & 3) * 32 + (SPLIT ? 16 * wg : 0);
-                    constexpr int kIter = SPLIT ? 8 : 16;
-#pragma unroll 1
-                    for (int i0 = 0; i0 < kIter; i0 += 8) {
-                        uint4 x[8];
+                    const float4* sk = reinterpret_cast<const float4*>(sm.sk[info]);
+                    const float4 u = sk[0], w = sk[1];
+                    f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = w.x, f[5] = w.y, f[6] = w.z, f[7] = w.w;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = (SPLIT ? 0 : wg * kRowsTile) + first + 2 * (i0 + i) + half;
-                            x[i] = make_uint4(0, 0, 0, 0);
-                            if (r < p.rows)
-                                x[i] = *reinterpret_cast<const uint4*>(
-                                    a.q + ((p.t0 + (r >> gs)) * hq + p.head * G + (r & (G - 1))) * kPagedD + 8 * piece);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                            const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(u);
-                            const __nv_bfloat162 t2 = __hmax2(__hmax2(__habs2(b[0]), __habs2(b[1])), __hmax2(__habs2(b[2]), __habs2(b[3])));
-                            float top = fmaxf(__low2float(t2), __high2float(t2));
-#pragma unroll
-                            for (int o = 8; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                            // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
-                            const uint32_t ub = __float_as_uint(top);
-                            const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
-                            const float inv = a.scale_log2e < 0.f ? -pow2f(-e) : pow2f(-e);
-                            uint32_t h[4], l[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __half2 y = __floats2half2_rn(__uint_as_float(u[k] << 16) * inv,
-                                                                    __uint_as_float(u[k] & 0xFFFF0000u) * inv);
-                                h[k] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-                                const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h[k], __NV_E4M3);
-                                l[k] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(
-                                    __hsub2(y, *reinterpret_cast<const __half2*>(&back)), __NV_SATFINITE, __NV_E4M3);
-                            }
-                            const int rr = first + 2 * (i0 + i) + half;
-                            const int at = rr * kPagedD + (((piece >> 1) ^ (rr & 7)) << 4) + 8 * (piece & 1);
-                            *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-                            *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-                            if (piece == 0) sm.fr[SPLIT ? 0 : wg][rr] = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fabsf(a.scale_log2e) * pow2f(e);
-                        }
+                    for (int i = 0; i < 8; ++i) {
+                        hole |= f[i] == 0.f;
+                        f[i] *= fr;
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(smem_u32(&sm.q_full[SPLIT ? 0 : wg]));
-                    __syncwarp();
                 }
-
-                float m = valid ? ninf : 0.f, l = 0.f, le = 0.f;       // le: roundings of l
-                bool any = false;                                      // O holds something
-                bool ok = true;
-                for (int j = SPLIT ? wg : 0; j < p.n; j += SPLIT ? 2 : 1) {
-                    if (!(ok = wait(&sm.s_full[wg], taken & 1u))) break;
-                    ++taken;
-                    const float fr = sm.fr[SPLIT ? 0 : wg][rl];        // written before the products that s_full reports
-                    const int info = (cnt + j) % kInfo;
-                    float f[8];                                        // logit factors, 16 columns each
-                    bool hole = false;                                 // a page that is not there
-                    {
-                        const float4* sk = reinterpret_cast<const float4*>(sm.sk[info]);
-                        const float4 u = sk[0], w = sk[1];
-                        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = w.x, f[5] = w.y, f[6] = w.z, f[7] = w.w;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            hole |= f[i] == 0.f;
-                            f[i] *= fr;
-                        }
-                    }
-                    const int key0 = (p.k0 + j) * kKT;
-                    float sum = 0.f;
-                    // a new reference maximum, of sum and O, unless the old one will do for all of the warp's rows
-                    auto move_max = [&](float mt) {
-                        if (!__any_sync(0xffffffffu, mt > m + kSlack)) return;
-                        mt = fmaxf(mt, m);
-                        const float al = m == mt ? 1.f : ex2(m - mt);
-                        m = mt;
-                        l *= al;
-                        le *= al;
-                        if (any) {
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t x[32];
-                                tmem_issue32(to + 32 * c, x);
-                                tmem_wait32(x);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
-                                tmem_st32_u32(to + 32 * c, x);
-                            }
-                        }
-                    };
-                    bool slow = hole || key0 + kKT > seen_warp;
-                    if (!slow) {
-                        uint32_t xa[32], xb[32], pk[64];
-                        if (__any_sync(0xffffffffu, m == ninf)) {      // the row's first keys
-                            float mt = m;
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                tmem_issue32(ts + 32 * c, xa);
-                                tmem_wait32(xa);
-                                float y = ninf, z = ninf;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    y = fmaxf(y, __uint_as_float(xa[i]));
-                                    z = fmaxf(z, __uint_as_float(xa[16 + i]));
-                                }
-                                mt = fmaxf(mt, fmaxf(y * (fr * sm.sk[info][2 * c]), z * (fr * sm.sk[info][2 * c + 1])));   // f > 0
-                            }
-                            move_max(mt);
-                            if (m == ninf) m = 0.f;                    // a row of NaN: it need not come here again
-                        }
-                        // against the reference maximum as it is; V's scale goes into P's exponent
-                        const float ref = m == ninf ? 0.f : m;
-                        const float4* evs = reinterpret_cast<const float4*>(sm.ev[info]);
-                        const float4* ivs = reinterpret_cast<const float4*>(sm.iv[info]);
-                        const float4 e4[2] = {evs[0], evs[1]}, i4[2] = {ivs[0], ivs[1]};
-                        auto part = [&](uint32_t (&x)[32], int at) {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int c = 2 * at + h;
-                                const float ff = f[c], nm = (&e4[c >> 2].x)[c & 3] - ref;
-                                uint64_t sum2 = 0;
-#pragma unroll
-                                for (int i = 16 * h; i < 16 * h + 16; i += 2) {
-                                    const uint64_t y = fma2(pair_u(x[i], x[i + 1]), pair(ff, ff), pair(nm, nm));
-                                    const float p0 = ex2(first(y)), p1 = ex2(second(y));
-                                    sum2 = add2(sum2, pair(p0, p1));
-                                    pk[16 * at + i / 2] = pack_bf16(p0, p1);
-                                }
-                                sum = fmaf(first(sum2) + second(sum2), (&i4[c >> 2].x)[c & 3], sum);
-                            }
-                        };
-                        tmem_issue32(ts, xa);
-                        tmem_wait32(xa);
-                        tmem_issue32(ts + 32, xb);
-                        part(xa, 0);
-                        tmem_wait32(xb);
-                        tmem_issue32(ts + 64, xa);
-                        part(xb, 1);
-                        tmem_wait32(xa);
-                        tmem_issue32(ts + 96, xb);
-                        part(xa, 2);
-                        tmem_wait32(xb);
-                        part(xb, 3);
-                        slow = __any_sync(0xffffffffu, sum > kTrigger);
-                        if (!slow) {
-                            tmem_st32_u32(ts, pk);
-                            tmem_st32_u32(ts + 32, pk + 32);
-                        }
-                    }
-                    if (slow) {
-                        // masked tiles, and those that move the maximum: 32 columns at a time
-                        const int vis = seen - key0;
-                        const float* sk = sm.sk[info];
-                        float mt = m;
+                const int key0 = (p.k0 + j) * kKT;
+                float sum = 0.f;
+                // a new reference maximum, of sum and O, unless the old one will do for all of the warp's rows
+                auto move_max = [&](float mt) {
+                    if (!__any_sync(0xffffffffu, mt > m + kSlack)) return;
+                    mt = fmaxf(mt, m);
+                    const float al = m == mt ? 1.f : ex2(m - mt);
+                    m = mt;
+                    l *= al;
+                    le *= al;
+                    if (any) {
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t x[32];
-                            tmem_issue32(ts + 32 * c, x);
+                            tmem_issue32(to + 32 * c, x);
                             tmem_wait32(x);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float ks = sk[2 * c + (i >> 4)];
-                                mt = fmaxf(mt, (32 * c + i < vis && ks != 0.f) ? __uint_as_float(x[i]) * (fr * ks) : ninf);
-                            }
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
+                            tmem_st32_u32(to + 32 * c, x);
                         }
-                        move_max(mt);
-                        const float ref = m == ninf ? 0.f : m;
-                        sum = 0.f;
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {                  // P overwrites columns that have been read
-                            uint32_t x[32], y[16];
-                            tmem_issue32(ts + 32 * c, x);
-                            tmem_wait32(x);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float ks = sk[2 * c + h], ff = fr * ks, nm = sm.ev[info][2 * c + h] - ref;
-                                float part = 0.f;
-#pragma unroll
-                                for (int i = 16 * h; i < 16 * h + 16; i += 2) {
-                                    float q[2];
-#pragma unroll
-                                    for (int k = 0; k < 2; ++k) {
-                                        q[k] = (32 * c + i + k < vis && ks != 0.f) ? ex2(fmaf(__uint_as_float(x[i + k]), ff, nm)) : 0.f;
-                                        part += q[k];
-                                    }
-                                    y[i / 2] = pack_bf16(q[0], q[1]);
-                                }
-                                sum = fmaf(part, sm.iv[info][2 * c + h], sum);
-                            }
-                            tmem_st16_u32(ts + 16 * c, y);
-                        }
-                    }
-                    any = true;
-                    {
-                        const float d = sum - le, t = l + d;
-                        le = (t - l) - d;
-                        l = t;
-                    }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                    mbar_arrive(smem_u32(&sm.p_full[wg]));
-                }
-                if (ok && any) ok = wait(&sm.o_done[wg], (uint32_t)pieces & 1u);
-                if (any) ++pieces;
-                if (!SPLIT && !ok) return false;
-                cnt += p.n;
-
-                // out, or the workspace
-                const bool whole = p.starts && p.ends;
-                const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (p.starts ? 1 : 0)) * a.rows + row0;
-                // a piece of a row: four columns from `col` on of row r of the warp's
-                auto put = [&](int r, int col, float4 y) {
-                    const int rr = row0 + r;
-                    if (rr >= p.rows) return;
-                    if (whole) {
-                        uint2 u;
-                        u.x = pack_bf16(y.x, y.y);
-                        u.y = pack_bf16(y.z, y.w);
-                        const int off = ((rr >> gs) * hq + (rr & (G - 1))) * kPagedD + col;
-                        *reinterpret_cast<uint2*>(a.out + (p.t0 * hq + p.head * G) * kPagedD + off) = u;
-                    } else {
-                        *reinterpret_cast<float4*>(a.part_o + slot0 * kPagedD + r * kPagedD + col) = y;
                     }
                 };
-                if (SPLIT) {
-                    // Both warpgroups' parts are joined, each warpgroup for half of the columns: the other half goes to the
-                    // other one through the place of the queries (the first row block's for columns 0 .. 63, which
-                    // warpgroup 1 writes). Named barrier 1 holds the two together.
-                    sm.ml[wg][rl] = make_float2(m, l);
-                    asm volatile("bar.sync 1, 256;" ::: "memory");     // no product reads the queries any more
-                    const float2 other = sm.ml[wg ^ 1][rl];
-                    const float M = fmaxf(m, other.x);
-                    float w0 = m == ninf ? 0.f : ex2(m - M), w1 = other.x == ninf ? 0.f : ex2(other.x - M);
-                    l = (m == ninf ? l : w0 * l) + (other.x == ninf ? other.y : w1 * other.y);
-                    m = M;
-                    float x[64];
-                    tmem_ld64(to + 64 * (wg ^ 1), x);
-                    float4* theirs = reinterpret_cast<float4*>(sm.q[wg ^ 1][0]) + rl * 16;
+                bool slow = hole || key0 + kKT > seen_warp;
+                if (!slow) {
+                    uint32_t xa[32], xb[32], pk[64];
+                    if (__any_sync(0xffffffffu, m == ninf)) {      // the row's first keys
+                        float mt = m;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_issue32(ts + 32 * c, xa);
+                            tmem_wait32(xa);
+                            float y = ninf, z = ninf;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) theirs[i ^ (rl & 15)] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    tmem_ld64(to + 64 * wg, x);
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
-                    const float f = !whole ? 1.f : l == 0.f ? 0.f : kUnit / l;
-                    w0 *= f;
-                    w1 *= f;
-                    float4* mine = reinterpret_cast<float4*>(sm.q[wg][0]) + rl * 16;
+                            for (int i = 0; i < 16; ++i) {
+                                y = fmaxf(y, __uint_as_float(xa[i]));
+                                z = fmaxf(z, __uint_as_float(xa[16 + i]));
+                            }
+                            mt = fmaxf(mt, fmaxf(y * (fr * sm.sk[info][2 * c]), z * (fr * sm.sk[info][2 * c + 1])));   // f > 0
+                        }
+                        move_max(mt);
+                        if (m == ninf) m = 0.f;                    // a row of NaN: it need not come here again
+                    }
+                    // against the reference maximum as it is; V's scale goes into P's exponent
+                    const float ref = m == ninf ? 0.f : m;
+                    const float4* evs = reinterpret_cast<const float4*>(sm.ev[info]);
+                    const float4* ivs = reinterpret_cast<const float4*>(sm.iv[info]);
+                    const float4 e4[2] = {evs[0], evs[1]}, i4[2] = {ivs[0], ivs[1]};
+                    auto part = [&](uint32_t (&x)[32], int at) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float4 y = mine[i ^ (rl & 15)];          // a part without a key may hold anything
-                        float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (w0 != 0.f) z = make_float4(w0 * x[4 * i], w0 * x[4 * i + 1], w0 * x[4 * i + 2], w0 * x[4 * i + 3]);
-                        if (w1 != 0.f) z = make_float4(fmaf(w1, y.x, z.x), fmaf(w1, y.y, z.y), fmaf(w1, y.z, z.z), fmaf(w1, y.w, z.w));
-                        mine[i ^ (rl & 15)] = z;
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = 2 * at + h;
+                            const float ff = f[c], nm = (&e4[c >> 2].x)[c & 3] - ref;
+                            uint64_t sum2 = 0;
+#pragma unroll
+                            for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+                                const uint64_t y = fma2(pair_u(x[i], x[i + 1]), pair(ff, ff), pair(nm, nm));
+                                const float p0 = ex2(first(y)), p1 = ex2(second(y));
+                                sum2 = add2(sum2, pair(p0, p1));
+                                pk[16 * at + i / 2] = pack_bf16(p0, p1);
+                            }
+                            sum = fmaf(first(sum2) + second(sum2), (&i4[c >> 2].x)[c & 3], sum);
+                        }
+                    };
+                    tmem_issue32(ts, xa);
+                    tmem_wait32(xa);
+                    tmem_issue32(ts + 32, xb);
+                    part(xa, 0);
+                    tmem_wait32(xb);
+                    tmem_issue32(ts + 64, xa);
+                    part(xb, 1);
+                    tmem_wait32(xa);
+                    tmem_issue32(ts + 96, xb);
+                    part(xa, 2);
+                    tmem_wait32(xb);
+                    part(xb, 3);
+                    slow = __any_sync(0xffffffffu, sum > kTrigger);
+                    if (!slow) {
+                        tmem_st32_u32(ts, pk);
+                        tmem_st32_u32(ts + 32, pk + 32);
+                    }
+                }
+                if (slow) {
+                    // masked tiles, and those that move the maximum: 32 columns at a time
+                    const int vis = seen - key0;
+                    const float* sk = sm.sk[info];
+                    float mt = m;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_issue32(ts + 32 * c, x);
+                        tmem_wait32(x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float ks = sk[2 * c + (i >> 4)];
+                            mt = fmaxf(mt, (32 * c + i < vis && ks != 0.f) ? __uint_as_float(x[i]) * (fr * ks) : ninf);
+                        }
+                    }
+                    move_max(mt);
+                    const float ref = m == ninf ? 0.f : m;
+                    sum = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {                  // P overwrites columns that have been read
+                        uint32_t x[32], y[16];
+                        tmem_issue32(ts + 32 * c, x);
+                        tmem_wait32(x);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float ks = sk[2 * c + h], ff = fr * ks, nm = sm.ev[info][2 * c + h] - ref;
+                            float part = 0.f;
+#pragma unroll
+                            for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+                                float q[2];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    q[k] = (32 * c + i + k < vis && ks != 0.f) ? ex2(fmaf(__uint_as_float(x[i + k]), ff, nm)) : 0.f;
+                                    part += q[k];
+                                }
+                                y[i / 2] = pack_bf16(q[0], q[1]);
+                            }
+                            sum = fmaf(part, sm.iv[info][2 * c + h], sum);
+                        }
+                        tmem_st16_u32(ts + 16 * c, y);
+                    }
+                }
+                any = true;
+                {
+                    const float d = sum - le, t = l + d;
+                    le = (t - l) - d;
+                    l = t;
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sm.p_full[wg]));
+            }
+            if (ok && any) ok = wait(&sm.o_done[wg], (uint32_t)pieces & 1u);
+            if (any) ++pieces;
+            if (!SPLIT && !ok) return false;
+            cnt += p.n;
+
+            // out, or the workspace
+            const bool whole = p.starts && p.ends;
+            const int64_t slot0 = ((int64_t)blockIdx.x * 2 + (p.starts ? 1 : 0)) * a.rows + row0;
+            // a piece of a row: four columns from `col` on of row r of the warp's
+            auto put = [&](int r, int col, float4 y) {
+                const int rr = row0 + r;
+                if (rr >= p.rows) return;
+                if (whole) {
+                    uint2 u;
+                    u.x = pack_bf16(y.x, y.y);
+                    u.y = pack_bf16(y.z, y.w);
+                    const int off = ((rr >> gs) * hq + (rr & (G - 1))) * kPagedD + col;
+                    *reinterpret_cast<uint2*>(a.out + (p.t0 * hq + p.head * G) * kPagedD + off) = u;
+                } else {
+                    *reinterpret_cast<float4*>(a.part_o + slot0 * kPagedD + r * kPagedD + col) = y;
+                }
+            };
+            if (SPLIT) {
+                // Both warpgroups' parts are joined, each warpgroup for half of the columns: the other half goes to the
+                // other one through the place of the queries (the first row block's for columns 0 .. 63, which
+                // warpgroup 1 writes). Named barrier 1 holds the two together.
+                sm.ml[wg][rl] = make_float2(m, l);
+                asm volatile("bar.sync 1, 256;" ::: "memory");     // no product reads the queries any more
+                const float2 other = sm.ml[wg ^ 1][rl];
+                const float M = fmaxf(m, other.x);
+                float w0 = m == ninf ? 0.f : ex2(m - M), w1 = other.x == ninf ? 0.f : ex2(other.x - M);
+                l = (m == ninf ? l : w0 * l) + (other.x == ninf ? other.y : w1 * other.y);
+                m = M;
+                float x[64];
+                tmem_ld64(to + 64 * (wg ^ 1), x);
+                float4* theirs = reinterpret_cast<float4*>(sm.q[wg ^ 1][0]) + rl * 16;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) theirs[i ^ (rl & 15)] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                tmem_ld64(to + 64 * wg, x);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                const float f = !whole ? 1.f : l == 0.f ? 0.f : kUnit / l;
+                w0 *= f;
+                w1 *= f;
+                float4* mine = reinterpret_cast<float4*>(sm.q[wg][0]) + rl * 16;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 y = mine[i ^ (rl & 15)];          // a part without a key may hold anything
+                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (w0 != 0.f) z = make_float4(w0 * x[4 * i], w0 * x[4 * i + 1], w0 * x[4 * i + 2], w0 * x[4 * i + 3]);
+                    if (w1 != 0.f) z = make_float4(fmaf(w1, y.x, z.x), fmaf(w1, y.y, z.y), fmaf(w1, y.z, z.z), fmaf(w1, y.w, z.w));
+                    mine[i ^ (rl & 15)] = z;
+                }
+                __syncwarp();
+                // sixteen lanes write a row's half
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const int r = 2 * i + (lane >> 4), c = lane & 15;
+                    put(r, 64 * wg + 4 * c, reinterpret_cast<const float4*>(sm.q[wg][0])[((warp & 3) * 32 + r) * 16 + (c ^ (r & 15))]);
+                }
+            } else {
+                // 32 columns of the warp's rows at a time, through the place of its queries (which no product reads any
+                // more), so that eight lanes write a row's piece
+                const float f = !whole ? 1.f : l == 0.f ? 0.f : kUnit / l;
+#pragma unroll 1
+                for (int part = 0; part < 4; ++part) {
+                    float x[32];
+                    tmem_ld32(to + 32 * part, x);
+                    float4* stage = reinterpret_cast<float4*>(sm.q[wg][part & 1] + (warp & 3) * 32 * kPagedD);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        stage[lane * 8 + (i ^ (lane & 7))] = make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3), c = lane & 7;
+                        put(r, 32 * part + 4 * c, stage[r * 8 + (c ^ (r & 7))]);
                     }
                     __syncwarp();
-                    // sixteen lanes write a row's half
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = 2 * i + (lane >> 4), c = lane & 15;
-                        put(r, 64 * wg + 4 * c, reinterpret_cast<const float4*>(sm.q[wg][0])[((warp & 3) * 32 + r) * 16 + (c ^ (r & 15))]);
-                    }
+                }
+            }
+            if (valid && (!SPLIT || wg == 0)) {
+                if (whole) {
+                    if (a.lse) a.lse[gr] = l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
                 } else {
-                    // 32 columns of the warp's rows at a time, through the place of its queries (which no product reads any
-                    // more), so that eight lanes write a row's piece
-                    const float f = !whole ? 1.f : l == 0.f ? 0.f : kUnit / l;
-#pragma unroll 1
-                    for (int part = 0; part < 4; ++part) {
-                        float x[32];
-                        tmem_ld32(to + 32 * part, x);
-                        float4* stage = reinterpret_cast<float4*>(sm.q[wg][part & 1] + (warp & 3) * 32 * kPagedD);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            stage[lane * 8 + (i ^ (lane & 7))] = make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
-                        __syncwarp();
-#pragma unroll 4
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3), c = lane & 7;
-                            put(r, 32 * part + 4 * c, stage[r * 8 + (c ^ (r & 7))]);
-                        }
-                        __syncwarp();
-                    }
+                    a.part_ml[slot0 + lane] = make_float2(m, l);
                 }
-                if (valid && (!SPLIT || wg == 0)) {
-                    if (whole) {
-                        if (a.lse) a.lse[gr] = l == 0.f ? ninf : (m + log2f(l)) * 0.6931471805599453f;
-                    } else {
-                        a.part_ml[slot0 + lane] = make_float2(m, l);
-                    }
-                }
-                tc_fence_before();
-                if (SPLIT) {
-                    // the next piece's queries may come; both warpgroups go on, or neither
-                    if (wg == 0 && rl == 0) sm.stop = *abort_flag;
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
-                    return sm.stop == 0;
-                }
-                return true;
-            });
-        }
+            }
+            tc_fence_before();
+            if (SPLIT) {
+                // the next piece's queries may come; both warpgroups go on, or neither
+                if (wg == 0 && rl == 0) sm.stop = *abort_flag;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                return sm.stop == 0;
+            }
+            return true;
+        });
     }
     __syncthreads();
     if (*abort_flag) {
