@@ -64,6 +64,7 @@ constexpr int kSms = 148;
 
 struct AttnPlan {
     bool few;                     // the few-rows kernel
+    bool uncut;                   // no segment will be cut: there is nothing to combine
     int grid, rows;
     size_t o, ml, open, bytes;    // offsets in the workspace
 };
@@ -71,19 +72,21 @@ AttnPlan attn_plan(int64_t n_tok, int n_seq, int max_new, int hq, int hkv, int m
     AttnPlan p{};
     const int G = hq / hkv;
     p.few = k > 0 || (int64_t)max_new * G <= kDecodeRows;
-    int64_t tiles, most;          // upper bounds: of the tiles that there can be, of the CTAs that pay
+    // upper bounds of the segments that there can be, and of a segment's tiles
+    int64_t segments, tiles;
     if (p.few) {
         p.rows = kDecodeRows;
-        const int64_t pages = k > 0 ? n_tok * k : std::min<int64_t>(n_tok, n_seq) * max_pages;
-        tiles = (pages * hkv * std::max(1, page / kDecodeTile) + kMinDecodeTiles - 1) / kMinDecodeTiles;
-        most = kSms;
+        segments = (k > 0 ? n_tok : std::min<int64_t>(n_tok, n_seq)) * hkv;
+        tiles = k > 0 ? (page == 16 ? ((int64_t)k + 1) / 2 : (int64_t)k * (page / kDecodeTile))
+                      : ((int64_t)max_pages * page + kDecodeTile - 1) / kDecodeTile;
     } else {
         p.rows = (int64_t)max_new * G <= 128 ? 128 : 256;
-        const int64_t blocks = ((int64_t)max_new * G + p.rows - 1) / p.rows * std::min<int64_t>(n_tok, n_seq);
-        tiles = blocks * hkv * (((int64_t)max_pages * page + kPromptTile - 1) / kPromptTile);
-        most = kSms;
+        segments = ((int64_t)max_new * G + p.rows - 1) / p.rows * std::min<int64_t>(n_tok, n_seq) * hkv;
+        tiles = ((int64_t)max_pages * page + kPromptTile - 1) / kPromptTile;
     }
-    p.grid = (int)std::max<int64_t>(1, std::min(most, tiles));
+    p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(kSms, segments * tiles));
+    // (the kernel decides by the lengths themselves; this is what it will find whatever those are)
+    p.uncut = p.few && segments <= p.grid && tiles <= kDecodeUncut && (k > 0 || n_seq <= kDecodeSeqs);
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t was = at;
@@ -157,7 +160,7 @@ extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_
         b.tok_off += first;
         if (p.few) MSA_RETURN_IF(launch_paged_decode(b, p.grid, s));
         else MSA_RETURN_IF(launch_paged_prompt(b, p.grid, s));
-        if (p.grid == 1) continue;
+        if (p.grid == 1 || p.uncut) continue;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

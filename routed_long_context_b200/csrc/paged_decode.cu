@@ -42,7 +42,8 @@ constexpr int kWarps = 10, kConsumers = 32 * kWarps, kThreads = kConsumers + 64;
 constexpr int kSlots = 2 * kWarps;                         // two of its own for each warp
 static_assert(kSlots <= 32, "a lane per slot");
 constexpr int kTileBytes = 2 * kDecodeTile * kPagedD;      // K and V of a tile
-constexpr int kWindow = kConsumers;                        // sequences looked at together
+constexpr int kWindow = kDecodeSeqs;                       // sequences looked at together
+static_assert(kWindow == kConsumers, "a thread per sequence");
 constexpr int kSegs = 2;                                   // segments whose queries are ready
 constexpr int kSegWeight = 8;                              // what starting and ending one costs, in tiles
 constexpr float kSlack = 24.f;
@@ -76,7 +77,8 @@ struct DecodeSmem {
     long long pre[kWindow + 1], pre_u[kWindow + 1];        // tiles before each sequence of the window, and units
     int64_t t0[kWindow], first[kWindow];
     int n_new[kWindow], len[kWindow];
-    long long scan[kWarps], scan_u[kWarps];
+    long long scan[kWarps];
+    int scan_live[kWarps], scan_most[kWarps];
     int abort_flag;
 };
 
@@ -151,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     // tiles per page, or two pages per tile
     const bool pairs = page == 16;
     const int per_page = pairs ? 1 : page / kDecodeTile;
+    const int list_tiles = !LIST ? 1 : pairs ? (a.k + 1) / 2 : a.k * per_page;
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
     // the combine pass may be launched: it waits for this grid's end before it reads
@@ -170,26 +173,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     }
 
     // Tiles of all sequences, a thread per sequence of the window; and units, in which the blocks' shares are measured: a
-    // segment's tiles and kSegWeight more, so that a block with many short segments gets fewer tiles.
+    // segment's tiles and kSegWeight more, so that a block with many short segments gets fewer tiles; or whole segments,
+    // where each gets a block.
     const int n_windows = LIST ? 1 : (v.n_seq + kWindow - 1) / kWindow;
     const bool at_hand = LIST && v.n_seq <= kWindow;       // the offsets and lengths of all sequences in shared memory
     struct Sums {
         long long tiles, units;
     };
+    bool uncut = LIST && list_tiles <= kDecodeUncut && a.n_tok * v.hkv <= (long long)gridDim.x;
     auto load_window = [&](int w) -> Sums {
         const int s = w * kWindow + tid;
         SeqSpan sp{0, 0, 0};
         if (tid < kWindow && s < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, blockIdx.x == 0 ? a.err : nullptr);
         const int per_head = sp.n_new ? (sp.len + kDecodeTile - 1) / kDecodeTile : 0;
-        long long up = (long long)v.hkv * per_head, up_u = per_head ? up + (long long)v.hkv * kSegWeight : 0;
+        long long up = (long long)v.hkv * per_head;
+        int live = per_head ? 1 : 0, most = per_head;      // sequences with something to do
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_up_sync(0xffffffffu, up_u, o);
+            const long long y = __shfl_up_sync(0xffffffffu, up, o);
+            const int z = __shfl_up_sync(0xffffffffu, live, o);
             if (lane >= o) {
                 up += y;
-                up_u += z;
+                live += z;
             }
         }
+        most = __reduce_max_sync(0xffffffffu, most);
         __syncthreads();
         if (tid < kWindow) {
             sm.t0[tid] = sp.t0;
@@ -198,32 +206,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             sm.len[tid] = sp.len;
             if (lane == 31) {
                 sm.scan[warp] = up;
-                sm.scan_u[warp] = up_u;
+                sm.scan_live[warp] = live;
+                sm.scan_most[warp] = most;
             }
         }
         __syncthreads();
-        long long before = 0, before_u = 0;
-        Sums all{0, 0};
+        long long before = 0, tiles = 0;
+        int before_live = 0, all_live = 0;
+        most = 0;
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-            const long long x = sm.scan[i], y = sm.scan_u[i];
+            const long long x = sm.scan[i];
+            const int y = sm.scan_live[i];
             if (i < warp) {
                 before += x;
-                before_u += y;
+                before_live += y;
             }
-            all.tiles += x;
-            all.units += y;
+            tiles += x;
+            all_live += y;
+            most = max(most, sm.scan_most[i]);
         }
+        if (!LIST) uncut = n_windows == 1 && most <= kDecodeUncut && (long long)all_live * v.hkv <= (long long)gridDim.x;
+        const long long per_seg = uncut ? 1 : kSegWeight;
         if (tid < kWindow) {
             sm.pre[tid + 1] = before + up;
-            sm.pre_u[tid + 1] = before_u + up_u;
+            sm.pre_u[tid + 1] = (uncut ? 0 : before + up) + (before_live + live) * per_seg * v.hkv;
         }
+        const Sums all{tiles, (uncut ? 0 : tiles) + all_live * per_seg * v.hkv};
         if (tid == 0) sm.pre[0] = sm.pre_u[0] = 0;
         __syncthreads();
         return all;
     };
     Sums total{0, 0}, first_total{0, 0};
-    const int list_tiles = !LIST ? 1 : pairs ? (a.k + 1) / 2 : a.k * per_page;
     if (LIST) {
         if (at_hand) load_window(0);
         else __syncthreads();
@@ -242,11 +256,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
         if (u >= sm.pre_u[n_win]) return sm.pre[n_win];
         const int lo = find(sm.pre_u, n_win, u);
         const int per_head = (sm.len[lo] + kDecodeTile - 1) / kDecodeTile;
+        if (uncut) return sm.pre[lo] + (u - sm.pre_u[lo]) * per_head;
         const int head = quotient(u - sm.pre_u[lo], per_head + kSegWeight);
         const int r = (int)(u - sm.pre_u[lo] - (long long)head * (per_head + kSegWeight));
         return sm.pre[lo] + (long long)head * per_head + min(r, per_head);
     };
-    const int n_cta = (int)min((long long)gridDim.x, total.tiles);
+    const int n_cta = (int)min((long long)gridDim.x, uncut ? total.units / (LIST ? list_tiles : 1) : total.tiles);
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
         return;
