@@ -366,18 +366,29 @@ class PagedKV:
         return ws
 
     def _check(self, who: str, tok_off, x, heads: int, *others) -> None:
-        """The kernels run on the current device and read plain memory of it: anything else is refused."""
+        """The kernels run on the current device and read plain, dense memory of it: anything else is refused."""
         dev = self._index
         if dev < 0 or dev != torch.cuda.current_device():
             raise ValueError(f"{who}: the cache is on {self.device}, not on the current CUDA device")
         for t in (tok_off, x, *others):
-            if t is not None and t.get_device() != dev:
-                raise ValueError(f"{who}: a tensor of shape {tuple(t.shape)} is on {t.device}, the cache on {self.device}")
+            if t is not None:
+                if t.get_device() != dev:
+                    raise ValueError(f"{who}: a tensor of shape {tuple(t.shape)} is on {t.device}, the cache on {self.device}")
+                if not t.is_contiguous():
+                    raise ValueError(f"{who}: tensor of shape {tuple(t.shape)} and strides {t.stride()} must be contiguous")
         if tok_off.dtype != torch.int64 or tok_off.shape != self._off_shape:
             raise ValueError(f"{who}: tok_off must be int64 [{self.n_seq + 1}], got {tok_off.dtype} of "
                              f"{tuple(tok_off.shape)}")
         if x.shape[1:] != (heads, self.d):
             raise ValueError(f"{who}: expected [n_tok, {heads}, {self.d}], got {tuple(x.shape)}")
+
+    def _stream(self, stream) -> int:
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
+
+
+def _addr(t) -> int | None:
+    """Address of a tensor that _check has looked at."""
+    return None if t is None else t.data_ptr()
 
 
 def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offset: int = 0, q=None, q_rot=None,
@@ -386,23 +397,28 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
     int64 [n_seq + 1] (device) splits the packed tokens, at most max_new a sequence; kv.seq_len already counts them.
     With q [n_tok, hq, d] the queries are rotated too: returns q_rot (allocated when not given), else None."""
     kv._check("msa_paged_append", tok_off, k, kv.hkv, v, cos_sin, q, q_rot)
-    _want("msa_paged_append", "v", v, k.dtype, k.shape)
+    n_tok = k.shape[0]
+    if v.dtype != k.dtype or v.shape != k.shape:
+        _want("msa_paged_append", "v", v, k.dtype, k.shape)
     if cos_sin.dtype != torch.float32 or cos_sin.shape[1:] != (kv.d // 2, 2):
         raise ValueError(f"msa_paged_append: cos_sin must be float32 [max_pos, {kv.d // 2}, 2]")
     hq = 0
     if q is not None:
         hq = q.shape[1]
-        _want("msa_paged_append", "q", q, k.dtype, (k.shape[0], hq, kv.d))
+        _want("msa_paged_append", "q", q, k.dtype, (n_tok, hq, kv.d))
         if q_rot is None:
             q_rot = torch.empty_like(q)
             if stream is not None:
                 q_rot.record_stream(stream)
         else:
             _want("msa_paged_append", "q_rot", q_rot, q.dtype, q.shape)
-    check(lib.msa_paged_append(kv._ref, _ptr(k), _ptr(v), _ptr(q), _dt(k), k.shape[0], hq, _ptr(tok_off), max_new,
-                               pos_offset, _ptr(cos_sin), cos_sin.shape[0], _ptr(q_rot) if q is not None else None,
-                               _stream(stream)), "msa_paged_append")
-    return q_rot if q is not None else None
+    else:
+        q_rot = None
+    st = lib.msa_paged_append(kv._ref, k.data_ptr(), v.data_ptr(), _addr(q), _dt(k), n_tok, hq, tok_off.data_ptr(), max_new,
+                              pos_offset, cos_sin.data_ptr(), cos_sin.shape[0], _addr(q_rot), kv._stream(stream))
+    if st:
+        check(st, "msa_paged_append")
+    return q_rot
 
 
 @functools.lru_cache(maxsize=256)
@@ -423,8 +439,10 @@ def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int =
         _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
         ws = kv._scratch(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages) or 256, stream, sel)
-    check(lib.msa_page_select(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, k, recent, _ptr(sel),
-                              _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "msa_page_select")
+    st = lib.msa_page_select(kv._ref, q.data_ptr(), _dt(q), n_tok, hq, tok_off.data_ptr(), max_new, k, recent, sel.data_ptr(),
+                             ws.data_ptr(), ws.nbytes, kv._stream(stream))
+    if st:
+        check(st, "msa_page_select")
     return sel
 
 
@@ -460,9 +478,10 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
         ws = kv._scratch(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k), stream,
                          out, lse)
     scale = 1.0 / math.sqrt(kv.d) if scale is None else scale
-    check(lib.msa_paged_attn(kv._ref, _ptr(q), _dt(q), n_tok, hq, _ptr(tok_off), max_new, _ptr(sel), k, scale,
-                             _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-          "msa_paged_attn")
+    st = lib.msa_paged_attn(kv._ref, q.data_ptr(), _dt(q), n_tok, hq, tok_off.data_ptr(), max_new, _addr(sel), k, scale,
+                            out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes, kv._stream(stream))
+    if st:
+        check(st, "msa_paged_attn")
     return out if lse is None else (out, lse)
 
 

@@ -789,6 +789,40 @@ def test_offsets_past_32_bits(m):
     assert m.device_status() == 0
 
 
+def test_the_binding_refuses_what_the_kernels_would_misread(m):
+    c = Cache(m, 91, [40, 40], 16, 2)
+    off_d, off = _offsets([2, 2])
+    q_d, _ = _queries(92, 4, 8)
+    cs = m.rope_table(64, D, BASE)
+    k = torch.zeros((4, 2, D), dtype=torch.bfloat16, device="cuda")
+    wide = torch.zeros((4, 16, D), dtype=torch.bfloat16, device="cuda")[:, ::2]
+    cases = [
+        lambda: m.msa_paged_attn(c.kv, wide, off_d, 2), lambda: m.msa_paged_attn(c.kv, q_d.cpu(), off_d, 2),
+        lambda: m.msa_paged_attn(c.kv, q_d, off_d.int(), 2), lambda: m.msa_paged_attn(c.kv, q_d, off_d[:2], 2),
+        lambda: m.msa_paged_attn(c.kv, q_d[:, :, :64].contiguous(), off_d, 2),
+        lambda: m.msa_paged_attn(c.kv, q_d, off_d, 2, out=torch.empty_like(q_d).float()),
+        lambda: m.msa_paged_attn(c.kv, q_d, off_d, 2, lse=torch.empty((4, 4), device="cuda")),
+        lambda: m.msa_paged_attn(c.kv, q_d, off_d, 2, sel=torch.zeros((4, 8, 3), dtype=torch.int32, device="cuda")),
+        lambda: m.msa_paged_attn(c.kv, q_d, off_d, 2, sel=torch.zeros((4, 2, 3), dtype=torch.int64, device="cuda")),
+        lambda: m.msa_page_select(c.kv, q_d, off_d, 2, 3, sel=torch.zeros((4, 2, 4), dtype=torch.int32, device="cuda")),
+        lambda: m.msa_paged_append(c.kv, k, k.float(), off_d, 2, cs),
+        lambda: m.msa_paged_append(c.kv, k, k, off_d, 2, cs.bfloat16()),
+        lambda: m.msa_paged_append(c.kv, k, k, off_d, 2, cs, q=q_d.float()),
+        lambda: m.msa_paged_append(c.kv, k, k, off_d, 2, cs, q=q_d, q_rot=q_d[:2]),
+        lambda: m.msa_paged_append(c.kv, torch.zeros((4, 4, D), dtype=torch.bfloat16, device="cuda")[:, ::2], k, off_d, 2, cs),
+    ]
+    before = c.kv.pages.view(torch.uint8).clone()
+    for call in cases:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(m.MSAError):
+        m.msa_paged_attn(c.kv, q_d, off_d, 2, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(m.MSAError):
+        m.msa_paged_attn(c.kv, q_d.float(), off_d, 2)
+    torch.cuda.synchronize()
+    assert m.device_status() == 0 and torch.equal(before, c.kv.pages.view(torch.uint8))
+
+
 def test_nothing_to_do(m):
     kv = m.PagedKV.empty(2, 2, 2, 2, 16)
     off = torch.zeros(3, dtype=torch.int64, device="cuda")
