@@ -493,9 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal
+                // s = 2^e with top <= 448 s; the range keeps s and 1 / s normal, and the logit factor at 2^-76 or more: times
+                // any scale of K it is not 0, which would make a NaN of a masked place (zero queries or softmax scales; what
+                // smaller queries lose moves no logit by 2^-20)
                 const uint32_t ub = __float_as_uint(top);
-                const int e = max(-100, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
+                const int e_min = max(-100, -76 - exponent_of(a.scale_log2e));
+                const int e = max(e_min, min(120, (int)(ub >> 23) - 127 - 8 + ((ub & 0x7FFFFFu) > 0x600000u ? 1 : 0)));
                 const float inv = a.scale_log2e < 0.f ? -pow2f(-e) : pow2f(-e);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                         ql[2 * i + j] = l0 | (l1 << 16);
                     }
                 }
-                const float f = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fabsf(a.scale_log2e) * pow2f(e);
+                const float f = ub >= 0x7F800000u ? __int_as_float(0x7FFFFFFF) : fmaxf(fabsf(a.scale_log2e) * pow2f(e), pow2f(-76));
                 const int at = n_seg % kSegs;
                 if (!__all_sync(0xffffffffu,
                                 mbar_wait(smem_u32(&sm.seg_empty[at]), ((uint32_t)(n_seg / kSegs) & 1u) ^ 1u, abort_flag)))

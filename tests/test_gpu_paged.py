@@ -383,6 +383,35 @@ def test_attention_over_the_smallest_values(m, new):
         _check_attn(c, [new], off, q, out, lse, 4, scale)
 
 
+@pytest.mark.parametrize("new", [1, 2, 40])
+@pytest.mark.parametrize("listed", [False, True])
+def test_attention_without_logits(m, new, listed):
+    """Queries and keys of zeros (at the smallest scale, as they are appended), and a softmax scale of zero: the mean of
+    the values that a row sees, whatever lies in the places that it does not see."""
+    sel = None
+    for lens in ([77], [1000]):
+        c = Cache(m, 45, lens, 16, 2)
+        off_d, off = _offsets([new])
+        q_d, q = _queries(46, new, 8)
+        if listed:
+            sel = torch.full((new, 2, 3), -1, dtype=torch.int32, device="cuda")
+            for i in range(new):
+                sel[i, :, 0], sel[i, :, 2] = 1, (lens[0] - new + i) // 16
+        sel_np = None if sel is None else sel.cpu().numpy()
+        out, lse = m.msa_paged_attn(c.kv, q_d, off_d, new, sel=sel, scale=0.0, want_lse=True)
+        assert m.device_status() == 0
+        _check_attn(c, [new], off, q, out, lse, 8, 0.0, sel=sel_np)
+        c.kv.pages[:, 0] = torch.zeros_like(c.kv.pages[:, 0])
+        c.kv.scales[:, 0] = 2.0 ** -50
+        c.vals[:, 0] = 0.0
+        c.scales[:, 0] = 2.0 ** -50
+        q_d.zero_()
+        q[:] = 0.0
+        out, lse = m.msa_paged_attn(c.kv, q_d, off_d, new, sel=sel, want_lse=True)
+        assert m.device_status() == 0
+        _check_attn(c, [new], off, q, out, lse, 8, 1 / math.sqrt(D), sel=sel_np)
+
+
 def test_a_list_of_the_callers_own(m):
     """Empty entries anywhere, a page named twice, one out of range, a row without any page."""
     c = Cache(m, 50, [500, 100], 32, 1)
