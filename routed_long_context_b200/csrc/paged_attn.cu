@@ -14,12 +14,13 @@
 namespace msa {
 namespace {
 
-// The combine pass, a programmatic dependent of the attention kernel: warp w of block (i, y) joins row 8 y + w of the
+// The combine pass: warp w of block (i, y) joins row 8 y + w of the
 // segment that starts in CTA i and goes on in later ones, in the CTAs' order, four columns a lane. Up to 32 pieces'
 // maxima and sums come at once, a lane each, and the pieces' rows four at a time: a handful of latencies in all.
 constexpr int kCombineRows = 8;
 __global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const PagedAttnArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    next_may_launch();
+    wait_for_earlier();
     const OpenSegment seg = a.open[blockIdx.x];
     const int n = blockIdx.y * kCombineRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (seg.n_more == 0 || n >= seg.rows) return;
@@ -161,16 +162,8 @@ extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_
         if (p.few) MSA_RETURN_IF(launch_paged_decode(b, p.grid, s));
         else MSA_RETURN_IF(launch_paged_prompt(b, p.grid, s));
         if (p.grid == 1 || p.uncut) continue;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.gridDim = dim3((unsigned)p.grid, (unsigned)((rows + kCombineRows - 1) / kCombineRows));
-        cfg.blockDim = dim3(32 * kCombineRows);
-        cfg.stream = s;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        MSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, paged_combine_kernel, b));
+        const dim3 grid((unsigned)p.grid, (unsigned)((rows + kCombineRows - 1) / kCombineRows));
+        MSA_CUDA_TRY(launch_early(paged_combine_kernel, grid, 32 * kCombineRows, 0, s, b));
     }
     return MSA_OK;
 }

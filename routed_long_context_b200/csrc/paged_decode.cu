@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     const int list_tiles = !LIST ? 1 : pairs ? (a.k + 1) / 2 : a.k * per_page;
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
-    // the combine pass may be launched: it waits for this grid's end before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    next_may_launch();
+    if (tid == 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm)) : "memory");
     if (tid == 0) sm.abort_flag = 0;
     if (tid == 0) mbar_init(smem_u32(&sm.joined), kWarps);
     if (tid < kSegs) {
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    wait_for_earlier();
 
     // Tiles of all sequences, a thread per sequence of the window; and units, in which the blocks' shares are measured: a
     // segment's tiles and kSegWeight more, so that a block with many short segments gets fewer tiles; or whole segments,
@@ -805,9 +806,8 @@ msa_status launch_paged_decode(const PagedAttnArgs& a, int grid, cudaStream_t s)
     const uint64_t strides[1] = {kPagedD};
     const uint32_t box[2] = {64, (uint32_t)std::min(a.v.page, kDecodeTile)};
     MSA_RETURN_IF(make_tensor_map_bf16(&tm, a.v.pages, 2, dims, strides, box));
-    if (a.sel) paged_decode_kernel<true><<<grid, kThreads, smem, s>>>(tm, a);
-    else paged_decode_kernel<false><<<grid, kThreads, smem, s>>>(tm, a);
-    MSA_LAUNCH_CHECK();
+    MSA_CUDA_TRY(launch_early(a.sel ? paged_decode_kernel<true> : paged_decode_kernel<false>, dim3((unsigned)grid), kThreads,
+                              smem, s, tm, a));
     return MSA_OK;
 }
 

@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     const int tpb = (SPLIT ? kRowsTile : 2 * kRowsTile) / G;       // tokens of a row block
     const float ninf = -INFINITY;
     volatile int* abort_flag = &sm.abort_flag;
-    // the combine pass may be launched: it waits for this grid's end before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    next_may_launch();
+    if (tid == 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm)) : "memory");
 
     if (tid == 0) {
         for (int i = 0; i < kKStages; ++i) mbar_init(smem_u32(&sm.k_full[i]), 1), mbar_init(smem_u32(&sm.k_empty[i]), 1);
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
 
+    wait_for_earlier();
     const bool alloc = warp == 1;
     if (alloc) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
@@ -863,8 +864,7 @@ msa_status launch(const CUtensorMap& tm, const PagedAttnArgs& a, int grid, cudaS
             if (dev >= 0 && dev < 64) opted[dev] = true;
         }
     }
-    paged_prompt_kernel<SPLIT><<<grid, kThreads, smem, s>>>(tm, a);
-    MSA_LAUNCH_CHECK();
+    MSA_CUDA_TRY(launch_early(paged_prompt_kernel<SPLIT>, dim3((unsigned)grid), kThreads, smem, s, tm, a));
     return MSA_OK;
 }
 

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) 
     const int s = blockIdx.x / a.chunks, chunk = blockIdx.x - s * a.chunks;
     const int g = blockIdx.y / a.token_parts, part = blockIdx.y - g * a.token_parts;
     const int G = a.G, gs = 31 - __clz(G), hq = v.hkv * G;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    next_may_launch();
     SeqSpan sp;
     if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) || sp.n_new == 0) return;
     const int n_pages = (sp.len + v.page - 1) >> v.shift;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     const int64_t t = blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.G, hq = v.hkv * G;
-    asm volatile("griddepcontrol.wait;" ::: "memory");     // of the scoring kernel, where there is one
+    wait_for_earlier();
     const int s = seq_of_token(a.tok_off, v.n_seq, t);
     SeqSpan sp;
     int32_t* sel = a.sel + (t * v.hkv + g) * a.k;
@@ -722,16 +722,6 @@ extern "C" msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa
             if (dev >= 0 && dev < 64) opted[dev] = true;
         }
     }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)n_tok, (unsigned)kv->hkv);
-    cfg.blockDim = dim3(kPickThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = scored ? 1 : 0;
-    MSA_CUDA_TRY(cudaLaunchKernelEx(&cfg, page_pick_kernel, a));
+    MSA_CUDA_TRY(launch_early(page_pick_kernel, dim3((unsigned)n_tok, (unsigned)kv->hkv), kPickThreads, smem, s, a));
     return MSA_OK;
 }

@@ -690,6 +690,60 @@ def test_a_captured_step_replays_on_new_lengths(m):
     assert m.device_status() == 0
 
 
+@pytest.mark.parametrize("new", [1, 30])
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_right_behind_what_they_depend_on(m, new, captured):
+    """Lengths, table, queries and values that a copy, a fill or another stream brings directly before the call, and the
+    same outputs and workspace used by call after call: no call may begin to read or write early."""
+    c = Cache(m, 85, [4000, 900], 16, 4)
+    off_d, off = _offsets([new, new])
+    hq, n_tok = 8, 2 * new
+    ws = torch.empty(m.paged_attn_workspace_size(n_tok, 2, new, hq, 4, c.kv.max_pages, 16), dtype=torch.uint8, device="cuda")
+    lens = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([4000, 900], [77, 850], [2222, 31])]
+    host = [x.cpu().pin_memory() for x in lens]
+    qs = [_queries(86 + i, n_tok, hq)[0] for i in range(3)]
+    q = torch.empty_like(qs[0])
+    outs = [torch.empty_like(q) for _ in range(6)]
+    out = torch.empty_like(q)
+    want = []
+    for i in range(3):
+        c.kv.seq_len.copy_(lens[i])
+        torch.cuda.synchronize()
+        want.append(m.msa_paged_attn(c.kv, qs[i], off_d, new))
+        torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    def steps():
+        for r in range(6):
+            i = r % 3
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                q.copy_(qs[i])                              # by another stream
+            if r % 2:
+                c.kv.seq_len.copy_(host[i], non_blocking=True)
+            else:
+                c.kv.seq_len.copy_(lens[i])
+            out.zero_()
+            torch.cuda.current_stream().wait_stream(side)
+            m.msa_paged_attn(c.kv, q, off_d, new, out=out, ws=ws)
+            m.msa_paged_attn(c.kv, q, off_d, new, out=out, ws=ws)
+            outs[r].copy_(out)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            steps()
+        run = graph.replay
+    else:
+        run = steps
+    for _ in range(5):
+        run()
+        torch.cuda.synchronize()
+        for r in range(6):
+            assert torch.equal(outs[r], want[r % 3]), r
+    assert m.device_status() == 0
+
+
 def test_a_stream_of_the_callers_own(m):
     """Calls on a stream that is not the current one, with scratch and results allocated by the call, while the current
     stream allocates and overwrites memory of the same sizes; two such streams at once."""
