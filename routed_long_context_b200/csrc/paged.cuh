@@ -155,12 +155,14 @@ __device__ __forceinline__ int cta_of_tile(int64_t total, int n, int64_t x) {
     return i;
 }
 
-// The few-rows kernel (paged_decode.cu) and the many-rows kernel (paged_prompt.cu).
+// The few-rows kernel (paged_decode.cu: blocks of 8 rows, tiles of 32 keys) and the many-rows kernel (paged_prompt.cu: 128
+// or 256 rows, 128 keys).
 constexpr int kDecodeRows = 8;
 constexpr int kDecodeTile = 32;
 // Few rows: where every segment can have a CTA of its own and none has more tiles than this, each has one (a segment that
 // is cut costs its pieces' start and merge and the combine pass). 48 tokens of 4 heads over 194: 12 -> 9 us.
 constexpr int kDecodeUncut = 32;
+constexpr int kSegWeight = 8;        // what starting and ending a segment costs, in tiles, in either kernel
 constexpr int kDecodeSeqs = 320;     // sequences that a CTA looks at together
 constexpr int kPromptTile = 128;
 constexpr int kPromptSeqs = 512;     // sequences per launch

@@ -2,8 +2,8 @@
 //
 //   out = softmax(scale q . K) V over the cached tokens that a query token sees: those at or before its own
 //   place in the sequence, and of these the listed pages where a list is given.
-// Up to 8 rows (token, query head) of a kv head at a time, and page lists, go to the few-rows kernel, which the
-// bytes bound; more rows to the tensor-core kernel, which the products bound. Both cut the keys of all sequences
+// Up to 8 rows (token, query head) of a kv head and sequence, page lists and small calls go to the few-rows kernel, which
+// the bytes bound; more rows to the tcgen05 kernel, which the products bound. Both cut the keys of all sequences
 // evenly over the SMs; the softmaxes that end up in several pieces are joined here.
 #include <algorithm>
 
@@ -72,18 +72,30 @@ struct AttnPlan {
 AttnPlan attn_plan(int64_t n_tok, int n_seq, int max_new, int hq, int hkv, int max_pages, int page, int k) {
     AttnPlan p{};
     const int G = hq / hkv;
-    p.few = k > 0 || (int64_t)max_new * G <= kDecodeRows;
+    const int64_t seqs = std::min<int64_t>(n_tok, n_seq), keys = (int64_t)max_pages * page;
     // upper bounds of the segments that there can be, and of a segment's tiles
-    int64_t segments, tiles;
-    if (p.few) {
-        p.rows = kDecodeRows;
-        segments = (k > 0 ? n_tok : std::min<int64_t>(n_tok, n_seq)) * hkv;
-        tiles = k > 0 ? (page == 16 ? ((int64_t)k + 1) / 2 : (int64_t)k * (page / kDecodeTile))
-                      : ((int64_t)max_pages * page + kDecodeTile - 1) / kDecodeTile;
-    } else {
-        p.rows = (int64_t)max_new * G <= 128 ? 128 : 256;
-        segments = ((int64_t)max_new * G + p.rows - 1) / p.rows * std::min<int64_t>(n_tok, n_seq) * hkv;
-        tiles = ((int64_t)max_pages * page + kPromptTile - 1) / kPromptTile;
+    const int64_t blocks = std::min<int64_t>(((int64_t)max_new * G + kDecodeRows - 1) / kDecodeRows * seqs,
+                                             n_tok * G / kDecodeRows + seqs);
+    int64_t segments = (k > 0 ? n_tok : blocks) * hkv;
+    int64_t tiles = k > 0 ? (page == 16 ? ((int64_t)k + 1) / 2 : (int64_t)k * (page / kDecodeTile))
+                          : (keys + kDecodeTile - 1) / kDecodeTile;
+    p.few = k > 0 || (int64_t)max_new * G <= kDecodeRows;
+    p.rows = kDecodeRows;
+    if (!p.few) {
+        // More rows take the many-rows kernel, or, where there is little to do, blocks of 8 in the few-rows kernel, which
+        // starts and ends sooner. Measured, with u the units (tiles and kSegWeight a segment) that a block gets and m the
+        // tiles of a segment, of which a block of the many-rows kernel takes 9 at least where there are so many:
+        // 7.5 + 0.3 u against 14.7 + 1.2 m us for 128 rows and 2.4 m for 256. One sequence of 64 tokens over 2,000 of 2
+        // kv heads 18.8 us (many rows 34.3), 22 of 8 heads over 242 15.1 (21.8), 4 of 9 over 33 7.4 (13.1); on the
+        // border 100 over 100 17.6 (17.5); beyond it 7 of up to 41 over up to 85 22.3 (20.0).
+        const int rows = (int64_t)max_new * G <= 128 ? 128 : 256;
+        const int64_t many = (keys + kPromptTile - 1) / kPromptTile;
+        p.few = segments * (tiles + kSegWeight) <= kSms * (24 + 4 * std::min<int64_t>(many, 9) * (rows / 128));
+        if (!p.few) {
+            p.rows = rows;
+            segments = ((int64_t)max_new * G + rows - 1) / rows * seqs * hkv;
+            tiles = many;
+        }
     }
     p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(kSms, segments * tiles));
     // (the kernel decides by the lengths themselves; this is what it will find whatever those are)

@@ -1,5 +1,5 @@
-// Attention of few query rows over a paged 8-bit cache: single tokens, a handful of drafted ones, and single
-// tokens over their page lists.
+// Attention of few query rows over a paged 8-bit cache: single tokens, a handful of drafted ones, single tokens over
+// their page lists, and more tokens in blocks of 8 rows where there is little to do.
 //
 //   out = softmax(scale q . K) V,  up to 8 rows (token, query head) of one kv head at a time.
 // Every cached byte is read once for 4 * 8 operations at most, so the bytes bound it, and what a warp spends on
@@ -11,8 +11,9 @@
 //   D   [128 x 8 rows]      = V^T [128 x 32] (Phi + Plo)^T,   O^T += D 2^(mt - m) scale(V)
 // Q is split into two e4m3 parts of a row scaled to 224..448: eight significant bits, all that bf16 has, down to
 // 2^-11 of the row's largest; what lies below is off by at most 2^-10 of the scale. P is taken against the
-// tile's own maximum mt, times 2^8, and split alike: an error of 2^-8 of the value (half a step twice, what one
-// rounding to bf16 costs), or of 2^-18 of the tile's largest for small ones. O and the sum are fp32 against a
+// tile's own maximum mt, times 2^8, and split into e4m3 and e5m2: an error of 2^-8 of the value (what one rounding
+// to bf16 costs: e4m3 leaves less than 2^-4, and e5m2 an eighth of half of that), or of 2^-22 of the tile's largest
+// for small ones, whose e4m3 part is a multiple of 2^-9 and leaves 2^-10 at most. O and the sum are fp32 against a
 // maximum m that moves only when a tile exceeds it by 2^24. The order of d and of the keys inside the products
 // is free: a thread takes the 16-byte pieces that it can read from shared memory without bank conflicts, and V
 // needs no more than 4 x 4 byte transposes.
@@ -45,7 +46,6 @@ constexpr int kTileBytes = 2 * kDecodeTile * kPagedD;      // K and V of a tile
 constexpr int kWindow = kDecodeSeqs;                       // sequences looked at together
 static_assert(kWindow == kConsumers, "a thread per sequence");
 constexpr int kSegs = 2;                                   // segments whose queries are ready
-constexpr int kSegWeight = 8;                              // what starting and ending one costs, in tiles
 constexpr float kSlack = 24.f;
 
 struct __align__(16) TileInfo {      // of the tile's two halves of 16 keys
@@ -98,6 +98,14 @@ __device__ __forceinline__ void mma_e4m3_16832_first(float* c, uint32_t a0, uint
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// the same, B in e5m2
+__device__ __forceinline__ void mma_e4m3_e5m2_16832(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                    uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e5m2.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -114,13 +122,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// x0, x1 as e4m3 pairs: the nearest, and the nearest to what that leaves (all within fp16's range)
+// x0, x1 as pairs of e4m3, the nearest, and of e4m3 or e5m2, the nearest to what that leaves (all within fp16's range)
+template <__nv_fp8_interpretation_t LO = __NV_E4M3>
 __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t* hi, uint32_t* lo) {
     const __half2 y = __floats2half2_rn(x0, x1);
     *hi = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
     const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)*hi, __NV_E4M3);
-    *lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__hsub2(y, *reinterpret_cast<const __half2*>(&back)), __NV_SATFINITE,
-                                               __NV_E4M3);
+    *lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__hsub2(y, *reinterpret_cast<const __half2*>(&back)), __NV_SATFINITE, LO);
 }
 
 // x / d; the short division where it will do
@@ -187,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
         SeqSpan sp{0, 0, 0};
         if (tid < kWindow && s < v.n_seq) seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, blockIdx.x == 0 ? a.err : nullptr);
         const int per_head = sp.n_new ? (sp.len + kDecodeTile - 1) / kDecodeTile : 0;
-        long long up = (long long)v.hkv * per_head;
-        int live = per_head ? 1 : 0, most = per_head;      // sequences with something to do
+        int live = (sp.n_new * G + kDecodeRows - 1) / kDecodeRows, most = per_head;    // row blocks
+        long long up = (long long)v.hkv * per_head * live;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, up, o);
@@ -251,6 +259,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             total.units += first_total.units;
         }
     }
+    // Segment i of sequence `lo` of the window: head i % hkv, row block i / hkv, which is that of a sequence that ends
+    // with the block's last token. (All segments of a sequence count as many tiles as the last block's; those behind a
+    // block's end are passed over.)
+    auto block_of = [&](int lo, int i, int* head, int64_t* t0, int* n_new, int* len) {
+        const int rb = i / v.hkv, before = rb * (kDecodeRows >> gs), all = sm.n_new[lo];
+        *head = i - rb * v.hkv;
+        *t0 = sm.t0[lo] + before;
+        *n_new = min(kDecodeRows >> gs, all - before);
+        *len = sm.len[lo] - all + before + *n_new;
+    };
     // tiles of the window before its unit u
     auto tiles_before = [&](long long u, int n_win) -> long long {
         if (LIST) return u;
@@ -340,11 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                     } else {
                         const int lo = find(sm.pre, n_win, g);
                         s = w * kWindow + lo;
-                        seen = sm.len[lo];
-                        const int per_head = (seen + kDecodeTile - 1) / kDecodeTile;
+                        const int per_head = (sm.len[lo] + kDecodeTile - 1) / kDecodeTile;
                         const long long in_seq = g - sm.pre[lo];
-                        head = quotient(in_seq, per_head);
-                        at = (int)(in_seq - (long long)head * per_head);
+                        const int nth = quotient(in_seq, per_head);
+                        at = (int)(in_seq - (long long)nth * per_head);
+                        int64_t t0;
+                        int n_new;
+                        block_of(lo, nth, &head, &t0, &n_new, &seen);
                     }
                     const int n_pages = (seen + page - 1) >> v.shift;
                     const int32_t* table = v.table + (int64_t)s * v.max_pages;
@@ -453,15 +473,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                     sg.n_new = live ? 1 : 0;
                 } else {
                     const int lo = find(sm.pre, n_win, g0);
-                    sg.t0 = sm.t0[lo];
-                    sg.n_new = sm.n_new[lo];
-                    sg.len = sm.len[lo];
-                    const int per_head = (sg.len + kDecodeTile - 1) / kDecodeTile;
-                    sg.head = quotient(g0 - sm.pre[lo], per_head);
-                    seg_a = sm.pre[lo] + (long long)sg.head * per_head;
+                    const int per_head = (sm.len[lo] + kDecodeTile - 1) / kDecodeTile;
+                    const int nth = quotient(g0 - sm.pre[lo], per_head);
+                    block_of(lo, nth, &sg.head, &sg.t0, &sg.n_new, &sg.len);
+                    seg_a = sm.pre[lo] + (long long)nth * per_head;
                     seg_b = seg_a + per_head;
                     if (seg_a == g0 && seg_b > B) {        // it goes on in other blocks: what the combine pass needs to know
-                        const long long u = base + sm.pre_u[lo] + (long long)sg.head * (per_head + kSegWeight) + per_head - 1;
+                        const long long u = base + sm.pre_u[lo] + (long long)nth * (per_head + kSegWeight) + per_head - 1;
                         open = OpenSegment{sg.t0, sg.head, sg.n_new * G, cta_of_tile(total.units, n_cta, u) - (int)blockIdx.x, 1.f};
                     }
                 }
@@ -666,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                                 ta += p0 + p2;
                                 tb += p1 + p3;
                                 uint32_t ha, la, hb, lb;
-                                split_e4m3(p0 * fac[h], p2 * fac[h], &ha, &la);
-                                split_e4m3(p1 * fac[h], p3 * fac[h], &hb, &lb);
+                                split_e4m3<__NV_E5M2>(p0 * fac[h], p2 * fac[h], &ha, &la);
+                                split_e4m3<__NV_E5M2>(p1 * fac[h], p3 * fac[h], &hb, &lb);
                                 bh[h] = transpose8x8(__byte_perm(ha, hb, 0x5410));
                                 bl[h] = transpose8x8(__byte_perm(la, lb, 0x5410));
                             }
@@ -701,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
                                 for (int z = 0; z < 2; ++z) {
                                     float d[4];
                                     mma_e4m3_16832_first(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bh[0], bh[1]);
-                                    mma_e4m3_16832(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bl[0], bl[1]);
+                                    mma_e4m3_e5m2_16832(d, f[0][2 * z], f[0][2 * z + 1], f[1][2 * z], f[1][2 * z + 1], bl[0], bl[1]);
                                     float* oo = o[2 * i + z];
                                     oo[0] = fmaf(d[0], wa, oo[0]);
                                     oo[1] = fmaf(d[1], wb, oo[1]);

@@ -44,7 +44,6 @@ constexpr int kRowsTile = 128;                             // MMA M
 constexpr int kKStages = 3, kVStages = 2, kV16Stages = 2, kInfo = 8;
 constexpr int kWin = kPromptSeqs;                          // sequences of a launch, a thread each
 static_assert(kWin == kThreads, "a thread per sequence");
-constexpr int kSegWeight = 8;                              // what starting and ending a segment costs, in tiles
 constexpr float kTrigger = 32768.f;                        // a tile's sum above it moves the reference maximum
 constexpr float kSlack = 8.f;                              // log2 of how far logits may lie above the reference
 

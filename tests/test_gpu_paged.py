@@ -224,6 +224,25 @@ def test_attention_of_many_sequences(m, new):
     _check_attn(c, news, off, q, out, lse, 2, 1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("lens,news,page,hkv,G", [
+    ([33, 9, 20, 31], [9, 9, 1, 3], 128, 2, 4),            # every row block has a block of its own
+    ([100], [100], 16, 2, 8),                              # a token a row block
+    ([1311, 600], [142, 9], 64, 2, 1),                     # eight tokens a row block, cut over the blocks
+    ([2000], [64], 32, 2, 4),
+    ([345] * 20 + [17, 0], [4] * 20 + [3, 0], 16, 2, 4),
+])
+def test_attention_of_many_rows_in_small_calls(m, lens, news, page, hkv, G):
+    c = Cache(m, 47, lens, page, hkv)
+    off_d, off = _offsets(news)
+    hq = hkv * G
+    q_d, q = _queries(48, off[-1], hq)
+    out, lse = m.msa_paged_attn(c.kv, q_d, off_d, max(news), want_lse=True)
+    assert m.device_status() == 0
+    _check_attn(c, news, off, q, out, lse, hq, 1 / math.sqrt(D))
+    again, lse2 = m.msa_paged_attn(c.kv, q_d, off_d, max(news), want_lse=True)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("new", [1, 24])
 def test_attention_far_scales_and_sharp_logits(m, new):
     """Scales of neighbouring pages 2^40 apart, a softmax that one key takes, and a negative scale."""
@@ -688,6 +707,38 @@ def test_a_captured_step_replays_on_new_lengths(m):
         ids = a.page_table[0, :n_p].long()
         assert torch.equal(a.scales[ids], b.scales[ids]) and torch.equal(a.bounds[ids], b.bounds[ids])
     assert m.device_status() == 0
+
+
+class Roomy(Cache):
+    """With room for long contexts, which is what the choice of the kernel goes by."""
+
+    def __init__(self, m, seed, lens, page, hkv, max_pages=None, **kw):
+        super().__init__(m, seed, lens, page, hkv, max_pages=1 << 13, **kw)
+
+
+@pytest.mark.parametrize("name,args", [("test_attention", x) for x in ATTN if max(x[1]) * x[4] > 8] + [
+    ("test_attention_leaves_rows_outside_the_sequences", ([3, 1, 40],)),
+    ("test_attention_ignores_what_lies_behind_the_end", (16, 20)),
+    ("test_attention_ignores_what_lies_behind_the_end", (128, 20)),
+    ("test_attention_far_scales_and_sharp_logits", (24,)),
+    ("test_a_sink_key_does_not_swallow_a_long_tail", ()),
+    ("test_attention_skips_bad_sequences_and_pages", (33,)),
+    ("test_attention_over_the_smallest_values", (40,)),
+    ("test_attention_without_logits", (40, False)),
+    ("test_calls_right_behind_what_they_depend_on", (30, False)),
+    ("test_a_query_that_is_not_finite_spoils_its_own_row_only", (30, math.nan)),
+    ("test_a_query_that_is_not_finite_spoils_its_own_row_only", (30, math.inf)),
+    ("test_attention_records_more_tokens_than_it_was_told", ()),
+    ("test_nothing_is_written_beside_the_outputs", (30, 16, 4)),
+    ("test_nothing_is_written_beside_the_outputs", (70, 128, 4)),
+])
+def test_small_calls_with_room_for_long_contexts(m, monkeypatch, name, args):
+    """The same calls where the table has room for long contexts: those of more than 8 rows go another way."""
+    import inspect
+
+    f = globals()[name]
+    monkeypatch.setitem(globals(), "Cache", Roomy)
+    f(**dict(zip(inspect.signature(f).parameters, (m, *args))))
 
 
 @pytest.mark.parametrize("new", [1, 30])
