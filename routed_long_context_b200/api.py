@@ -366,21 +366,22 @@ class PagedKV:
         return ws
 
     def _check(self, who: str, tok_off, x, heads: int, *others) -> None:
-        """The kernels run on the current device and read plain, dense memory of it: anything else is refused."""
+        """The kernels run on the current device and read plain, dense memory of it: anything else is refused. (Every call
+        comes through here: a small one takes the GPU as long as the host.)"""
         dev = self._index
-        if dev < 0 or dev != torch.cuda.current_device():
+        if dev < 0 or dev != torch._C._cuda_getDevice():
             raise ValueError(f"{who}: the cache is on {self.device}, not on the current CUDA device")
         for t in (tok_off, x, *others):
-            if t is not None:
+            if t is not None and (t.get_device() != dev or not t.is_contiguous()):
                 if t.get_device() != dev:
                     raise ValueError(f"{who}: a tensor of shape {tuple(t.shape)} is on {t.device}, the cache on {self.device}")
-                if not t.is_contiguous():
-                    raise ValueError(f"{who}: tensor of shape {tuple(t.shape)} and strides {t.stride()} must be contiguous")
+                raise ValueError(f"{who}: tensor of shape {tuple(t.shape)} and strides {t.stride()} must be contiguous")
         if tok_off.dtype != torch.int64 or tok_off.shape != self._off_shape:
             raise ValueError(f"{who}: tok_off must be int64 [{self.n_seq + 1}], got {tok_off.dtype} of "
                              f"{tuple(tok_off.shape)}")
-        if x.shape[1:] != (heads, self.d):
-            raise ValueError(f"{who}: expected [n_tok, {heads}, {self.d}], got {tuple(x.shape)}")
+        shape = x.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != self.d:
+            raise ValueError(f"{who}: expected [n_tok, {heads}, {self.d}], got {tuple(shape)}")
 
     def _stream(self, stream) -> int:
         return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
@@ -397,25 +398,28 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
     int64 [n_seq + 1] (device) splits the packed tokens, at most max_new a sequence; kv.seq_len already counts them.
     With q [n_tok, hq, d] the queries are rotated too: returns q_rot (allocated when not given), else None."""
     kv._check("msa_paged_append", tok_off, k, kv.hkv, v, cos_sin, q, q_rot)
-    n_tok = k.shape[0]
-    if v.dtype != k.dtype or v.shape != k.shape:
-        _want("msa_paged_append", "v", v, k.dtype, k.shape)
-    if cos_sin.dtype != torch.float32 or cos_sin.shape[1:] != (kv.d // 2, 2):
+    shape, dtype = k.shape, k.dtype
+    if v.dtype != dtype or v.shape != shape:
+        _want("msa_paged_append", "v", v, dtype, shape)
+    n_tok, angles = shape[0], cos_sin.shape
+    if cos_sin.dtype != torch.float32 or len(angles) != 3 or angles[1:] != (kv.d // 2, 2):
         raise ValueError(f"msa_paged_append: cos_sin must be float32 [max_pos, {kv.d // 2}, 2]")
     hq = 0
     if q is not None:
-        hq = q.shape[1]
-        _want("msa_paged_append", "q", q, k.dtype, (n_tok, hq, kv.d))
+        shape = q.shape
+        if q.dtype != dtype or len(shape) != 3 or shape[0] != n_tok or shape[2] != kv.d:
+            raise ValueError(f"msa_paged_append: q must be {dtype} [{n_tok}, hq, {kv.d}], got {q.dtype} of {tuple(shape)}")
+        hq = shape[1]
         if q_rot is None:
             q_rot = torch.empty_like(q)
             if stream is not None:
                 q_rot.record_stream(stream)
-        else:
-            _want("msa_paged_append", "q_rot", q_rot, q.dtype, q.shape)
+        elif q_rot.dtype != dtype or q_rot.shape != shape:
+            _want("msa_paged_append", "q_rot", q_rot, dtype, shape)
     else:
         q_rot = None
     st = lib.msa_paged_append(kv._ref, k.data_ptr(), v.data_ptr(), _addr(q), _dt(k), n_tok, hq, tok_off.data_ptr(), max_new,
-                              pos_offset, cos_sin.data_ptr(), cos_sin.shape[0], _addr(q_rot), kv._stream(stream))
+                              pos_offset, cos_sin.data_ptr(), angles[0], _addr(q_rot), kv._stream(stream))
     if st:
         check(st, "msa_paged_append")
     return q_rot

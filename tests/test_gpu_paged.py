@@ -957,6 +957,23 @@ def test_the_binding_refuses_what_the_kernels_would_misread(m):
     assert m.device_status() == 0 and torch.equal(before, c.kv.pages.view(torch.uint8))
 
 
+def test_the_binding_refuses_other_numbers_of_dimensions(m):
+    c = Cache(m, 93, [40], 16, 2)
+    off_d, _ = _offsets([2])
+    cs = m.rope_table(64, D, BASE)
+    k = torch.zeros((2, 2, D), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((2, 4, D), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: m.msa_paged_append(c.kv, k[..., None], k[..., None], off_d, 2, cs),
+                 lambda: m.msa_paged_append(c.kv, k.view(-1), k.view(-1), off_d, 2, cs),
+                 lambda: m.msa_paged_append(c.kv, k, k, off_d, 2, cs.view(-1)),
+                 lambda: m.msa_paged_append(c.kv, k, k, off_d, 2, cs, q=q.view(-1)),
+                 lambda: m.msa_paged_append(c.kv, k, k, off_d, 2, cs, q=q[:1]),
+                 lambda: m.msa_paged_attn(c.kv, q.view(2, -1), off_d, 2),
+                 lambda: m.msa_page_select(c.kv, q[..., None], off_d, 2, 3)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_nothing_to_do(m):
     kv = m.PagedKV.empty(2, 2, 2, 2, 16)
     off = torch.zeros(3, dtype=torch.int64, device="cuda")
