@@ -18,11 +18,12 @@
 // The products cost 8 * 128^3 flops a tile and row block, 1,024 cycles at the tensor peak; 128 * 128 exponentials take
 // as long on the special-function units: both bound it. Measured, a tile of both row blocks takes 4,200 cycles: a
 // warpgroup's exponentials and their reading and writing of TMEM 2,100, its products 1,300 (shared memory feeds Q K^T no
-// faster), and what passes between them. 2,000 tokens of 32 heads over 18,000: 606 us, 918 TFLOP/s. Not faster: an issuer
+// faster), and what passes between them. 2,000 tokens of 32 heads over 18,000: 604 to 621 us on two
+// GPUs, 897 to 922 TFLOP/s. Not faster: an issuer
 // of products for each warpgroup (764 us; in strict turns 655), steps of 64 keys with S ahead (738), part of the
 // exponentials by arithmetic (641 and more), waits by one lane of a warp (741).
 // With few tiles to a block, what starts and ends a segment is most of it: 8 sequences of up to 32 tokens over up to
-// 8,096 take 44 us, 57 where a segment's cost is left out of the blocks' shares.
+// 8,096 take 42 us; 57 before the launches overlapped and where a segment's cost is left out of the blocks' shares.
 //
 // Roles of the 512 threads: warp 0 loads pages by TMA (128-byte swizzle, K three tiles deep, V two), warp 1 issues the
 // products, warps 4..11 run the softmax, warps 12..15 convert V. Every wait is bounded; when one runs out the block
