@@ -435,10 +435,10 @@ def page_select_workspace_size(n_tok: int, hkv: int, max_pages: int) -> int:
 def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int = 1, sel=None, ws=None, stream=None):
     """The k pages that each new token's query heads q [n_tok, hq, d] (rotated) should attend over, by the bounds of
     the pages' keys -> sel int32 [n_tok, hkv, k], ascending page indices of the sequence, -1 where there are fewer."""
-    n_tok, hq = q.shape[:2]
+    n_tok, hq, _ = q.shape
     kv._check("msa_page_select", tok_off, q, hq, sel, ws)
     if sel is None:
-        sel = kv.seq_len.new_empty((n_tok, kv.hkv, k))
+        sel = kv.seq_len.new_empty(n_tok, kv.hkv, k)
     else:
         _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
@@ -464,7 +464,7 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     """Attention of the new tokens q [n_tok, hq, d] (bf16, rotated) over the cache, causal within the call; with sel
     int32 [n_tok, hkv, k] over the listed pages only. Returns out [n_tok, hq, d], with lse float32 [n_tok, hq]
     (given or wanted) the pair (out, lse)."""
-    n_tok, hq = q.shape[:2]
+    n_tok, hq, d = q.shape
     kv._check("msa_paged_attn", tok_off, q, hq, out, lse, sel, ws)
     if out is None:
         out = torch.empty_like(q)
@@ -473,7 +473,7 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     if lse is not None:
         _want("msa_paged_attn", "lse", lse, torch.float32, (n_tok, hq))
     elif want_lse:
-        lse = kv.scales.new_empty((n_tok, hq))
+        lse = kv.scales.new_empty(n_tok, hq)
     k = 0
     if sel is not None:
         k = sel.shape[-1]
@@ -481,7 +481,8 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     if ws is None:
         ws = kv._scratch(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k), stream,
                          out, lse)
-    scale = 1.0 / math.sqrt(kv.d) if scale is None else scale
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
     st = lib.msa_paged_attn(kv._ref, q.data_ptr(), _dt(q), n_tok, hq, tok_off.data_ptr(), max_new, _addr(sel), k, scale,
                             out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes, kv._stream(stream))
     if st:

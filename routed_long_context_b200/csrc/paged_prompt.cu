@@ -23,7 +23,7 @@
 // of products for each warpgroup (764 us; in strict turns 655), steps of 64 keys with S ahead (738), part of the
 // exponentials by arithmetic (641 and more), waits by one lane of a warp (741).
 // With few tiles to a block, what starts and ends a segment is most of it: 8 sequences of up to 32 tokens over up to
-// 8,096 take 42 us; 57 before the launches overlapped and where a segment's cost is left out of the blocks' shares.
+// 8,096 take 42 us (before launches overlapped 45, and 57 where a segment's cost is left out of the blocks' shares).
 //
 // Roles of the 512 threads: warp 0 loads pages by TMA (128-byte swizzle, K three tiles deep, V two), warp 1 issues the
 // products, warps 4..11 run the softmax, warps 12..15 convert V. Every wait is bounded; when one runs out the block
