@@ -58,7 +58,7 @@ enum { MSA_F32 = 0, MSA_BF16 = 1 };
 enum {
     MSA_DEV_OK = 0,
     MSA_DEV_ROPE_POSITION = 1, /* a RoPE position was >= max_pos; that row was not rotated/pooled */
-    MSA_DEV_WAIT_TIMEOUT = 2,  /* an mbarrier wait in the tensor-core router ran out of time */
+    MSA_DEV_WAIT_TIMEOUT = 2,  /* an mbarrier wait inside a kernel ran out of time */
     MSA_DEV_BAD_INDEX = 3,     /* a doc or page index, an offset or a length out of range reached a kernel */
     MSA_DEV_NONFINITE = 4      /* a NaN or infinite value was appended to an 8-bit cache */
 };
