@@ -41,6 +41,22 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _on_stream(stream, call, *args, **kw):
+    """`call` with `stream` as the current one, so that what it allocates or fills belongs to that stream: a block from
+    another stream's memory may still be in use by what is queued there. Results stay reserved until the stream that was
+    current, where the caller takes them, is done with them too."""
+    was = torch.cuda.current_stream()
+    if stream.device != was.device:
+        raise ValueError(f"{call.__name__}: the stream is on {stream.device}, the current device is {was.device}")
+    with torch.cuda.stream(stream):
+        got = call(*args, **kw)
+    given = (*args, *kw.values())
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None and t.is_cuda and not any(t is x for x in given):
+            t.record_stream(was)
+    return got
+
+
 def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
@@ -323,7 +339,8 @@ class PagedKV:
 
     pages float8_e4m3fn [n_pages, 2, hkv, page, d], scales float32 [n_pages, 2, hkv], page_table int32 [n_seq,
     max_pages], seq_len int32 [n_seq] (the tokens of a call included), bounds bfloat16 [n_pages, hkv, 2, d] or None.
-    The tensors stay where they are: page_table and seq_len are refilled in place as sequences grow."""
+    The tensors stay where they are: page_table and seq_len are refilled in place as sequences grow. A call with a
+    `stream` of its own needs its inputs ready on that stream, and what it returns is ready there."""
 
     def __init__(self, pages, scales, page_table, seq_len, bounds=None):
         n_pages, two, hkv, page, d = pages.shape
@@ -355,16 +372,6 @@ class PagedKV:
                    torch.zeros(n_seq, dtype=torch.int32, device=device),
                    torch.zeros((n_pages, hkv, 2, d), dtype=torch.bfloat16, device=device) if bounds else None)
 
-    def _scratch(self, nbytes: int, stream, *results) -> torch.Tensor:
-        """A workspace; it and the results allocated with it stay reserved until the stream that uses them, where that is
-        not the current one, is done."""
-        ws = self._u8.new_empty(nbytes)
-        if stream is not None:
-            for t in (ws, *results):
-                if t is not None:
-                    t.record_stream(stream)
-        return ws
-
     def _check(self, who: str, tok_off, x, heads: int, *others) -> None:
         """The kernels run on the current device and read plain, dense memory of it: anything else is refused. (Every call
         comes through here: a small one takes the GPU as long as the host.)"""
@@ -383,8 +390,8 @@ class PagedKV:
         if len(shape) != 3 or shape[1] != heads or shape[2] != self.d:
             raise ValueError(f"{who}: expected [n_tok, {heads}, {self.d}], got {tuple(shape)}")
 
-    def _stream(self, stream) -> int:
-        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
+    def _stream(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
 
 def _addr(t) -> int | None:
@@ -397,6 +404,8 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
     """Append k, v [n_tok, hkv, d] to the cache, keys rotated to pos_offset + their place in the sequence; tok_off
     int64 [n_seq + 1] (device) splits the packed tokens, at most max_new a sequence; kv.seq_len already counts them.
     With q [n_tok, hq, d] the queries are rotated too: returns q_rot (allocated when not given), else None."""
+    if stream is not None:
+        return _on_stream(stream, msa_paged_append, kv, k, v, tok_off, max_new, cos_sin, pos_offset, q, q_rot)
     kv._check("msa_paged_append", tok_off, k, kv.hkv, v, cos_sin, q, q_rot)
     shape, dtype = k.shape, k.dtype
     if v.dtype != dtype or v.shape != shape:
@@ -412,14 +421,12 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
         hq = shape[1]
         if q_rot is None:
             q_rot = torch.empty_like(q)
-            if stream is not None:
-                q_rot.record_stream(stream)
         elif q_rot.dtype != dtype or q_rot.shape != shape:
             _want("msa_paged_append", "q_rot", q_rot, dtype, shape)
     else:
         q_rot = None
     st = lib.msa_paged_append(kv._ref, k.data_ptr(), v.data_ptr(), _addr(q), _dt(k), n_tok, hq, tok_off.data_ptr(), max_new,
-                              pos_offset, cos_sin.data_ptr(), angles[0], _addr(q_rot), kv._stream(stream))
+                              pos_offset, cos_sin.data_ptr(), angles[0], _addr(q_rot), kv._stream())
     if st:
         check(st, "msa_paged_append")
     return q_rot
@@ -435,6 +442,8 @@ def page_select_workspace_size(n_tok: int, hkv: int, max_pages: int) -> int:
 def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int = 1, sel=None, ws=None, stream=None):
     """The k pages that each new token's query heads q [n_tok, hq, d] (rotated) should attend over, by the bounds of
     the pages' keys -> sel int32 [n_tok, hkv, k], ascending page indices of the sequence, -1 where there are fewer."""
+    if stream is not None:
+        return _on_stream(stream, msa_page_select, kv, q, tok_off, max_new, k, recent, sel, ws)
     n_tok, hq, _ = q.shape
     kv._check("msa_page_select", tok_off, q, hq, sel, ws)
     if sel is None:
@@ -442,9 +451,9 @@ def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int =
     else:
         _want("msa_page_select", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
-        ws = kv._scratch(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages) or 256, stream, sel)
+        ws = kv._u8.new_empty(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages) or 256)
     st = lib.msa_page_select(kv._ref, q.data_ptr(), _dt(q), n_tok, hq, tok_off.data_ptr(), max_new, k, recent, sel.data_ptr(),
-                             ws.data_ptr(), ws.nbytes, kv._stream(stream))
+                             ws.data_ptr(), ws.nbytes, kv._stream())
     if st:
         check(st, "msa_page_select")
     return sel
@@ -464,6 +473,8 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     """Attention of the new tokens q [n_tok, hq, d] (bf16, rotated) over the cache, causal within the call; with sel
     int32 [n_tok, hkv, k] over the listed pages only. Returns out [n_tok, hq, d], with lse float32 [n_tok, hq]
     (given or wanted) the pair (out, lse)."""
+    if stream is not None:
+        return _on_stream(stream, msa_paged_attn, kv, q, tok_off, max_new, sel, scale, out, lse, want_lse, ws)
     n_tok, hq, d = q.shape
     kv._check("msa_paged_attn", tok_off, q, hq, out, lse, sel, ws)
     if out is None:
@@ -479,12 +490,11 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
         k = sel.shape[-1]
         _want("msa_paged_attn", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
-        ws = kv._scratch(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k), stream,
-                         out, lse)
+        ws = kv._u8.new_empty(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     st = lib.msa_paged_attn(kv._ref, q.data_ptr(), _dt(q), n_tok, hq, tok_off.data_ptr(), max_new, _addr(sel), k, scale,
-                            out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes, kv._stream(stream))
+                            out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes, kv._stream())
     if st:
         check(st, "msa_paged_attn")
     return out if lse is None else (out, lse)

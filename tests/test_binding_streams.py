@@ -1,0 +1,121 @@
+"""What the binding allocates for a call on a stream of the caller's own. No GPU is needed: streams and the library
+are stood in for, and the allocations are watched as torch makes them."""
+import contextlib
+
+import pytest
+import torch
+from torch.utils._python_dispatch import TorchDispatchMode
+
+import routed_long_context_b200 as m
+from routed_long_context_b200 import api
+
+D = 128
+ALLOCATIONS = ("empty", "new_empty", "empty_like", "zeros", "new_zeros", "zeros_like", "fill_", "zero_", "full")
+
+
+class Stream:
+    def __init__(self, cuda_stream, index=0):
+        self.cuda_stream = cuda_stream
+        self.device = torch.device("cuda", index)
+
+
+class Watch(TorchDispatchMode):
+    """Where each allocation or fill happened: the current stream of that moment."""
+
+    def __init__(self, world):
+        super().__init__()
+        self.world, self.seen = world, []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        name = func.overloadpacket.__name__
+        if name in ALLOCATIONS:
+            self.seen.append((name, self.world.current))
+        return func(*args, **(kwargs or {}))
+
+
+class World:
+    """Streams as torch would show them, and the records of what is kept for which."""
+
+    def __init__(self, monkeypatch):
+        self.usual, self.side = Stream(7), Stream(9)
+        self.current, self.kept, self.launched = self.usual, [], []
+
+        @contextlib.contextmanager
+        def on(stream):
+            was, self.current = self.current, stream
+            yield
+            self.current = was
+
+        monkeypatch.setattr(torch.cuda, "stream", on)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.current)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: self.current.cuda_stream)
+        monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: self.kept.append((t, s)))
+        monkeypatch.setattr(torch.Tensor, "is_cuda", True, raising=False)
+
+    def stub(self, monkeypatch, name):
+        monkeypatch.setattr(api.lib, name, lambda *a: self.launched.append((name, a)) or 0)
+
+    def kept_for(self, t):
+        return [s for x, s in self.kept if x is t]
+
+
+@pytest.fixture
+def world(monkeypatch):
+    return World(monkeypatch)
+
+
+def _cache(monkeypatch):
+    kv = m.PagedKV(torch.empty((3, 2, 2, 16, D), dtype=torch.float8_e4m3fn), torch.ones((3, 2, 2)),
+                   torch.zeros((1, 3), dtype=torch.int32), torch.zeros(1, dtype=torch.int32),
+                   torch.zeros((3, 2, 2, D), dtype=torch.bfloat16))
+    monkeypatch.setattr(m.PagedKV, "_check", lambda *a: None)
+    return kv
+
+
+def _paged_calls(kv):
+    q, off = torch.zeros((2, 4, D), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    k, cs = torch.zeros((2, 2, D), dtype=torch.bfloat16), torch.zeros((4, D // 2, 2))
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    return {
+        "append": ("msa_paged_append", lambda **s: m.msa_paged_append(kv, k, k, off, 2, cs, q=q, **s)),
+        "select": ("msa_page_select", lambda **s: m.msa_page_select(kv, q, off, 2, 3, **s)),
+        "select, scratch given": ("msa_page_select", lambda **s: m.msa_page_select(kv, q, off, 2, 3, ws=ws, **s)),
+        "attend": ("msa_paged_attn", lambda **s: m.msa_paged_attn(kv, q, off, 2, want_lse=True, **s)),
+        "attend, scratch given": ("msa_paged_attn", lambda **s: m.msa_paged_attn(kv, q, off, 2, want_lse=True, ws=ws, **s)),
+    }
+
+
+@pytest.mark.parametrize("which", ["append", "select", "select, scratch given", "attend", "attend, scratch given"])
+def test_what_a_paged_call_allocates_belongs_to_its_stream(monkeypatch, world, which):
+    """Memory of the current stream may still be in use by what is queued there: results and scratch come from the
+    call's own stream, and the results are kept until the current stream is done with them."""
+    kv = _cache(monkeypatch)
+    name, call = _paged_calls(kv)[which]
+    world.stub(monkeypatch, name)
+    with Watch(world) as w:
+        got = call(stream=world.side)
+    assert w.seen and all(s is world.side for _, s in w.seen), w.seen
+    assert [a[-1] for _, a in world.launched] == [world.side.cuda_stream] and world.current is world.usual
+    for t in got if isinstance(got, tuple) else (got,):
+        assert world.usual in world.kept_for(t)
+
+
+@pytest.mark.parametrize("which", ["append", "select", "attend"])
+def test_a_paged_call_without_a_stream_stays_on_the_current_one(monkeypatch, world, which):
+    kv = _cache(monkeypatch)
+    name, call = _paged_calls(kv)[which]
+    world.stub(monkeypatch, name)
+    with Watch(world) as w:
+        call()
+    assert all(s is world.usual for _, s in w.seen) and not world.kept
+    assert world.launched[0][1][-1] == world.usual.cuda_stream
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch, world):
+    kv = _cache(monkeypatch)
+    for name, call in _paged_calls(kv).values():
+        world.stub(monkeypatch, name)
+        with pytest.raises(ValueError, match="device"):
+            call(stream=Stream(11, index=1))
+    assert not world.launched
