@@ -45,6 +45,8 @@ def _on_stream(stream, call, *args, **kw):
     """`call` with `stream` as the current one, so that what it allocates or fills belongs to that stream: a block from
     another stream's memory may still be in use by what is queued there. Results stay reserved until the stream that was
     current, where the caller takes them, is done with them too."""
+    if not hasattr(stream, "device"):            # anything else that has a cuda_stream
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
     was = torch.cuda.current_stream()
     if stream.device != was.device:
         raise ValueError(f"{call.__name__}: the stream is on {stream.device}, the current device is {was.device}")
@@ -55,6 +57,21 @@ def _on_stream(stream, call, *args, **kw):
         if t is not None and t.is_cuda and not any(t is x for x in given):
             t.record_stream(was)
     return got
+
+
+def _allocates(f):
+    """An entry point that allocates or fills memory: given a stream, it does so on that stream."""
+    names = f.__code__.co_varnames[:f.__code__.co_argcount]
+    at = len(names) - 1
+    name = names[at]
+    assert name in ("stream", "copy_stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = kw.pop(name, None) if len(args) <= at else args[at]
+        return f(*args[:at], **kw) if stream is None else _on_stream(stream, f, *args[:at], **kw)
+
+    return call
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -79,6 +96,7 @@ def rope_table(max_pos: int, d: int, base: float = 1.0e6, device="cuda") -> torc
     return torch.from_numpy(host).to(device)
 
 
+@_allocates
 def chunk_doc_map(doc_chunk_off: torch.Tensor, n_chunks: int, stream=None) -> torch.Tensor:
     out = torch.empty(n_chunks, dtype=torch.int32, device=doc_chunk_off.device)
     check(lib.msa_chunk_doc_map(_ptr(doc_chunk_off), doc_chunk_off.numel() - 1, n_chunks, _ptr(out), _stream(stream)),
@@ -96,6 +114,7 @@ def msa_rope_doc(x: torch.Tensor, seg_tok_off: torch.Tensor, pos_offset: int, co
     return out
 
 
+@_allocates
 def msa_pool_chunks(k, v, kr, doc_tok_off, doc_chunk_off, chunk_doc, chunk: int, cos_sin=None,
                     fuse_doc_rope: bool = True, out_dtype=None, normalize_router: bool = True, kvbar=None,
                     kr_index=None, stream=None):
@@ -119,6 +138,7 @@ def msa_pool_chunks(k, v, kr, doc_tok_off, doc_chunk_off, chunk_doc, chunk: int,
     return (kvbar if k is not None else None), (kr_index if kr is not None else None)
 
 
+@_allocates
 def msa_pack_tokens(k, v, doc_tok_off, cos_sin, bank=None, stream=None):
     """Token-level memory bank of the fine stage: k, v [n_tok, hkv, d] -> bank [n_tok, 2, hkv, d] with each
     key rotated to its position inside its document (doc_tok_off [n_docs+1], device int64)."""
@@ -163,6 +183,7 @@ def route_set_impl(impl: int) -> None:
     check(lib.msa_route_set_impl(impl), "msa_route_set_impl")
 
 
+@_allocates
 def msa_route_scores(kr_index, chunk_doc, n_docs: int, qr, doc_scores=None, chunk_scores=None,
                      want_chunk_scores: bool = False, ws=None, stream=None):
     """Router scores: kr_index [C, H, d] (index form), qr [n_q, T, H, d] -> doc_scores [n_q, n_docs]
@@ -197,6 +218,7 @@ def topk_workspace_size(n_q: int, n_docs: int, k: int) -> int:
     return n.value
 
 
+@_allocates
 def msa_topk_docs(doc_scores, k: int, idx=None, score=None, ws=None, stream=None):
     """-> (idx int32 [n_q, k], score float32 [n_q, k]) by descending score, ties to the lower index."""
     n_q, n_docs = doc_scores.shape
@@ -210,6 +232,7 @@ def msa_topk_docs(doc_scores, k: int, idx=None, score=None, ws=None, stream=None
     return idx, score
 
 
+@_allocates
 def msa_topk_docs_noalloc(doc_scores, k: int, idx=None, score=None, stream=None):
     """msa_topk_docs without a workspace: for callers that cannot allocate device memory at selection
     time. Scratch is the library's fixed device array; calls that overlap on the GPU race."""
@@ -222,6 +245,7 @@ def msa_topk_docs_noalloc(doc_scores, k: int, idx=None, score=None, stream=None)
     return idx, score
 
 
+@_allocates
 def msa_topk_merge(cand_score, cand_idx, shard_doc_off, k: int, idx=None, score=None, shard_stride=None,
                    stream=None):
     """Memory Parallel merge: cand_score float32 / cand_idx int32 lists [n_q, k_cand] of every shard (device,
@@ -245,6 +269,7 @@ def msa_topk_merge(cand_score, cand_idx, shard_doc_off, k: int, idx=None, score=
     return idx, score
 
 
+@_allocates
 def msa_gather_kv(host_bank, doc_chunk_off_host, idx_host, max_mem: int, dev_mem_kv=None, device="cuda",
                   copy_stream=None):
     """Copy the selected docs' rows [*, 2, hkv, d] from the pinned host bank into
@@ -261,6 +286,7 @@ def msa_gather_kv(host_bank, doc_chunk_off_host, idx_host, max_mem: int, dev_mem
     return dev_mem_kv, mem_len
 
 
+@_allocates
 def msa_gather_kv_device(host_bank, doc_chunk_off, idx, max_mem: int, dev_mem_kv=None, mem_len=None, stream=None):
     """Device-side fetch: idx [n_q, k] int32 and doc_chunk_off on the device; the pinned host bank is
     read by a kernel. Returns (dev_mem_kv [n_q, max_mem, 2, hkv, d], mem_len int32 [n_q] on the device)."""
@@ -277,6 +303,7 @@ def msa_gather_kv_device(host_bank, doc_chunk_off, idx, max_mem: int, dev_mem_kv
     return dev_mem_kv, mem_len
 
 
+@_allocates
 def msa_sparse_attn(q, mem_kv, mem_len, local_k, local_v, L: int, q_start: int, scale: float | None = None,
                     out=None, stream=None):
     """q [n_q, T, hq, d] (rotated), mem_kv [n_q, max_mem, 2, hkv, d], mem_len int32 [n_q] (device),
@@ -309,6 +336,7 @@ def sparse_attn_split_plan(n_q: int, T: int, hq: int, hkv: int, max_mem: int, L:
     return {"row_blocks": rb.value, "key_ranges": kr.value, "cluster": cl.value}
 
 
+@_allocates
 def msa_sparse_attn_split(q, mem_kv, mem_len, local_k, local_v, L: int, q_start: int, scale: float | None = None,
                           out=None, ws=None, lse=None, stream=None):
     """msa_sparse_attn for long memories (token-level fine stage): keys split into ranges that run as
@@ -501,6 +529,7 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
 
 
 # ------------------------------------------------------------------------------------------------ backward
+@_allocates
 def msa_sparse_attn_backward(q, mem_kv, mem_len, local_k, local_v, L: int, q_start: int, out, dout, lse,
                              scale: float | None = None, grads=None, ws=None, stream=None):
     """Gradients of the sparse attention (bf16 inputs): returns (dq [n_q, T, hq, d], dmem_kv [n_q, max_mem, 2,
@@ -528,6 +557,7 @@ def msa_sparse_attn_backward(q, mem_kv, mem_len, local_k, local_v, L: int, q_sta
     return grads
 
 
+@_allocates
 def msa_gather_kv_backward(dmem_kv, doc_chunk_off, idx, n_chunks: int, dkvbar=None, accumulate: bool = False,
                            stream=None):
     """Memory-row gradients [n_q, max_mem, 2, hkv, d] (fp32) into chunk-row gradients dkvbar [n_chunks, 2, hkv, d]
@@ -543,6 +573,7 @@ def msa_gather_kv_backward(dmem_kv, doc_chunk_off, idx, n_chunks: int, dkvbar=No
     return dkvbar
 
 
+@_allocates
 def msa_pool_chunks_backward(dkvbar, dkr_index, doc_tok_off, doc_chunk_off, chunk_doc, chunk: int, n_tok: int,
                              kr=None, cos_sin=None, fuse_doc_rope: bool = True, normalize_router: bool = True,
                              stream=None):
@@ -568,6 +599,7 @@ def msa_pool_chunks_backward(dkvbar, dkr_index, doc_tok_off, doc_chunk_off, chun
     return dk, dv, dkr
 
 
+@_allocates
 def msa_router_aux_loss(doc_scores, evidence, tau: float, stream=None):
     """(loss per query [n_q], dL/d doc_scores [n_q, D]) of the auxiliary router loss; evidence int32 [n_q, n_ev]
     (-1 padding). The gradient is that of the mean of the per-query losses."""
@@ -580,6 +612,7 @@ def msa_router_aux_loss(doc_scores, evidence, tau: float, stream=None):
     return loss, grad
 
 
+@_allocates
 def msa_route_backward(kr_index, doc_chunk_off, qr, d_doc_scores, stream=None):
     """(dqr [n_q, T, H, d], dkhat [C, H, d]) fp32: gradients of the router's document scores."""
     C, H, d = kr_index.shape
@@ -597,7 +630,8 @@ def msa_route_backward(kr_index, doc_chunk_off, qr, d_doc_scores, stream=None):
 
 
 class InterleaveRound:
-    """Marshals msa_interleave_args for one round; holds the ctypes structures alive."""
+    """Marshals msa_interleave_args for one round; holds the ctypes structures alive. Its workspace, unless given, comes
+    from the stream that is current at creation: a `compute` or `copy` stream of the caller's own waits for that one first."""
 
     def __init__(self, layers, *, n_chunks, n_docs, doc_chunk_off, doc_chunk_off_host, chunk_doc, n_q, H, d, hq, hkv,
                  k, L_prev, T_new, new_q_stride, L_max, max_mem, cos_sin, scale=None, dtype=torch.bfloat16, ws=None,

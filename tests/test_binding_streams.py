@@ -119,3 +119,68 @@ def test_a_stream_of_another_device_is_refused(monkeypatch, world):
         with pytest.raises(ValueError, match="device"):
             call(stream=Stream(11, index=1))
     assert not world.launched
+
+
+def _older_calls():
+    bf, i32, i64, f32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
+    x, off = torch.zeros((6, 2, D), dtype=bf), torch.tensor([0, 3, 6])
+    off2 = torch.tensor([0, 1, 2])
+    chunks, cs, doc = torch.zeros((2, 2, D), dtype=bf), torch.zeros((8, D // 2, 2)), torch.zeros(2, dtype=i32)
+    bank, qr = torch.zeros((2, 2, 2, D), dtype=bf), torch.zeros((1, 3, 2, D), dtype=bf)
+    q, loc = torch.zeros((1, 3, 4, D), dtype=bf), torch.zeros((1, 4, 2, D), dtype=bf)
+    mem, ln = torch.zeros((1, 2, 2, 2, D), dtype=bf), torch.zeros(1, dtype=i32)
+    sc, idx = torch.zeros((1, 2)), torch.zeros((1, 1), dtype=i32)
+    fq, dmem = torch.zeros((1, 3, 4)), torch.zeros((1, 2, 2, 2, D))
+    return {
+        "msa_chunk_doc_map": lambda **s: m.chunk_doc_map(off, 6, **s),
+        "msa_pool_chunks": lambda **s: m.msa_pool_chunks(x, x, x, off, off2, doc, 3, cos_sin=cs, **s),
+        "msa_pack_tokens": lambda **s: m.msa_pack_tokens(x, x, off, cs, **s),
+        "msa_route_scores": lambda **s: m.msa_route_scores(chunks, doc, 2, qr, want_chunk_scores=True, **s),
+        "msa_topk_docs": lambda **s: m.msa_topk_docs(sc, 1, **s),
+        "msa_topk_docs_noalloc": lambda **s: m.msa_topk_docs_noalloc(sc, 1, **s),
+        "msa_topk_merge": lambda **s: m.msa_topk_merge(sc[None], idx.expand(1, 2)[None].contiguous(), [0, 2], 1, **s),
+        "msa_gather_kv": lambda **s: m.msa_gather_kv(bank, off2, idx, 2, device="cpu", **{"copy_" + n: v for n, v in s.items()}),
+        "msa_gather_kv_device": lambda **s: m.msa_gather_kv_device(bank, off2, idx, 2, **s),
+        "msa_sparse_attn": lambda **s: m.msa_sparse_attn(q, mem, ln, loc, loc, 4, 1, **s),
+        "msa_sparse_attn_split": lambda **s: m.msa_sparse_attn_split(q, mem, ln, loc, loc, 4, 1, **s),
+        "msa_sparse_attn_backward": lambda **s: m.msa_sparse_attn_backward(q, mem, ln, loc, loc, 4, 1, q, q, fq, **s),
+        "msa_gather_kv_backward": lambda **s: m.msa_gather_kv_backward(dmem, off2, idx, 2, **s),
+        "msa_pool_chunks_backward": lambda **s: m.msa_pool_chunks_backward(
+            torch.zeros((2, 2, 2, D)), torch.zeros((2, 2, D)), off, off2, doc, 3, 6, kr=x, cos_sin=cs, **s),
+        "msa_router_aux_loss": lambda **s: m.msa_router_aux_loss(sc, idx.to(i64), 0.1, **s),
+        "msa_route_backward": lambda **s: m.msa_route_backward(chunks, off2, qr, sc, **s),
+    }
+
+
+def _made(w):
+    return [s for _, s in w.seen]
+
+
+@pytest.mark.parametrize("name", list(_older_calls()))
+def test_what_a_call_allocates_or_fills_belongs_to_its_stream(monkeypatch, world, name):
+    call = _older_calls()[name]
+    world.stub(monkeypatch, name)
+    with Watch(world) as w:
+        call()                                     # the inputs' own conversions may allocate too: not on this list
+    assert all(s is world.usual for s in _made(w)) and not world.kept
+    with Watch(world) as w:
+        got = call(stream=world.side)
+    assert world.side in _made(w)
+    # what the call made after it began: everything from the first allocation on the side stream
+    assert all(s is world.side for s in _made(w)[_made(w).index(world.side):])
+    handles = [a[-1] for _, a in world.launched]
+    assert handles == [world.usual.cuda_stream, world.side.cuda_stream]
+    for t in got if isinstance(got, tuple) else (got,):
+        assert world.usual in world.kept_for(t)
+
+
+def test_a_stream_may_be_given_by_place(monkeypatch, world):
+    world.stub(monkeypatch, "msa_topk_docs")
+    sc = torch.zeros((1, 2))
+    with Watch(world) as w:
+        m.msa_topk_docs(sc, 1, None, None, None, world.side)
+    assert _made(w) and all(s is world.side for s in _made(w))
+    given = torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 1))
+    world.kept.clear()
+    got = m.msa_topk_docs(sc, 1, idx=given[0], score=given[1], stream=world.side)
+    assert got[0] is given[0] and not world.kept       # the caller's own tensors are the caller's

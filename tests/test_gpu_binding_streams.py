@@ -85,3 +85,32 @@ def test_results_of_a_paged_call_outlive_what_the_current_stream_reads(m, new):
         for x, y in zip(kept, want):
             assert torch.equal(x, y)
     assert m.device_status() == 0
+
+
+def test_a_backlog_on_the_current_stream_does_not_reach_an_older_call(m):
+    """Selection (results and scratch), the fetch (rows that the call zeroes before it fills them) and attention."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    C, k, hkv = 4000, 8, 2
+    scores = torch.randn((4, C), generator=g, device="cuda")
+    bank = torch.randn((C, 2, hkv, D), generator=g, device="cuda").bfloat16().cpu().pin_memory()
+    off = torch.arange(C + 1, device="cuda")
+    q = torch.randn((4, 16, 8, D), generator=g, device="cuda").bfloat16()
+    loc = torch.randn((4, 16, hkv, D), generator=g, device="cuda").bfloat16()
+
+    def step(**s):
+        idx, top = m.msa_topk_docs(scores, k, **s)
+        mem, n = m.msa_gather_kv_device(bank, off, idx, k, **s)
+        return idx, top, mem, n, m.msa_sparse_attn(q, mem, n, loc, loc, 16, 0, **s), m.msa_sparse_attn_split(
+            q, mem, n, loc, loc, 16, 0, **s)
+
+    want = [x.clone() for x in step()]
+    torch.cuda.synchronize()
+    sizes = [x.nbytes for x in want] + [m.topk_workspace_size(4, C, k), m.sparse_attn_split_workspace_size(4, 16, 8, hkv, k, 16)]
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        _leave_queued(sizes)
+        got = step(stream=side)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    assert m.device_status() == 0
