@@ -515,7 +515,9 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
         lse = kv.scales.new_empty(n_tok, hq)
     k = 0
     if sel is not None:
-        k = sel.shape[-1]
+        k = sel.shape[2] if sel.dim() == 3 else 0
+        if k == 0:                               # an empty tensor has no address: the call would not see the list
+            raise ValueError(f"msa_paged_attn: sel must be int32 [n_tok, hkv, k] with k at least 1, got {tuple(sel.shape)}")
         _want("msa_paged_attn", "sel", sel, torch.int32, (n_tok, kv.hkv, k))
     if ws is None:
         ws = kv._u8.new_empty(paged_attn_workspace_size(n_tok, kv.n_seq, max_new, hq, kv.hkv, kv.max_pages, kv.page, k))

@@ -1,0 +1,24 @@
+"""A page list without entries is refused: it is not the same as no list. No GPU is needed."""
+import pytest
+import torch
+
+import routed_long_context_b200 as m
+from routed_long_context_b200 import api
+
+D = 128
+
+
+@pytest.mark.parametrize("shape", [(2, 2, 0), (2, 0), (0,), ()])
+def test_an_empty_page_list_is_refused(monkeypatch, shape):
+    kv = m.PagedKV(torch.empty((3, 2, 2, 16, D), dtype=torch.float8_e4m3fn), torch.ones((3, 2, 2)),
+                   torch.zeros((1, 3), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    monkeypatch.setattr(m.PagedKV, "_check", lambda *a: None)
+    monkeypatch.setattr(m.PagedKV, "_stream", lambda *a: 0)
+    launched = []
+    monkeypatch.setattr(api.lib, "msa_paged_attn", lambda *a: launched.append(a) or 0)
+    q, off = torch.zeros((2, 4, D), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="sel"):
+        m.msa_paged_attn(kv, q, off, 2, sel=torch.zeros(shape, dtype=torch.int32))
+    assert not launched
+    m.msa_paged_attn(kv, q, off, 2, sel=torch.zeros((2, 2, 1), dtype=torch.int32))
+    assert launched[0][7] and launched[0][8] == 1
