@@ -339,7 +339,8 @@ msa_status msa_sparse_attn_split_plan(int n_q, int T, int hq, int hkv, int max_m
  * k, v, q and out are the last n = tok_off[s+1] - tok_off[s] tokens of sequence s, n from 0 to max_new.
  * Rows before tok_off[0] or from tok_off[n_seq] on are neither read nor written. A sequence whose offsets
  * or length contradict n_tok, max_new, max_pages or one another records MSA_DEV_BAD_INDEX and is skipped
- * whole; a page index outside [0, n_pages) records it too, and that page's tokens are skipped: not stored,
+ * whole (where offsets decrease, which of the sequences that then share rows are served in part is not
+ * defined; nothing beside their pages and rows is written); a page index outside [0, n_pages) records it too, and that page's tokens are skipped: not stored,
  * and not seen by any query. Pages may be shared by sequences that only read them; a page that a call
  * appends to belongs to one sequence.
  * --------------------------------------------------------------------------------------------- */

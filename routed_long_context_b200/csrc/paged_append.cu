@@ -174,6 +174,9 @@ __global__ void __launch_bounds__(4 * PAGE, PAGE == 128 ? 1 : 768 / (4 * PAGE)) 
         int64_t first;
         s = seq_of_item(a, item, &first);
         j = item - first;
+        // where offsets decrease the search may find no item of some sequence: each is looked at by a block of its own
+        SeqSpan each;
+        if (part == 0 && item < v.n_seq && tid == 32) seq_span(v, a.tok_off, a.n_tok, a.max_new, item, &each, a.err);
     }
     SeqSpan sp;
     if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, tid == 0 ? a.err : nullptr)) return;

@@ -248,8 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
     };
     Sums total{0, 0}, first_total{0, 0};
     if (LIST) {
-        if (at_hand) load_window(0);
-        else __syncthreads();
+        if (at_hand) {
+            load_window(0);
+        } else {                                           // sequences that no token leads to are looked at too
+            SeqSpan each;
+            for (int64_t i = blockIdx.x + (int64_t)tid * gridDim.x; i < v.n_seq; i += (int64_t)kThreads * gridDim.x)
+                seq_span(v, a.tok_off, a.n_tok, a.max_new, (int)i, &each, a.err);
+            __syncthreads();
+        }
         total.tiles = total.units = a.n_tok * v.hkv * (long long)list_tiles;       // all segments are alike
         first_total = total;
     } else {

@@ -304,6 +304,11 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.G, hq = v.hkv * G;
     wait_for_earlier();
+    if (g == 0 && warp == kPickThreads / 32 - 1) {         // sequences that no token leads to are looked at too
+        SeqSpan each;
+        for (int64_t i = blockIdx.x + (int64_t)lane * gridDim.x; i < v.n_seq; i += 32ll * gridDim.x)
+            seq_span(v, a.tok_off, a.n_tok, a.max_new, (int)i, &each, a.err);
+    }
     const int s = seq_of_token(a.tok_off, v.n_seq, t);
     SeqSpan sp;
     int32_t* sel = a.sel + (t * v.hkv + g) * a.k;
