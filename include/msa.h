@@ -395,8 +395,9 @@ msa_status msa_paged_attn_workspace_size(int64_t n_tok, int n_seq, int max_new, 
 /* Pages for a sparse pass of msa_paged_attn: for every new token and kv head the k pages, of those that the
  * token sees, with the largest score
  *   max over the group's query heads of sum_d max(q_d * bounds_min_d, q_d * bounds_max_d),
- * the largest q . k that keys inside the page's bounds could give (summed in 64 bits); the `recent` newest
- * pages always count as the best, equal scores go to the lower page. sel: device int32 [n_tok][hkv][k], page
+ * the largest q . k that keys inside the page's bounds could give (summed in 64 bits; a head whose sum is NaN
+ * counts for nothing, a page without any other sum as the lowest); the `recent` newest pages always count as the
+ * best, equal scores go to the lower page. sel: device int32 [n_tok][hkv][k], page
  * indices into the sequence's row of page_table, ascending, -1 behind the last where the token sees fewer
  * than k pages. Rows outside the sequences are left as they were. bf16 queries (rotated), 1 <= recent <= k,
  * hq/hkv in {1, 2, 4, 8}. ws: msa_page_select_workspace_size bytes. */

@@ -49,6 +49,13 @@ constexpr int kCand = 1023;                    // candidates for the k best that
 constexpr size_t kPickSmem = 200 * 1024;       // of scores; more pages are all summed in 64 bits
 constexpr float kNoPage = -3.402823466e38f;    // score of a page that is not there
 
+// The larger; a NaN stays.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float z;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+    return z;
+}
+
 __global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) {
     __shared__ uint4 s_q[kGroup][8][32];       // B fragments: [row tile][16-byte piece][lane]
     __shared__ float s_top[8];
@@ -166,20 +173,16 @@ __global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) 
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float x = fabsf(__uint_as_float(u[j] << 16)), y = fabsf(__uint_as_float(u[j] & 0xFFFF0000u));
-                    top = x <= top ? top : x;              // a NaN stays
-                    top = y <= top ? top : y;
+                    top = max_nan(top, max_nan(x, y));
                 }
             }
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            const float x = __shfl_xor_sync(0xffffffffu, top, o);
-            top = x <= top ? top : x;
-        }
+        for (int o = 16; o >= 1; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane == 0) s_top[warp] = top;
         __syncthreads();
         if (tid == 0) {
             float x = 0.f;
-            for (int i = 0; i < 8; ++i) x = s_top[i] <= x ? x : s_top[i];
+            for (int i = 0; i < 8; ++i) x = max_nan(x, s_top[i]);
             a.bmax[(sp.t0 * v.hkv + g) * a.chunks + chunk] = x;
         }
     }
@@ -452,10 +455,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
         s_score[i] = x;
         mine = max(mine, x);
     }
-    for (int i = tid; i < (n + kScorePages - 1) / kScorePages; i += kPickThreads) {
-        const float b = bmax[i];
-        bm = b <= bm ? bm : b;                             // a NaN stays
-    }
+    for (int i = tid; i < (n + kScorePages - 1) / kScorePages; i += kPickThreads) bm = max_nan(bm, bmax[i]);
     float qs = 0.f;
     if (warp < G) {
 #pragma unroll
@@ -464,10 +464,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
         for (int o = 16; o >= 1; o >>= 1) qs += __shfl_xor_sync(0xffffffffu, qs, o);
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        const float b = __shfl_xor_sync(0xffffffffu, bm, o);
-        bm = b <= bm ? bm : b;
-    }
+    for (int o = 16; o >= 1; o >>= 1) bm = max_nan(bm, __shfl_xor_sync(0xffffffffu, bm, o));
     if (lane == 0) {
         sm.red[0][warp] = qs;
         sm.red[1][warp] = bm;
@@ -476,10 +473,11 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     qs = bm = 0.f;
 #pragma unroll
     for (int w = 0; w < kPickThreads / 32; ++w) {
-        qs = sm.red[0][w] <= qs ? qs : sm.red[0][w];
-        bm = sm.red[1][w] <= bm ? bm : sm.red[1][w];
+        qs = max_nan(qs, sm.red[0][w]);
+        bm = max_nan(bm, sm.red[1][w]);
     }
-    const float E = qs * bm * 6.103515625e-05f + 1e-36f;   // 2^-14, and what underflow may lose
+    // 2^-14, and what underflow may lose; NaN, and with it all pages near the border, where a query or a bound is
+    const float E = qs * bm * 6.103515625e-05f + 1e-36f;
 
     // Few candidates first, where k allows: at least k scores reach the k-th best of the threads' own maxima, folded to
     // 2 k of them or a little more (about 1.4 k scores reach that; fewer maxima are quicker to rank).

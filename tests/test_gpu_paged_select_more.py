@@ -1,0 +1,75 @@
+"""Page selection where the 32-bit scores do not decide: queries and bounds that are not finite, more pages than
+candidates are kept for, near-ties."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_cache as C
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+
+
+@pytest.fixture(scope="module")
+def m():
+    import routed_long_context_b200 as m
+
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return m
+
+
+def _cache(m, lo, hi, page=16):
+    """One sequence of len(lo) full pages with these bounds [pages, hkv, d], in shuffled places; keys do not matter."""
+    n, hkv, _ = lo.shape
+    kv = m.PagedKV.empty(n + 3, 1, n, hkv, page)
+    ids = torch.from_numpy(np.random.default_rng(n).permutation(n + 3)[:n].astype(np.int32))
+    kv.page_table.copy_(ids[None])
+    kv.seq_len.fill_(n * page)
+    kv.bounds[ids.long().cuda()] = torch.stack((lo, hi), 2).cuda().bfloat16()
+    return kv
+
+
+def _near_ties(seed, n, hkv=1):
+    """Bounds of which one element is large, so that the sums of the small ones are lost in 32 bits."""
+    x = torch.rand((n, hkv, D), generator=torch.Generator().manual_seed(seed)) * 0.1
+    x[..., 0] = 2.0 ** 20
+    x = x.bfloat16().float()
+    return -x, x
+
+
+def _want(lo, hi, q, k, recent):
+    """The definition over the heads of q [G, d] (finite ones)."""
+    return C.pick(C.page_scores(q, lo.double().numpy(), hi.double().numpy()), k, recent)
+
+
+@pytest.mark.parametrize("k", [20, 300])
+@pytest.mark.parametrize("where", [1, 2])
+def test_a_query_head_that_is_nan_does_not_blur_the_others(m, where, k):
+    """Its sum counts for nothing, and what the sums of the other heads may be off by is still allowed for."""
+    lo, hi = _near_ties(1, 700)
+    kv = _cache(m, lo, hi)
+    q = torch.zeros((1, 4, D))
+    q[0, 0] = 1.0
+    q[0, where, 7] = math.nan
+    off = torch.tensor([0, 1], device="cuda")
+    sel = m.msa_page_select(kv, q.bfloat16().cuda(), off, 1, k).cpu().numpy()
+    assert m.device_status() == 0
+    np.testing.assert_array_equal(sel[0, 0], _want(lo[:, 0], hi[:, 0], np.ones((1, D)), k, 1))
+
+
+@pytest.mark.parametrize("place", [0, 1, 127, 128, 500])
+def test_a_page_whose_bounds_are_nan_does_not_blur_the_others(m, place):
+    lo, hi = _near_ties(2, 700)
+    nan_lo, nan_hi = lo.clone(), hi.clone()
+    nan_lo[place], nan_hi[place] = math.nan, math.nan
+    # the largest bounds of the other pages come before and after it
+    kv = _cache(m, nan_lo, nan_hi)
+    off = torch.tensor([0, 1], device="cuda")
+    sel = m.msa_page_select(kv, torch.ones((1, 1, D), dtype=torch.bfloat16, device="cuda"), off, 1, 20).cpu().numpy()
+    assert m.device_status() == 0
+    s = C.page_scores(np.ones((1, D)), lo[:, 0].double().numpy(), hi[:, 0].double().numpy())
+    s[place] = -np.inf
+    np.testing.assert_array_equal(sel[0, 0], C.pick(s, 20, 1))
