@@ -492,19 +492,18 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
         const float f = unordered32(t);
         // everything near the border, wherever above it that turns out to be, and all that compares with nothing
         const uint32_t floor = t == 0xFFFFFFFFu ? t : (f - 2.f * E > -3.402823466e38f) ? ordered32(f - 2.f * E) : 0u;
-        for (int i = tid; i < n; i += kPickThreads) {
-            const uint32_t x = s_score[i];
-            const bool yes = x >= floor || x == 0;
-            const unsigned m = __ballot_sync(__activemask(), yes);
-            if (yes) {
-                const int leader = __ffs(m) - 1;
-                int at = 0;
-                if (lane == leader) at = atomicAdd(&sm.n_cand, __popc(m));
-                at = __shfl_sync(m, at, leader) + __popc(m & ((1u << lane) - 1));
-                if (at < kCand) {
-                    sm.cand[at] = x;
-                    sm.cand_page[at] = i;
-                }
+        for (int i0 = 0; i0 < n; i0 += kPickThreads) {     // as many turns for every lane: all take part in the votes
+            const int i = i0 + tid;
+            const uint32_t x = i < n ? s_score[i] : 0;
+            const bool yes = i < n && (x >= floor || x == 0);
+            const unsigned m = __ballot_sync(0xffffffffu, yes);
+            if (m == 0) continue;                          // of the whole warp
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&sm.n_cand, __popc(m));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+            if (yes && at < kCand) {
+                sm.cand[at] = x;
+                sm.cand_page[at] = i;
             }
         }
         __syncthreads();

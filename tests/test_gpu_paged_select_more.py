@@ -73,3 +73,24 @@ def test_a_page_whose_bounds_are_nan_does_not_blur_the_others(m, place):
     s = C.page_scores(np.ones((1, D)), lo[:, 0].double().numpy(), hi[:, 0].double().numpy())
     s[place] = -np.inf
     np.testing.assert_array_equal(sel[0, 0], C.pick(s, 20, 1))
+
+
+def _ordinary(seed, n, hkv):
+    g = torch.Generator().manual_seed(seed)
+    a, b = torch.randn((2, n, hkv, D), generator=g).bfloat16().float()
+    return torch.minimum(a, b), torch.maximum(a, b)
+
+
+@pytest.mark.parametrize("n", [18, 33, 65, 255, 257, 300, 511, 513, 1000, 1025, 2047, 2081])
+@pytest.mark.parametrize("k", [1, 17, 63, 250])
+def test_any_number_of_pages(m, n, k):
+    """Warps whose lanes have unlike numbers of pages, and single lanes with one."""
+    lo, hi = _ordinary(n + k, n, 2)
+    kv = _cache(m, lo, hi)
+    q = torch.randn((1, 4, D), generator=torch.Generator().manual_seed(k)).bfloat16()
+    off = torch.tensor([0, 1], device="cuda")
+    recent = min(2, k)
+    sel = m.msa_page_select(kv, q.cuda(), off, 1, k, recent).cpu().numpy()
+    assert m.device_status() == 0
+    for g in range(2):
+        np.testing.assert_array_equal(sel[0, g], _want(lo[:, g], hi[:, g], q[0, 2 * g:2 * g + 2].double().numpy(), k, recent))
