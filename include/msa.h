@@ -400,7 +400,8 @@ msa_status msa_paged_attn_workspace_size(int64_t n_tok, int n_seq, int max_new, 
  * best, equal scores go to the lower page. sel: device int32 [n_tok][hkv][k], page
  * indices into the sequence's row of page_table, ascending, -1 behind the last where the token sees fewer
  * than k pages. Rows outside the sequences are left as they were. bf16 queries (rotated), 1 <= recent <= k,
- * hq/hkv in {1, 2, 4, 8}. ws: msa_page_select_workspace_size bytes. */
+ * hq/hkv in {1, 2, 4, 8}. ws: msa_page_select_workspace_size bytes, at most 256 MiB unless one token's scores take
+ * more (long calls go through their tokens in slices). */
 msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa_dtype dt, int64_t n_tok, int hq,
                            const int64_t* tok_off, int max_new, int k, int recent, int32_t* sel, void* ws,
                            size_t ws_bytes, void* stream);

@@ -34,8 +34,10 @@ struct SelectArgs {
     const int64_t* tok_off;
     int max_new, G, k, recent;
     int32_t* sel;
-    unsigned long long* rows;      // [n_tok][hkv][max_pages]: fp32 scores in a row's first half, later 64-bit keys
-    float* bmax;                   // [n_tok][hkv][chunks], row of a sequence's first token: largest |bound| of 128 pages
+    int64_t first, last;           // the packed rows of this launch
+    // from `first` on: [rows][hkv][max_pages], fp32 scores in a row's first half, later 64-bit keys
+    unsigned long long* rows;
+    float* bmax;                   // [rows][hkv][chunks], row of a sequence's first token: largest |bound| of 128 pages
     int chunks, token_parts;       // of the scoring grid
     int scores_in_smem;
     int* err;
@@ -48,6 +50,14 @@ constexpr int kNear = kPickThreads;            // border pages that are ranked i
 constexpr int kCand = 1023;                    // candidates for the k best that are kept there
 constexpr size_t kPickSmem = 200 * 1024;       // of scores; more pages are all summed in 64 bits
 constexpr float kNoPage = -3.402823466e38f;    // score of a page that is not there
+
+// Of a sequence's new tokens those of this launch, as if the last of them ended the sequence.
+__device__ __forceinline__ void clip(const SelectArgs& a, SeqSpan* sp) {
+    const int64_t end = sp->t0 + sp->n_new, t0 = max(sp->t0, a.first), t1 = max(t0, min(end, a.last));
+    sp->len -= (int)(end - t1);
+    sp->n_new = (int)(t1 - t0);
+    sp->t0 = t0;
+}
 
 // The larger; a NaN stays.
 __device__ __forceinline__ float max_nan(float x, float y) {
@@ -66,7 +76,9 @@ __global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) 
     const int G = a.G, gs = 31 - __clz(G), hq = v.hkv * G;
     next_may_launch();
     SeqSpan sp;
-    if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr) || sp.n_new == 0) return;
+    if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, nullptr)) return;
+    clip(a, &sp);
+    if (sp.n_new == 0) return;
     const int n_pages = (sp.len + v.page - 1) >> v.shift;
     const int p0 = chunk * kScorePages;
     if (p0 >= n_pages || n_pages <= a.k) return;           // every visible page is picked
@@ -149,7 +161,7 @@ __global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) 
                     float y = x[t][2 * h];
                     if (G == 1) {
                         if (mine && p < n_pages && row + 1 < sp.n_new)
-                            reinterpret_cast<float*>(a.rows + ((sp.t0 + row + 1) * v.hkv + g) * v.max_pages)[p] =
+                            reinterpret_cast<float*>(a.rows + ((sp.t0 - a.first + row + 1) * v.hkv + g) * v.max_pages)[p] =
                                 there[h] ? x[t][2 * h + 1] : kNoPage;
                     } else {
                         y = fmaxf(y, x[t][2 * h + 1]);
@@ -158,7 +170,8 @@ __global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) 
                     }
                     const int tok = row >> gs;
                     if (mine && (row & (G - 1)) == 0 && p < n_pages && tok < sp.n_new)
-                        reinterpret_cast<float*>(a.rows + ((sp.t0 + tok) * v.hkv + g) * v.max_pages)[p] = there[h] ? y : kNoPage;
+                        reinterpret_cast<float*>(a.rows + ((sp.t0 - a.first + tok) * v.hkv + g) * v.max_pages)[p] =
+                            there[h] ? y : kNoPage;
                 }
             }
         }
@@ -183,7 +196,7 @@ __global__ void __launch_bounds__(256, 2) page_score_kernel(const SelectArgs a) 
         if (tid == 0) {
             float x = 0.f;
             for (int i = 0; i < 8; ++i) x = max_nan(x, s_top[i]);
-            a.bmax[(sp.t0 * v.hkv + g) * a.chunks + chunk] = x;
+            a.bmax[((sp.t0 - a.first) * v.hkv + g) * a.chunks + chunk] = x;
         }
     }
 }
@@ -303,7 +316,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     extern __shared__ uint32_t s_score[];
     __shared__ PickSmem sm;
     const PagedView& v = a.v;
-    const int64_t t = blockIdx.x;
+    const int64_t t = a.first + blockIdx.x;
     const int g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.G, hq = v.hkv * G;
     wait_for_earlier();
@@ -318,13 +331,14 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     if (!seq_span(v, a.tok_off, a.n_tok, a.max_new, s, &sp, tid == 0 ? a.err : nullptr) || t < sp.t0 ||
         t >= sp.t0 + sp.n_new)
         return;
+    clip(a, &sp);
     const int n = ((sp.len - sp.n_new + (int)(t - sp.t0)) >> v.shift) + 1;      // visible pages
     if (n <= a.k) {
         for (int i = tid; i < a.k; i += kPickThreads) sel[i] = i < n ? i : -1;
         return;
     }
     const int newest = max(0, n - a.recent);               // pages from here on are in
-    unsigned long long* row64 = a.rows + (t * v.hkv + g) * v.max_pages;
+    unsigned long long* row64 = a.rows + ((int64_t)blockIdx.x * v.hkv + g) * v.max_pages;
     const __nv_bfloat16* q = a.q + (t * hq + g * G) * kPagedD;
 
     // a page's score in 64 bits, by one warp
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
 
     // the scores, and how far they may be off
     const float* score = reinterpret_cast<const float*>(row64);
-    const float* bmax = a.bmax + (sp.t0 * v.hkv + g) * a.chunks;
+    const float* bmax = a.bmax + ((sp.t0 - a.first) * v.hkv + g) * a.chunks;
     float bm = 0.f;
     uint32_t mine = 0;
 #pragma unroll 8
@@ -656,6 +670,25 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const SelectArg
     take_from_row(a.k);
 }
 
+// The workspace: rows of scores and maxima of bounds of as many packed rows as fit kSelectBytes, one at least; a longer
+// call goes through its rows in slices of that many. (All at once, 65,536 tokens of 8 kv heads over their 1,024 pages
+// would take 4 GB; a slice of them is 4,096 tokens, whose scores far outweigh reading the bounds again.)
+constexpr size_t kSelectBytes = 256u << 20;
+struct SelectPlan {
+    int64_t slice;         // packed rows
+    int chunks;
+    size_t bmax, bytes;    // offset and size in the workspace
+};
+SelectPlan select_plan(int64_t n_tok, int hkv, int max_pages) {
+    SelectPlan p{};
+    p.chunks = (max_pages + kScorePages - 1) / kScorePages;
+    const size_t row = (size_t)hkv * max_pages * sizeof(unsigned long long), top = (size_t)hkv * p.chunks * sizeof(float);
+    p.slice = std::min<int64_t>(n_tok, std::max<int64_t>(1, (int64_t)((kSelectBytes - 512) / (row + top))));
+    p.bmax = align_up(p.slice * row, 256);
+    p.bytes = p.bmax + align_up(p.slice * top, 256);
+    return p;
+}
+
 }  // namespace
 }  // namespace msa
 
@@ -665,8 +698,7 @@ extern "C" msa_status msa_page_select_workspace_size(int64_t n_tok, int hkv, int
     MSA_REQUIRE(bytes != nullptr, "msa_page_select_workspace_size: bytes is NULL");
     MSA_REQUIRE(n_tok >= 0 && n_tok < (int64_t)INT32_MAX / 2 && hkv > 0 && hkv <= 4096 && max_pages > 0,
                 "msa_page_select_workspace_size: bad sizes");
-    const size_t rows = (size_t)n_tok * hkv * max_pages;
-    *bytes = align_up(rows * sizeof(unsigned long long), 256) + align_up(rows * sizeof(float), 256);
+    *bytes = select_plan(n_tok, hkv, max_pages).bytes;
     return MSA_OK;
 }
 
@@ -693,26 +725,17 @@ extern "C" msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.n_tok = n_tok; a.tok_off = tok_off; a.max_new = max_new; a.k = k; a.recent = recent; a.sel = sel;
     a.rows = static_cast<unsigned long long*>(ws);
-    a.bmax = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                      align_up((size_t)n_tok * kv->hkv * kv->max_pages * sizeof(unsigned long long), 256));
+    const SelectPlan p = select_plan(n_tok, kv->hkv, kv->max_pages);
+    a.bmax = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.bmax);
     a.err = device_error_word();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    a.chunks = (kv->max_pages + kScorePages - 1) / kScorePages;
+    a.chunks = p.chunks;
     if ((int64_t)a.chunks * kv->n_seq > INT32_MAX)
         return set_error(MSA_ERR_UNSUPPORTED, "msa_page_select: n_seq * max_pages too large");
     size_t smem = (size_t)kv->max_pages * sizeof(uint32_t);
     a.scores_in_smem = smem <= kPickSmem;
     if (!a.scores_in_smem) smem = 0;
     const bool scored = k < kv->max_pages && a.scores_in_smem;
-    if (scored) {
-        // blocks for every SM: where pages and heads do not give enough, a sequence's query rows are parted too
-        const int64_t blocks = (int64_t)a.chunks * kv->n_seq * kv->hkv;
-        const int64_t groups = ((int64_t)std::min<int64_t>(max_new, n_tok) * a.G + 8 * kGroup - 1) / (8 * kGroup);
-        a.token_parts = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 592 / std::max<int64_t>(blocks, 1), 65535 / kv->hkv}));
-        const dim3 grid((unsigned)(a.chunks * kv->n_seq), (unsigned)(kv->hkv * a.token_parts));
-        page_score_kernel<<<grid, 256, 0, s>>>(a);
-        MSA_LAUNCH_CHECK();
-    }
     static std::mutex mu;
     static bool opted[64] = {false};
     int dev = 0;
@@ -724,6 +747,19 @@ extern "C" msa_status msa_page_select(const msa_paged_kv* kv, const void* q, msa
             if (dev >= 0 && dev < 64) opted[dev] = true;
         }
     }
-    MSA_CUDA_TRY(launch_early(page_pick_kernel, dim3((unsigned)n_tok, (unsigned)kv->hkv), kPickThreads, smem, s, a));
+    for (a.first = 0; a.first < n_tok; a.first = a.last) {
+        a.last = std::min(n_tok, a.first + p.slice);
+        const int64_t rows = a.last - a.first;
+        if (scored) {
+            // blocks for every SM: where pages and heads do not give enough, a sequence's query rows are parted too
+            const int64_t blocks = (int64_t)a.chunks * kv->n_seq * kv->hkv;
+            const int64_t groups = (std::min<int64_t>(max_new, rows) * a.G + 8 * kGroup - 1) / (8 * kGroup);
+            a.token_parts = (int)std::max<int64_t>(1, std::min<int64_t>({groups, 592 / std::max<int64_t>(blocks, 1), 65535 / kv->hkv}));
+            const dim3 grid((unsigned)(a.chunks * kv->n_seq), (unsigned)(kv->hkv * a.token_parts));
+            page_score_kernel<<<grid, 256, 0, s>>>(a);
+            MSA_LAUNCH_CHECK();
+        }
+        MSA_CUDA_TRY(launch_early(page_pick_kernel, dim3((unsigned)rows, (unsigned)kv->hkv), kPickThreads, smem, s, a));
+    }
     return MSA_OK;
 }

@@ -94,3 +94,56 @@ def test_any_number_of_pages(m, n, k):
     assert m.device_status() == 0
     for g in range(2):
         np.testing.assert_array_equal(sel[0, g], _want(lo[:, g], hi[:, g], q[0, 2 * g:2 * g + 2].double().numpy(), k, recent))
+
+
+@pytest.mark.parametrize("room", [40000, 60000])
+@pytest.mark.parametrize("first", [0, 5])
+def test_a_selection_that_goes_through_its_tokens_in_slices(m, room, first):
+    """A table with room for long contexts: the scratch holds fewer tokens than the call has. The slices end within
+    sequences; the same call with a tight table takes all tokens at once."""
+    hkv, G, page, news, lens = 8, 2, 16, [150, 0, 90, 33], [1700, 40, 2600, 33]
+    n_tok = first + sum(news) + 4
+    rows = n_tok * hkv * 8
+    assert m.page_select_workspace_size(n_tok, hkv, room) < rows * room and rows * 200 < 1 << 27
+    g = torch.Generator().manual_seed(room)
+    tight = m.PagedKV.empty(300, 4, 200, hkv, page)
+    a, b = torch.randn((2, 300, hkv, D), generator=g)
+    tight.bounds.copy_(torch.stack((torch.minimum(a, b), torch.maximum(a, b)), 2))
+    tight.page_table.copy_(torch.stack([torch.randperm(300, generator=g)[:200] for _ in range(4)]))
+    tight.seq_len.copy_(torch.tensor(lens))
+    table = torch.zeros((4, room), dtype=torch.int32, device="cuda")
+    table[:, :200] = tight.page_table
+    wide = m.PagedKV(tight.pages, tight.scales, table, tight.seq_len, tight.bounds)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(news)]) + first, device="cuda")
+    q = torch.randn((n_tok, hkv * G, D), generator=g).bfloat16().cuda()
+    sels = []
+    for kv in (tight, wide):
+        sel = torch.full((n_tok, hkv, 7), 77, dtype=torch.int32, device="cuda")
+        m.msa_page_select(kv, q, off, max(news), 7, 2, sel=sel)
+        sels.append(sel)
+    assert m.device_status() == 0
+    assert torch.equal(*sels)
+    assert (sels[0][:first] == 77).all() and (sels[0][-4:] == 77).all() and (sels[0][first:-4] < 77 * 3).all()
+    qs, bounds = q.double().cpu().numpy(), tight.bounds.double().cpu().numpy()
+    at = first
+    for s, n in enumerate(news):
+        for i in range(0, n, 29):
+            ids = tight.page_table[s, :(lens[s] - n + i) // page + 1].long().cpu().numpy()
+            for h in (0, hkv - 1):
+                sc = C.page_scores(qs[at + i, h * G:h * G + G], bounds[ids, h, 0], bounds[ids, h, 1])
+                np.testing.assert_array_equal(sels[0][at + i, h].cpu().numpy(), C.pick(sc, 7, 2))
+        at += n
+
+
+def test_guards_beside_the_scratch_of_slices(m):
+    hkv, room, n_tok = 8, 40000, 150
+    kv = m.PagedKV.empty(40, 1, room, hkv, 16)
+    kv.page_table[0, :40] = torch.arange(40, device="cuda")
+    kv.seq_len.fill_(640)
+    need = m.page_select_workspace_size(n_tok, hkv, room)
+    assert need < n_tok * hkv * room * 8
+    buf = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    q = torch.randn((n_tok, hkv, D), device="cuda").bfloat16()
+    m.msa_page_select(kv, q, torch.tensor([0, n_tok], device="cuda"), n_tok, 3, ws=buf[256:256 + need])
+    assert m.device_status() == 0
+    assert (buf[:256] == 0x5A).all() and (buf[256 + need:] == 0x5A).all()

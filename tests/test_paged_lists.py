@@ -22,3 +22,15 @@ def test_an_empty_page_list_is_refused(monkeypatch, shape):
     assert not launched
     m.msa_paged_attn(kv, q, off, 2, sel=torch.zeros((2, 2, 1), dtype=torch.int32))
     assert launched[0][7] and launched[0][8] == 1
+
+
+@pytest.mark.parametrize("n_tok,hkv,max_pages", [(65536, 8, 1025), (16384, 8, 12501), (1 << 20, 8, 16385), (4096, 1, 1 << 20)])
+def test_the_scratch_of_a_long_selection_is_bounded(n_tok, hkv, max_pages):
+    assert m.page_select_workspace_size(n_tok, hkv, max_pages) <= 256 << 20
+
+
+@pytest.mark.parametrize("n_tok,hkv,max_pages", [(1, 1, 1), (1, 8, 1025), (64, 8, 6251), (7, 3, 129), (1, 64, 1 << 20)])
+def test_the_scratch_of_a_selection_holds_a_row_of_scores_a_token(n_tok, hkv, max_pages):
+    """8 bytes a page, and a maximum of 128 pages' bounds beside them."""
+    least = n_tok * hkv * (8 * max_pages + 4 * -(-max_pages // 128))
+    assert least <= m.page_select_workspace_size(n_tok, hkv, max_pages) <= least + 512
