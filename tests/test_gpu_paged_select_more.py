@@ -147,3 +147,35 @@ def test_guards_beside_the_scratch_of_slices(m):
     m.msa_page_select(kv, q, torch.tensor([0, n_tok], device="cuda"), n_tok, 3, ws=buf[256:256 + need])
     assert m.device_status() == 0
     assert (buf[:256] == 0x5A).all() and (buf[256 + need:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("n", [1000, 3001])
+@pytest.mark.parametrize("k", [257, 300, 901])
+def test_more_pages_picked_than_candidates_are_kept_for(m, n, k):
+    lo, hi = _ordinary(n * 3 + k, n, 2)
+    kv = _cache(m, lo, hi)
+    new = 3
+    q = torch.randn((new, 8, D), generator=torch.Generator().manual_seed(n)).bfloat16()
+    off = torch.tensor([0, new], device="cuda")
+    sel = m.msa_page_select(kv, q.cuda(), off, new, k, 4).cpu().numpy()
+    assert m.device_status() == 0
+    for i in range(new):
+        for g in range(2):
+            np.testing.assert_array_equal(
+                sel[i, g], _want(lo[:, g], hi[:, g], q[i, 4 * g:4 * g + 4].double().numpy(), k, 4))
+
+
+@pytest.mark.parametrize("above,k", [(0, 20), (100, 120), (100, 139), (280, 281), (280, 300), (280, 319)])
+@pytest.mark.parametrize("near", [40, 250, 257])
+def test_near_ties_at_the_border_alone(m, above, k, near):
+    """Pages far above and far below, and some at the border that 32-bit sums cannot tell apart."""
+    n = 1500
+    lo, hi = _near_ties(above + near, n)
+    kind = torch.from_numpy(np.random.default_rng(near).permutation(n))
+    hi[kind < above, 0, 0] = 2.0 ** 21
+    hi[kind >= above + near, 0, 0] = 2.0 ** 19
+    kv = _cache(m, lo, hi)
+    off = torch.tensor([0, 1], device="cuda")
+    sel = m.msa_page_select(kv, torch.ones((1, 1, D), dtype=torch.bfloat16, device="cuda"), off, 1, k).cpu().numpy()
+    assert m.device_status() == 0
+    np.testing.assert_array_equal(sel[0, 0], _want(lo[:, 0], hi[:, 0], np.ones((1, D)), k, 1))
