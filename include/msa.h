@@ -388,6 +388,11 @@ msa_status msa_paged_append(const msa_paged_kv* kv, const void* k, const void* v
 msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_dtype dt, int64_t n_tok, int hq,
                           const int64_t* tok_off, int max_new, const int32_t* sel, int k, float scale, void* out,
                           float* lse, void* ws, size_t ws_bytes, void* stream);
+/* Failure-detection test hook of the attention kernels: from tile 20 * (on - 1) of a block on (many rows: tile
+ * 3 * (on - 1)) a launch's loader brings nothing, so the other warps' bounded waits expire (about 2 s); the kernel
+ * then records MSA_DEV_WAIT_TIMEOUT and leaves, with no copy or product in flight and the context usable. Results of
+ * such launches are meaningless. 0: off. Process-wide. */
+msa_status msa_paged_inject_stall(int on);
 /* k: entries of a page list, 0 without one. */
 msa_status msa_paged_attn_workspace_size(int64_t n_tok, int n_seq, int max_new, int hq, int hkv, int max_pages,
                                          int page, int k, size_t* bytes);

@@ -125,6 +125,7 @@ SIGNATURES = {
                                vp, i64, vp, vp]),
     "msa_paged_attn": (i32, [ctypes.POINTER(PagedKVArgs), vp, i32, i64, ctypes.c_int, vp, ctypes.c_int, vp,
                              ctypes.c_int, f32, vp, vp, vp, sz, vp]),
+    "msa_paged_inject_stall": (i32, [ctypes.c_int]),
     "msa_paged_attn_workspace_size": (i32, [i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                             ctypes.c_int, ctypes.c_int, ctypes.POINTER(sz)]),
     "msa_page_select": (i32, [ctypes.POINTER(PagedKVArgs), vp, i32, i64, ctypes.c_int, vp, ctypes.c_int, ctypes.c_int,

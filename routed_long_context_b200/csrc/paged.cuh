@@ -135,6 +135,7 @@ struct PagedAttnArgs {
     float* part_o;           // [CTA][2][rows][128], unnormalised
     float2* part_ml;         // [CTA][2][rows]: reference maximum (log2) and sum
     struct OpenSegment* open;  // [CTA]
+    int stall;               // testing, where not 0: the loader brings nothing from tile (stall - 1) * one round of its slots on
     int* err;
 };
 struct OpenSegment {         // the segment that starts in a CTA and ends in a later one

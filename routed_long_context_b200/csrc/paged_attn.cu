@@ -6,6 +6,7 @@
 // the bytes bound; more rows to the tcgen05 kernel, which the products bound. Both cut the keys of all sequences
 // evenly over the SMs; the softmaxes that end up in several pieces are joined here.
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 #include "mma.cuh"
@@ -61,6 +62,7 @@ __global__ void __launch_bounds__(32 * kCombineRows) paged_combine_kernel(const 
     if (a.lse && lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
+std::atomic<int> g_inject_stall{0};   // testing knob: make the next launches' waits time out
 constexpr int kSms = 148;
 
 struct AttnPlan {
@@ -128,6 +130,12 @@ extern "C" msa_status msa_paged_attn_workspace_size(int64_t n_tok, int n_seq, in
     return MSA_OK;
 }
 
+extern "C" msa_status msa_paged_inject_stall(int on) {
+    MSA_REQUIRE(on >= 0 && on <= 1000, "msa_paged_inject_stall: on must be between 0 and 1000");
+    g_inject_stall.store(on);
+    return MSA_OK;
+}
+
 extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_dtype dt, int64_t n_tok, int hq,
                                      const int64_t* tok_off, int max_new, const int32_t* sel, int k, float scale,
                                      void* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
@@ -155,6 +163,7 @@ extern "C" msa_status msa_paged_attn(const msa_paged_kv* kv, const void* q, msa_
     a.scale_log2e = scale * 1.4426950408889634f;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
+    a.stall = g_inject_stall.load();
     a.err = device_error_word();
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const AttnPlan p = attn_plan(n_tok, kv->n_seq, max_new, hq, kv->hkv, kv->max_pages, kv->page, sel ? k : 0);

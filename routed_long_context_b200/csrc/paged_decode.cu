@@ -337,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_decode_kernel(const __grid_
             // as many at a time as there are slots: two lanes waiting for the same slot, a phase apart, could not
             // tell by its parity whose turn it is
             for (int i0 = 0; i0 < count; i0 += kSlots) {
+                if (a.stall && done + i0 >= (a.stall - 1) * kSlots) break;
                 const int i = lane < kSlots ? i0 + lane : count;
                 TileInfo ti;
                 int row[2] = {0, 0}, rows[2] = {0, 0};

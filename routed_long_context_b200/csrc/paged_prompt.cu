@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                     scales(group + 1, id1, &sk1, &sv1);
                     for (int i = 0; i < 4 && 4 * group + i < p.n; ++i) {
                         const int n = cnt + 4 * group + i;
+                        if (a.stall && n >= (a.stall - 1) * kKStages) return false;
                         const int ks = n % kKStages, vs = n % kVStages;
                         const bool here = sub == i;
                         const bool first = here && id0 >= 0 && (c & ((1 << cps) - 1)) == 0;

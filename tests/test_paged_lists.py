@@ -1,4 +1,5 @@
-"""A page list without entries is refused: it is not the same as no list. No GPU is needed."""
+"""Paged attention over lists and page selection, what the host sees of them: a page list without entries is refused (it
+is not the same as no list), scratch is bounded. No GPU is needed."""
 import pytest
 import torch
 
@@ -34,3 +35,8 @@ def test_the_scratch_of_a_selection_holds_a_row_of_scores_a_token(n_tok, hkv, ma
     """8 bytes a page, and a maximum of 128 pages' bounds beside them."""
     least = n_tok * hkv * (8 * max_pages + 4 * -(-max_pages // 128))
     assert least <= m.page_select_workspace_size(n_tok, hkv, max_pages) <= least + 512
+
+
+def test_the_testing_hook_of_attention_refuses_what_is_no_setting():
+    assert api.lib.msa_paged_inject_stall(-1) == 1 and api.lib.msa_paged_inject_stall(1001) == 1
+    assert api.lib.msa_paged_inject_stall(0) == 0
