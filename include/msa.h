@@ -322,8 +322,8 @@ msa_status msa_sparse_attn_split_plan(int n_q, int T, int hq, int hkv, int max_m
  * Paged 8-bit key/value cache of the active context. msa_sparse_attn's local keys are one dense bf16
  * buffer with one length for all queries; contexts that grow long and apart (the Memory Interleave
  * loop of [P1] §组件 3 appends to them round by round) are kept here instead, in pages of 16, 32, 64 or
- * 128 tokens that the caller hands out, at a quarter to an eighth of the bytes. The pages define no
- * such cache; it is a library addition.
+ * 128 tokens that the caller hands out, a byte a value. The pages define no such cache; it is a library
+ * addition.
  *   pages:  e4m3 values, device [n_pages][2][hkv][page][d], K at [p][0] and V at [p][1];
  *   scales: device float [n_pages][2][hkv], powers of two from 2^-50 to 2^50: a stored value stands for
  *           e4m3 * scale, which is a bf16 number;

@@ -16,12 +16,13 @@
 // Two warpgroups take the two row blocks of 256 rows in turns (their products and exponentials overlap), or, of a
 // 128-row block, the even and the odd key tiles, joined at the end.
 // The products cost 8 * 128^3 flops a tile and row block, 1,024 cycles at the tensor peak; 128 * 128 exponentials take
-// as long on the special-function units: both bound it. Measured, a tile of both row blocks takes 4,200 cycles: a
-// warpgroup's exponentials and their reading and writing of TMEM 2,100, its products 1,300 (shared memory feeds Q K^T no
-// faster), and what passes between them. 2,000 tokens of 32 heads over 18,000: 604 to 621 us on two
-// GPUs, 897 to 922 TFLOP/s. Not faster: an issuer
-// of products for each warpgroup (764 us; in strict turns 655), steps of 64 keys with S ahead (738), part of the
-// exponentials by arithmetic (641 and more), waits by one lane of a warp (741).
+// as long on the special-function units: neither can take less, and neither bounds it. Measured, a tile of both row
+// blocks takes 4,200 cycles: a warpgroup's exponentials and their reading and writing of TMEM 2,100, its products 1,300
+// (shared memory feeds Q K^T no faster), and what passes between them, one after the other: S and P share a place in
+// TMEM, and two row blocks do not fill the gaps (1.6 instructions issued a cycle, the tensor pipe active for 48 %).
+// 2,000 tokens of 32 heads over 18,000: 593 to 621 us on four GPUs, 897 to 940 TFLOP/s. Not faster: an issuer of products
+// for each warpgroup (764 us; in strict turns 655), steps of 64 keys with S ahead (738), part of the exponentials by
+// arithmetic (641 and more), waits by one lane of a warp (741).
 // With few tiles to a block, what starts and ends a segment is most of it: 8 sequences of up to 32 tokens over up to
 // 8,096 take 42 us (before launches overlapped 45, and 57 where a segment's cost is left out of the blocks' shares).
 //
@@ -238,7 +239,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         sm.pre[tid + 1] = before + up;
         if (tid == 0) sm.pre[0] = 0;
     }
-    constexpr int kMinUnits = 1 + kSegWeight;              // no block with a segment's weight alone
+    // A block for each tile with its segment's weight, rounded up: of a call with few tiles a block's share may still be a
+    // weight alone, and the block finds no piece in it (a segment of 2 tiles: 10 units, two blocks of 5).
+    constexpr int kMinUnits = 1 + kSegWeight;
     const int n_cta = (int)min((long long)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
     if ((int)blockIdx.x >= n_cta) {
         if (tid == 0) a.open[blockIdx.x].n_more = 0;
