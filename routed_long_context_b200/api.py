@@ -44,14 +44,20 @@ def _stream(stream) -> int:
 def _on_stream(stream, call, *args, **kw):
     """`call` with `stream` as the current one, so that what it allocates or fills belongs to that stream: a block from
     another stream's memory may still be in use by what is queued there. Results stay reserved until the stream that was
-    current, where the caller takes them, is done with them too."""
-    if not hasattr(stream, "device"):            # anything else that has a cuda_stream
+    current, where the caller takes them, is done with them too. (Where nothing is allocated the call takes the stream's
+    handle alone: switching costs 10 us.)"""
+    if not hasattr(stream, "device_index"):      # anything else that has a cuda_stream
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
     was = torch.cuda.current_stream()
-    if stream.device != was.device:
-        raise ValueError(f"{call.__name__}: the stream is on {stream.device}, the current device is {was.device}")
-    with torch.cuda.stream(stream):
+    if stream == was:
+        return call(*args, **kw)
+    if stream.device_index != was.device_index:
+        raise ValueError(f"{call.__name__}: the stream is on device {stream.device_index}, the current one is {was.device_index}")
+    torch.cuda.set_stream(stream)
+    try:
         got = call(*args, **kw)
+    finally:
+        torch.cuda.set_stream(was)
     given = (*args, *kw.values())
     for t in got if isinstance(got, tuple) else (got,):
         if t is not None and t.is_cuda and not any(t is x for x in given):
@@ -59,19 +65,27 @@ def _on_stream(stream, call, *args, **kw):
     return got
 
 
-def _allocates(f):
-    """An entry point that allocates or fills memory: given a stream, it does so on that stream."""
-    names = f.__code__.co_varnames[:f.__code__.co_argcount]
-    at = len(names) - 1
-    name = names[at]
-    assert name in ("stream", "copy_stream")
+def _allocates(*outputs):
+    """An entry point that allocates or fills memory unless all of `outputs` are given (always, where none is named):
+    with a stream it does so on that stream."""
 
-    @functools.wraps(f)
-    def call(*args, **kw):
-        stream = kw.pop(name, None) if len(args) <= at else args[at]
-        return f(*args[:at], **kw) if stream is None else _on_stream(stream, f, *args[:at], **kw)
+    def wrap(f):
+        names = f.__code__.co_varnames[:f.__code__.co_argcount]
+        at, name = len(names) - 1, names[-1]
+        assert name in ("stream", "copy_stream")
+        places = [(names.index(o), o) for o in outputs]
 
-    return call
+        @functools.wraps(f)
+        def call(*args, **kw):
+            stream = args[at] if len(args) > at else kw.get(name)
+            if stream is None or places and all((args[i] if len(args) > i else kw.get(o)) is not None for i, o in places):
+                return f(*args, **kw)
+            kw.pop(name, None)
+            return _on_stream(stream, f, *args[:at], **kw)
+
+        return call
+
+    return wrap
 
 
 def _ws(nbytes: int, device) -> torch.Tensor:
@@ -96,7 +110,7 @@ def rope_table(max_pos: int, d: int, base: float = 1.0e6, device="cuda") -> torc
     return torch.from_numpy(host).to(device)
 
 
-@_allocates
+@_allocates()
 def chunk_doc_map(doc_chunk_off: torch.Tensor, n_chunks: int, stream=None) -> torch.Tensor:
     out = torch.empty(n_chunks, dtype=torch.int32, device=doc_chunk_off.device)
     check(lib.msa_chunk_doc_map(_ptr(doc_chunk_off), doc_chunk_off.numel() - 1, n_chunks, _ptr(out), _stream(stream)),
@@ -114,7 +128,7 @@ def msa_rope_doc(x: torch.Tensor, seg_tok_off: torch.Tensor, pos_offset: int, co
     return out
 
 
-@_allocates
+@_allocates("kvbar", "kr_index")
 def msa_pool_chunks(k, v, kr, doc_tok_off, doc_chunk_off, chunk_doc, chunk: int, cos_sin=None,
                     fuse_doc_rope: bool = True, out_dtype=None, normalize_router: bool = True, kvbar=None,
                     kr_index=None, stream=None):
@@ -138,7 +152,7 @@ def msa_pool_chunks(k, v, kr, doc_tok_off, doc_chunk_off, chunk_doc, chunk: int,
     return (kvbar if k is not None else None), (kr_index if kr is not None else None)
 
 
-@_allocates
+@_allocates("bank")
 def msa_pack_tokens(k, v, doc_tok_off, cos_sin, bank=None, stream=None):
     """Token-level memory bank of the fine stage: k, v [n_tok, hkv, d] -> bank [n_tok, 2, hkv, d] with each
     key rotated to its position inside its document (doc_tok_off [n_docs+1], device int64)."""
@@ -183,7 +197,7 @@ def route_set_impl(impl: int) -> None:
     check(lib.msa_route_set_impl(impl), "msa_route_set_impl")
 
 
-@_allocates
+@_allocates("doc_scores", "ws")
 def msa_route_scores(kr_index, chunk_doc, n_docs: int, qr, doc_scores=None, chunk_scores=None,
                      want_chunk_scores: bool = False, ws=None, stream=None):
     """Router scores: kr_index [C, H, d] (index form), qr [n_q, T, H, d] -> doc_scores [n_q, n_docs]
@@ -194,6 +208,8 @@ def msa_route_scores(kr_index, chunk_doc, n_docs: int, qr, doc_scores=None, chun
     if doc_scores is None:
         doc_scores = torch.empty((n_q, n_docs), dtype=torch.float32, device=dev)
     if want_chunk_scores and chunk_scores is None:
+        if stream is not None:
+            return _on_stream(stream, msa_route_scores, kr_index, chunk_doc, n_docs, qr, doc_scores, None, True, ws)
         chunk_scores = torch.empty((n_q, C), dtype=torch.float32, device=dev)
     if ws is None:
         ws = _ws(route_workspace_size(n_q, T, H, d, qr.dtype), dev)
@@ -218,7 +234,7 @@ def topk_workspace_size(n_q: int, n_docs: int, k: int) -> int:
     return n.value
 
 
-@_allocates
+@_allocates("idx", "score", "ws")
 def msa_topk_docs(doc_scores, k: int, idx=None, score=None, ws=None, stream=None):
     """-> (idx int32 [n_q, k], score float32 [n_q, k]) by descending score, ties to the lower index."""
     n_q, n_docs = doc_scores.shape
@@ -232,7 +248,7 @@ def msa_topk_docs(doc_scores, k: int, idx=None, score=None, ws=None, stream=None
     return idx, score
 
 
-@_allocates
+@_allocates("idx", "score")
 def msa_topk_docs_noalloc(doc_scores, k: int, idx=None, score=None, stream=None):
     """msa_topk_docs without a workspace: for callers that cannot allocate device memory at selection
     time. Scratch is the library's fixed device array; calls that overlap on the GPU race."""
@@ -245,7 +261,7 @@ def msa_topk_docs_noalloc(doc_scores, k: int, idx=None, score=None, stream=None)
     return idx, score
 
 
-@_allocates
+@_allocates("idx", "score")
 def msa_topk_merge(cand_score, cand_idx, shard_doc_off, k: int, idx=None, score=None, shard_stride=None,
                    stream=None):
     """Memory Parallel merge: cand_score float32 / cand_idx int32 lists [n_q, k_cand] of every shard (device,
@@ -269,7 +285,7 @@ def msa_topk_merge(cand_score, cand_idx, shard_doc_off, k: int, idx=None, score=
     return idx, score
 
 
-@_allocates
+@_allocates("dev_mem_kv")
 def msa_gather_kv(host_bank, doc_chunk_off_host, idx_host, max_mem: int, dev_mem_kv=None, device="cuda",
                   copy_stream=None):
     """Copy the selected docs' rows [*, 2, hkv, d] from the pinned host bank into
@@ -286,7 +302,7 @@ def msa_gather_kv(host_bank, doc_chunk_off_host, idx_host, max_mem: int, dev_mem
     return dev_mem_kv, mem_len
 
 
-@_allocates
+@_allocates("dev_mem_kv", "mem_len")
 def msa_gather_kv_device(host_bank, doc_chunk_off, idx, max_mem: int, dev_mem_kv=None, mem_len=None, stream=None):
     """Device-side fetch: idx [n_q, k] int32 and doc_chunk_off on the device; the pinned host bank is
     read by a kernel. Returns (dev_mem_kv [n_q, max_mem, 2, hkv, d], mem_len int32 [n_q] on the device)."""
@@ -303,7 +319,7 @@ def msa_gather_kv_device(host_bank, doc_chunk_off, idx, max_mem: int, dev_mem_kv
     return dev_mem_kv, mem_len
 
 
-@_allocates
+@_allocates("out")
 def msa_sparse_attn(q, mem_kv, mem_len, local_k, local_v, L: int, q_start: int, scale: float | None = None,
                     out=None, stream=None):
     """q [n_q, T, hq, d] (rotated), mem_kv [n_q, max_mem, 2, hkv, d], mem_len int32 [n_q] (device),
@@ -336,7 +352,7 @@ def sparse_attn_split_plan(n_q: int, T: int, hq: int, hkv: int, max_mem: int, L:
     return {"row_blocks": rb.value, "key_ranges": kr.value, "cluster": cl.value}
 
 
-@_allocates
+@_allocates("out", "ws")
 def msa_sparse_attn_split(q, mem_kv, mem_len, local_k, local_v, L: int, q_start: int, scale: float | None = None,
                           out=None, ws=None, lse=None, stream=None):
     """msa_sparse_attn for long memories (token-level fine stage): keys split into ranges that run as
@@ -418,8 +434,8 @@ class PagedKV:
         if len(shape) != 3 or shape[1] != heads or shape[2] != self.d:
             raise ValueError(f"{who}: expected [n_tok, {heads}, {self.d}], got {tuple(shape)}")
 
-    def _stream(self) -> int:
-        return torch._C._cuda_getCurrentRawStream(self._index)
+    def _stream(self, stream) -> int:
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
 
 
 def _addr(t) -> int | None:
@@ -432,8 +448,8 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
     """Append k, v [n_tok, hkv, d] to the cache, keys rotated to pos_offset + their place in the sequence; tok_off
     int64 [n_seq + 1] (device) splits the packed tokens, at most max_new a sequence; kv.seq_len already counts them.
     With q [n_tok, hq, d] the queries are rotated too: returns q_rot (allocated when not given), else None."""
-    if stream is not None:
-        return _on_stream(stream, msa_paged_append, kv, k, v, tok_off, max_new, cos_sin, pos_offset, q, q_rot)
+    if stream is not None and q is not None and q_rot is None:
+        return _on_stream(stream, msa_paged_append, kv, k, v, tok_off, max_new, cos_sin, pos_offset, q)
     kv._check("msa_paged_append", tok_off, k, kv.hkv, v, cos_sin, q, q_rot)
     shape, dtype = k.shape, k.dtype
     if v.dtype != dtype or v.shape != shape:
@@ -454,7 +470,7 @@ def msa_paged_append(kv: PagedKV, k, v, tok_off, max_new: int, cos_sin, pos_offs
     else:
         q_rot = None
     st = lib.msa_paged_append(kv._ref, k.data_ptr(), v.data_ptr(), _addr(q), _dt(k), n_tok, hq, tok_off.data_ptr(), max_new,
-                              pos_offset, cos_sin.data_ptr(), angles[0], _addr(q_rot), kv._stream())
+                              pos_offset, cos_sin.data_ptr(), angles[0], _addr(q_rot), kv._stream(stream))
     if st:
         check(st, "msa_paged_append")
     return q_rot
@@ -470,7 +486,7 @@ def page_select_workspace_size(n_tok: int, hkv: int, max_pages: int) -> int:
 def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int = 1, sel=None, ws=None, stream=None):
     """The k pages that each new token's query heads q [n_tok, hq, d] (rotated) should attend over, by the bounds of
     the pages' keys -> sel int32 [n_tok, hkv, k], ascending page indices of the sequence, -1 where there are fewer."""
-    if stream is not None:
+    if stream is not None and (sel is None or ws is None):
         return _on_stream(stream, msa_page_select, kv, q, tok_off, max_new, k, recent, sel, ws)
     n_tok, hq, _ = q.shape
     kv._check("msa_page_select", tok_off, q, hq, sel, ws)
@@ -481,7 +497,7 @@ def msa_page_select(kv: PagedKV, q, tok_off, max_new: int, k: int, recent: int =
     if ws is None:
         ws = kv._u8.new_empty(page_select_workspace_size(n_tok, kv.hkv, kv.max_pages) or 256)
     st = lib.msa_page_select(kv._ref, q.data_ptr(), _dt(q), n_tok, hq, tok_off.data_ptr(), max_new, k, recent, sel.data_ptr(),
-                             ws.data_ptr(), ws.nbytes, kv._stream())
+                             ws.data_ptr(), ws.nbytes, kv._stream(stream))
     if st:
         check(st, "msa_page_select")
     return sel
@@ -501,7 +517,7 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     """Attention of the new tokens q [n_tok, hq, d] (bf16, rotated) over the cache, causal within the call; with sel
     int32 [n_tok, hkv, k] over the listed pages only. Returns out [n_tok, hq, d], with lse float32 [n_tok, hq]
     (given or wanted) the pair (out, lse)."""
-    if stream is not None:
+    if stream is not None and (out is None or ws is None or (want_lse and lse is None)):
         return _on_stream(stream, msa_paged_attn, kv, q, tok_off, max_new, sel, scale, out, lse, want_lse, ws)
     n_tok, hq, d = q.shape
     kv._check("msa_paged_attn", tok_off, q, hq, out, lse, sel, ws)
@@ -524,14 +540,14 @@ def msa_paged_attn(kv: PagedKV, q, tok_off, max_new: int, sel=None, scale: float
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     st = lib.msa_paged_attn(kv._ref, q.data_ptr(), _dt(q), n_tok, hq, tok_off.data_ptr(), max_new, _addr(sel), k, scale,
-                            out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes, kv._stream())
+                            out.data_ptr(), _addr(lse), ws.data_ptr(), ws.nbytes, kv._stream(stream))
     if st:
         check(st, "msa_paged_attn")
     return out if lse is None else (out, lse)
 
 
 # ------------------------------------------------------------------------------------------------ backward
-@_allocates
+@_allocates("grads", "ws")
 def msa_sparse_attn_backward(q, mem_kv, mem_len, local_k, local_v, L: int, q_start: int, out, dout, lse,
                              scale: float | None = None, grads=None, ws=None, stream=None):
     """Gradients of the sparse attention (bf16 inputs): returns (dq [n_q, T, hq, d], dmem_kv [n_q, max_mem, 2,
@@ -559,7 +575,7 @@ def msa_sparse_attn_backward(q, mem_kv, mem_len, local_k, local_v, L: int, q_sta
     return grads
 
 
-@_allocates
+@_allocates("dkvbar")
 def msa_gather_kv_backward(dmem_kv, doc_chunk_off, idx, n_chunks: int, dkvbar=None, accumulate: bool = False,
                            stream=None):
     """Memory-row gradients [n_q, max_mem, 2, hkv, d] (fp32) into chunk-row gradients dkvbar [n_chunks, 2, hkv, d]
@@ -575,7 +591,7 @@ def msa_gather_kv_backward(dmem_kv, doc_chunk_off, idx, n_chunks: int, dkvbar=No
     return dkvbar
 
 
-@_allocates
+@_allocates()
 def msa_pool_chunks_backward(dkvbar, dkr_index, doc_tok_off, doc_chunk_off, chunk_doc, chunk: int, n_tok: int,
                              kr=None, cos_sin=None, fuse_doc_rope: bool = True, normalize_router: bool = True,
                              stream=None):
@@ -601,7 +617,7 @@ def msa_pool_chunks_backward(dkvbar, dkr_index, doc_tok_off, doc_chunk_off, chun
     return dk, dv, dkr
 
 
-@_allocates
+@_allocates()
 def msa_router_aux_loss(doc_scores, evidence, tau: float, stream=None):
     """(loss per query [n_q], dL/d doc_scores [n_q, D]) of the auxiliary router loss; evidence int32 [n_q, n_ev]
     (-1 padding). The gradient is that of the mean of the per-query losses."""
@@ -614,7 +630,7 @@ def msa_router_aux_loss(doc_scores, evidence, tau: float, stream=None):
     return loss, grad
 
 
-@_allocates
+@_allocates()
 def msa_route_backward(kr_index, doc_chunk_off, qr, d_doc_scores, stream=None):
     """(dqr [n_q, T, H, d], dkhat [C, H, d]) fp32: gradients of the router's document scores."""
     C, H, d = kr_index.shape

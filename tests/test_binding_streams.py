@@ -1,7 +1,5 @@
 """What the binding allocates for a call on a stream of the caller's own. No GPU is needed: streams and the library
 are stood in for, and the allocations are watched as torch makes them."""
-import contextlib
-
 import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
@@ -15,8 +13,7 @@ ALLOCATIONS = ("empty", "new_empty", "empty_like", "zeros", "new_zeros", "zeros_
 
 class Stream:
     def __init__(self, cuda_stream, index=0):
-        self.cuda_stream = cuda_stream
-        self.device = torch.device("cuda", index)
+        self.cuda_stream, self.device_index = cuda_stream, index
 
 
 class Watch(TorchDispatchMode):
@@ -40,13 +37,7 @@ class World:
         self.usual, self.side = Stream(7), Stream(9)
         self.current, self.kept, self.launched = self.usual, [], []
 
-        @contextlib.contextmanager
-        def on(stream):
-            was, self.current = self.current, stream
-            yield
-            self.current = was
-
-        monkeypatch.setattr(torch.cuda, "stream", on)
+        monkeypatch.setattr(torch.cuda, "set_stream", lambda s: setattr(self, "current", s))
         monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: self.current)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: self.current.cuda_stream)
@@ -184,3 +175,50 @@ def test_a_stream_may_be_given_by_place(monkeypatch, world):
     world.kept.clear()
     got = m.msa_topk_docs(sc, 1, idx=given[0], score=given[1], stream=world.side)
     assert got[0] is given[0] and not world.kept       # the caller's own tensors are the caller's
+
+
+def test_where_nothing_is_allocated_the_current_stream_stays(monkeypatch, world):
+    """The call goes to the stream by its handle alone, and nothing is kept for anyone."""
+    kv = _cache(monkeypatch)
+    for name in ("msa_paged_append", "msa_page_select", "msa_paged_attn", "msa_topk_docs", "msa_route_scores", "msa_sparse_attn"):
+        world.stub(monkeypatch, name)
+    monkeypatch.setattr(torch.cuda, "set_stream", None)
+    q, off = torch.zeros((2, 4, D), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int64)
+    k, cs, ws = torch.zeros((2, 2, D), dtype=torch.bfloat16), torch.zeros((4, D // 2, 2)), torch.zeros(1 << 20, dtype=torch.uint8)
+    sel, lse, sc = torch.zeros((2, 2, 3), dtype=torch.int32), torch.zeros((2, 4)), torch.zeros((1, 2))
+    idx, doc = torch.zeros((1, 1), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    qr, q4, loc = torch.zeros((1, 3, 2, D)), q[None], torch.zeros((1, 2, 2, D), dtype=torch.bfloat16)
+    mem = torch.zeros((1, 2, 2, 2, D), dtype=torch.bfloat16)
+    s = {"stream": world.side}
+    with Watch(world) as w:
+        m.msa_paged_append(kv, k, k, off, 2, cs, **s)
+        m.msa_paged_append(kv, k, k, off, 2, cs, q=q, q_rot=q, **s)
+        m.msa_page_select(kv, q, off, 2, 3, sel=sel, ws=ws, **s)
+        m.msa_paged_attn(kv, q, off, 2, out=q, ws=ws, **s)
+        m.msa_paged_attn(kv, q, off, 2, out=q, lse=lse, want_lse=True, ws=ws, **s)
+        m.msa_topk_docs(sc, 1, idx, sc[:, :1], ws, world.side)
+        m.msa_route_scores(qr[0], doc, 2, qr, doc_scores=sc, ws=ws, **s)
+        m.msa_sparse_attn(q4, mem, doc, loc, loc, 2, 0, out=q4, **s)
+    assert not w.seen and not world.kept
+    assert [a[-1] for _, a in world.launched] == [world.side.cuda_stream] * 8
+
+
+def test_the_current_stream_given_by_name_is_no_switch(monkeypatch, world):
+    kv = _cache(monkeypatch)
+    monkeypatch.setattr(torch.cuda, "set_stream", None)
+    for name, call in _paged_calls(kv).values():
+        world.stub(monkeypatch, name)
+        call(stream=world.usual)
+    assert not world.kept and all(a[-1] == world.usual.cuda_stream for _, a in world.launched)
+
+
+def test_chunk_scores_that_are_wanted_belong_to_the_stream_too(monkeypatch, world):
+    world.stub(monkeypatch, "msa_route_scores")
+    qr, sc = torch.zeros((1, 3, 2, D)), torch.zeros((1, 2))
+    args = qr[0], torch.zeros(2, dtype=torch.int32), 2, qr
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    with Watch(world) as w:
+        got = m.msa_route_scores(*args, doc_scores=sc, want_chunk_scores=True, ws=ws, stream=world.side)
+    assert _made(w) == [world.side] and got[0] is sc
+    assert world.kept_for(got[1]) == [world.usual] and not world.kept_for(sc)
+    assert world.launched[0][1][-1] == world.side.cuda_stream and world.current is world.usual
