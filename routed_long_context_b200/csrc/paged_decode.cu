@@ -22,8 +22,8 @@
 // 128-byte swizzle into a ring of 20 tiles of 8 KB (44 KB cover the latency of memory); another lays out the queries
 // of the segment after the one in work; 10 warps take the tiles in turns.
 //
-// Measured, one token of 32 heads over 500,001: 198 us where the same context is read again and again, 213 where it
-// changes from call to call; 156 are its bytes at the copy rate. A block's tiles pass at 21 bytes a cycle and SM: no pipe
+// Measured, one token of 32 heads over 500,001: 198 us where the same context is read again and again, 213 to 217
+// where it changes from call to call; 156 are its bytes at the copy rate. A block's tiles pass at 21 bytes a cycle and SM: no pipe
 // is full (DRAM 62 %, tensor 31 %, 2.1 instructions issued a cycle); 10 warps with some 500 instructions a tile, in chains
 // of shared memory, products and exponentials, set the pace. Start and merge take 10 us. 32 tokens over up to 16,384 each 122 us (89). Before:
 // fp32 arithmetic 94 ms; fp16 and bf16 mma.sync with converted operands and 16-key tiles 246 us; e4m3 operands with each
